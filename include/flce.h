@@ -260,6 +260,37 @@ int flce_ce_backward(const void* logits, int dtype, const int64_t* labels, const
                      flce_stream_t stream);
 
 /*
+ * Layer norm over the last dimension: the final norm whose output the head
+ * reads (the pages' losses take the final hidden states as given).
+ *   y[n] = (x[n] - mean_n) * rstd_n * weight + bias,
+ *   mean_n = sum x[n] / H, rstd_n = 1 / sqrt(sum (x[n] - mean_n)^2 / H + eps)
+ *   x, y, dy, dx   [N, H] rows ldx / ldy / lddy / lddx elements apart (ld >= H),
+ *                  one dtype (0 = BF16, 1 = FP32); any H >= 1, any alignment of
+ *                  whole elements (16-byte aligned rows are loaded fastest).
+ *   weight, bias   [H] in w_dtype; either may be NULL (ones, zeros).
+ *   eps            finite, >= 0.
+ *   mean, rstd     FP32 [N], written by the forward, read by the backward.
+ *   dx, dweight, dbias (backward) each may be NULL: not computed.  dweight and
+ *                  dbias are [H] in w_dtype, overwritten, summed over the rows
+ *                  in FP32 in a fixed order (zeros when N = 0).
+ *   workspace      >= flce_layer_norm_workspace_size(N, H) bytes, 16-byte
+ *                  aligned; only needed with dweight or dbias.
+ * All arithmetic between the inputs and the one rounding of each output is
+ * FP32.  Outputs may not overlap inputs.
+ */
+size_t flce_layer_norm_workspace_size(int64_t n_tokens, int64_t hidden_size);
+int flce_layer_norm_forward(const void* x, int dtype, int64_t n_tokens, int64_t hidden_size,
+                            int64_t ldx, const void* weight, const void* bias, int w_dtype,
+                            float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                            flce_stream_t stream);
+int flce_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int dtype,
+                             int64_t n_tokens, int64_t hidden_size, int64_t ldx,
+                             const void* weight, int w_dtype, const float* mean,
+                             const float* rstd, void* dx, int64_t lddx, void* dweight,
+                             void* dbias, void* workspace, size_t ws_bytes,
+                             flce_stream_t stream);
+
+/*
  * Forward that allocates nothing and takes no workspace (the pages have no
  * counterpart; it exists for callers that cannot supply scratch memory, such
  * as a plugin inside a framework whose allocator owns the whole device, or a

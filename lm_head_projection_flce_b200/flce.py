@@ -9,6 +9,7 @@ Entry points mirror include/flce.h:
   forward(hidden, weight, labels, ...)            -> (loss, lse)
   backward(hidden, weight, labels, lse, grad, ...) -> (dhidden, dweight)
   fused_linear_cross_entropy(...)                  autograd-aware convenience
+  layer_norm(...)                                  the final norm, autograd-aware
 with the options of the NeMo-AutoModel loss pages
 ("nemo_automodel.components.loss.linear_ce", FusedLinearCrossEntropy:
 ignore_index=-100, logit_softcapping=0, reduction='sum', num_label_tokens;
@@ -17,6 +18,7 @@ FP32 head rounded to BF16).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -76,6 +78,13 @@ SIGNATURES = {
                                  _c_int, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr]),
     "flce_ce_backward": (_c_int, [_c_ptr, _c_int, _c_ptr, _c_ptr, _c_i64, _c_i64, _c_i64, _c_i64,
                                   _c_int, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size, _c_ptr]),
+    "flce_layer_norm_workspace_size": (_c_size, [_c_i64, _c_i64]),
+    "flce_layer_norm_forward": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr,
+                                         _c_int, ctypes.c_float, _c_ptr, _c_i64, _c_ptr, _c_ptr,
+                                         _c_ptr]),
+    "flce_layer_norm_backward": (_c_int, [_c_ptr, _c_i64, _c_ptr, _c_int, _c_i64, _c_i64, _c_i64,
+                                          _c_ptr, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_ptr,
+                                          _c_ptr, _c_ptr, _c_size, _c_ptr]),
     "flce_launch_count": (ctypes.c_ulonglong, []),
     "flce_profile_start": (_c_int, []),
     "flce_profile_stop": (_c_int, [_c_ptr, _c_int, ctypes.POINTER(_c_int)]),
@@ -120,6 +129,18 @@ def _check(where: str, status: int) -> None:
 def _stream_handle(device: torch.device, stream=None):
     s = torch.cuda.current_stream(device) if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on(device: torch.device, stream=None):
+    """Context in which `device` and `stream` (None: the device's current stream)
+    are current, so that what is allocated inside belongs to that stream."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("stream must belong to the tensors' device")
+        return torch.cuda.stream(stream)
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _ptr(t: torch.Tensor | None):
@@ -337,8 +358,13 @@ class _FusedLinearCE(torch.autograd.Function):
 def fused_linear_cross_entropy(hidden, weight, labels, *, ignore_index: int = -100,
                                softcap: float = 0.0, unpadded_vocab: int | None = None,
                                reduction: str = "sum", num_label_tokens: int | None = None,
-                               fused_head_cast: bool = False):
+                               fused_head_cast: bool = False, norm_weight=None, norm_bias=None,
+                               norm_eps: float = 1e-5):
     """Autograd-aware loss: gradients flow to ``hidden`` and ``weight``.
+
+    With ``norm_weight`` and / or ``norm_bias`` ([H]), ``hidden`` is what enters
+    the final layer norm: it is normalised by ``layer_norm(hidden, norm_weight,
+    norm_bias, eps=norm_eps)`` first, and gradients flow to those two as well.
 
     With an FP32 head the forward's workspace (which holds the head's BF16
     copy, V x H x 2 bytes, and the backward's buffers) is kept until the
@@ -347,6 +373,8 @@ def fused_linear_cross_entropy(hidden, weight, labels, *, ignore_index: int = -1
     inside the GEMMs instead: no copy exists and nothing is kept (less memory,
     slower GEMMs, the same results).
     """
+    if norm_weight is not None or norm_bias is not None:
+        hidden = layer_norm(hidden, norm_weight, norm_bias, eps=norm_eps)
     return _FusedLinearCE.apply(hidden, weight, labels, ignore_index, softcap, unpadded_vocab,
                                 reduction, num_label_tokens, fused_head_cast)
 
@@ -545,3 +573,155 @@ def ce_backward(logits, labels, lse, grad_loss, *, mask=None, ignore_index: int 
                               _stream_handle(dev, stream))
     _check("flce_ce_backward", st)
     return out.reshape(logits.shape)
+
+
+# ---------------------------------------------------------------- layer norm
+
+def _rows(t, h: int, name: str) -> tuple[torch.Tensor, int]:
+    """`t` [..., h] as rows [N, h] of unit stride, and their distance in elements."""
+    rows = t.reshape(-1, h)
+    if h > 1 and rows.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    if rows.shape[0] <= 1:
+        return rows, h
+    if rows.stride(0) < h:
+        raise ValueError(f"{name} rows must not overlap")
+    return rows, rows.stride(0)
+
+
+def _cuda_tensor(t, dtypes, dev, name: str) -> None:
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {tuple(dtypes)}")
+    if t.device.type != "cuda" or (dev is not None and t.device != dev):
+        raise ValueError("tensors must be on one CUDA device")
+
+
+def _norm_params(weight, bias, h: int, dev, param_dtype=None) -> torch.dtype:
+    given = [p for p in (weight, bias) if p is not None]
+    for p in given:
+        _cuda_tensor(p, W_DTYPES, dev, "weight and bias")
+        if p.shape != (h,) or not p.is_contiguous():
+            raise ValueError("weight and bias must be contiguous [hidden] tensors")
+        if p.dtype != given[0].dtype:
+            raise TypeError("weight and bias must have one dtype")
+    dtype = given[0].dtype if given else (param_dtype or torch.float32)
+    if param_dtype is not None and param_dtype != dtype:
+        raise TypeError("param_dtype differs from the weight's dtype")
+    if dtype not in W_DTYPES:
+        raise TypeError("weight and bias must be bf16 or fp32")
+    return dtype
+
+
+def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5,
+                       y: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                       rstd: torch.Tensor | None = None, stream=None):
+    """Layer norm over the last dimension (flce_layer_norm_forward).
+
+    ``x`` [..., H] bf16 or fp32 (rows contiguous, any row stride); ``weight`` and
+    ``bias`` [H] bf16 or fp32, either may be None.  Returns ``(y, mean, rstd)``:
+    y in x's dtype and shape, the row statistics FP32 [N] for the backward.
+    """
+    lib = load_library()
+    _cuda_tensor(x, W_DTYPES, None, "x")
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x must be [..., hidden] with hidden >= 1")
+    dev, h = x.device, x.shape[-1]
+    w_dtype = _norm_params(weight, bias, h, dev)
+    rows, ldx = _rows(x, h, "x")
+    n = rows.shape[0]
+    with _on(dev, stream):
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else y
+        if y.shape != x.shape or y.dtype != x.dtype or y.device != dev:
+            raise ValueError("y must have x's shape, dtype and device")
+        out, ldy = _rows(y, h, "y")
+        if out.data_ptr() != y.data_ptr():
+            raise ValueError("y's rows must have one stride")
+        mean = (torch.empty(n, dtype=torch.float32, device=dev) if mean is None
+                else _buffer(mean, n, torch.float32, dev, "mean"))
+        rstd = (torch.empty(n, dtype=torch.float32, device=dev) if rstd is None
+                else _buffer(rstd, n, torch.float32, dev, "rstd"))
+        st = lib.flce_layer_norm_forward(_ptr(rows), W_DTYPES[x.dtype], n, h, ldx, _ptr(weight),
+                                         _ptr(bias), W_DTYPES[w_dtype], float(eps), _ptr(out), ldy,
+                                         _ptr(mean), _ptr(rstd), _stream_handle(dev, stream))
+    _check("flce_layer_norm_forward", st)
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, *, want=("dx", "dweight", "dbias"),
+                        param_dtype: torch.dtype | None = None, dx: torch.Tensor | None = None,
+                        dweight: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """Gradients ``(dx, dweight, dbias)`` of layer_norm_forward; None for what is
+    not in ``want``.  ``dx`` has x's dtype, the other two the weight's
+    (``param_dtype`` where there is no weight; FP32 by default)."""
+    lib = load_library()
+    _cuda_tensor(x, W_DTYPES, None, "x")
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x must be [..., hidden] with hidden >= 1")
+    unknown = set(want) - {"dx", "dweight", "dbias"}
+    if unknown:
+        raise ValueError(f"unknown gradients {sorted(unknown)}")
+    dev, h = x.device, x.shape[-1]
+    _cuda_tensor(dy, (x.dtype,), dev, "dy")
+    if dy.shape != x.shape:
+        raise ValueError("dy must have x's shape")
+    w_dtype = _norm_params(weight, None, h, dev, param_dtype)
+    rows, ldx = _rows(x, h, "x")
+    grads, lddy = _rows(dy, h, "dy")
+    n = rows.shape[0]
+    mean = _buffer(mean, n, torch.float32, dev, "mean")
+    rstd = _buffer(rstd, n, torch.float32, dev, "rstd")
+    with _on(dev, stream):
+        lddx = h
+        out = None
+        if "dx" in want:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
+            if dx.shape != x.shape or dx.dtype != x.dtype or dx.device != dev:
+                raise ValueError("dx must have x's shape, dtype and device")
+            out, lddx = _rows(dx, h, "dx")
+            if out.data_ptr() != dx.data_ptr():
+                raise ValueError("dx's rows must have one stride")
+        else:
+            dx = None
+        params = []
+        for name, given in (("dweight", dweight), ("dbias", dbias)):
+            if name not in want:
+                params.append(None)
+            else:
+                params.append(torch.empty(h, dtype=w_dtype, device=dev) if given is None
+                              else _buffer(given, h, w_dtype, dev, name))
+        ws, ws_bytes = None, 0
+        if params[0] is not None or params[1] is not None:
+            ws, ws_bytes = _workspace(workspace, int(lib.flce_layer_norm_workspace_size(n, h)), dev)
+        st = lib.flce_layer_norm_backward(_ptr(grads), lddy, _ptr(rows), W_DTYPES[x.dtype], n, h,
+                                          ldx, _ptr(weight), W_DTYPES[w_dtype], _ptr(mean),
+                                          _ptr(rstd), _ptr(out), lddx, _ptr(params[0]),
+                                          _ptr(params[1]), _ptr(ws), ws_bytes,
+                                          _stream_handle(dev, stream))
+    _check("flce_layer_norm_backward", st)
+    return dx, params[0], params[1]
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = layer_norm_forward(x, weight, bias, eps=eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.param_dtype = bias.dtype if bias is not None else None
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        want = [g for g, need in zip(("dx", "dweight", "dbias"), ctx.needs_input_grad) if need]
+        # a gradient that autograd broadcast (a sum's) has rows of stride 0
+        dx, dw, db = layer_norm_backward(dy.contiguous(), x, mean, rstd, weight, want=want,
+                                         param_dtype=ctx.param_dtype)
+        return dx, dw, db, None
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
+    """Autograd-aware layer norm over the last dimension: ``(x - mean) * rstd *
+    weight + bias``; gradients flow to ``x``, ``weight`` and ``bias``."""
+    return _LayerNorm.apply(x, weight, bias, eps)
