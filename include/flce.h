@@ -291,6 +291,45 @@ int flce_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int dt
                              flce_stream_t stream);
 
 /*
+ * The head in microscaled 4-bit floating point (MXFP4), for serving and for
+ * evaluating a quantised head: quantisation, its inverse, and the product
+ * with the hidden states.
+ *   Every 32 consecutive elements of a row share a power of two 2^e,
+ *   e = floor(log2(max |x|)) - 2 (at least -127), and each element is the
+ *   nearest E2M1 number (0, .5, 1, 1.5, 2, 3, 4, 6; ties to the even code;
+ *   saturating at 6) times 2^e, with x's sign.  A block that holds an Inf or a
+ *   NaN becomes NaN as a whole.
+ *   codes   flce_mxfp4_codes_size(rows, cols) bytes: row r at r * ceil(cols/32)
+ *           * 16, element 2i in the low half of byte i (a partly filled last
+ *           block is padded with zeros).
+ *   scales  flce_mxfp4_scales_size(rows, cols) bytes: e + 127 (255 = NaN) per
+ *           block, in tiles of 128 rows x 4 blocks of 512 bytes (tiles of one
+ *           128 rows follow one another along the columns); row r, block k of
+ *           a tile at (r % 32) * 16 + (r / 32) * 4 + k.
+ *   x / out [rows, cols], rows ld elements apart, BF16 (dtype 0) or FP32 (1);
+ *           any alignment of whole elements.  Both types hold the dequantised
+ *           numbers exactly.  codes and scales must be 16-byte aligned.
+ * flce_mxfp4_logits: logits[n, v] = cap(sum_h Q(hidden)[n, h] * W[v, h]) for
+ *   v < V = unpadded_vocab (<= 0: Vp), FP32 accumulation, cap(z) =
+ *   softcap * tanh(z / softcap) (0: no cap); hidden [N, H] rows ldh apart is
+ *   quantised into the workspace (flce_mxfp4_logits_workspace_size(N, H) bytes,
+ *   16-byte aligned); logits [N, V] rows ldo apart in out_dtype.  One token
+ *   and many use the same kernel.
+ */
+size_t flce_mxfp4_codes_size(int64_t rows, int64_t cols);
+size_t flce_mxfp4_scales_size(int64_t rows, int64_t cols);
+int flce_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                        void* codes, void* scales, flce_stream_t stream);
+int flce_mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, int64_t cols,
+                          void* out, int dtype, int64_t ld, flce_stream_t stream);
+size_t flce_mxfp4_logits_workspace_size(int64_t n_tokens, int64_t hidden_size);
+int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n_tokens, int64_t hidden_size,
+                      int64_t ldh, const void* w_codes, const void* w_scales,
+                      int64_t padded_vocab, int64_t unpadded_vocab, float softcap, void* logits,
+                      int out_dtype, int64_t ldo, void* workspace, size_t ws_bytes,
+                      flce_stream_t stream);
+
+/*
  * Forward that allocates nothing and takes no workspace (the pages have no
  * counterpart; it exists for callers that cannot supply scratch memory, such
  * as a plugin inside a framework whose allocator owns the whole device, or a

@@ -27,7 +27,7 @@
 // Cross entropy on given logits (chunked_ce page) is at the end of this file,
 // its row kernels in chunked_ce.cuh, and the forward without allocation.  The
 // operators around the head have their kernels and entry points in files of
-// their own, included last: layer_norm.cuh.
+// their own, included last: layer_norm.cuh, mxfp4.cuh and mxfp4_gemm.cuh.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -357,13 +357,14 @@ static int device_info(DeviceInfo** out) {
 enum KernelFamily {
   KF_CAST = 0, KF_ZERO, KF_GEMM_FWD, KF_MERGE, KF_FINAL, KF_BWD_PREP, KF_GEMM_GRAD, KF_GEMM_DW,
   KF_GEMM_DH, KF_SELFTEST_GEMM, KF_SELFTEST_WAIT, KF_GEMM_BWD, KF_CE_FWD, KF_CE_BWD, KF_LN_FWD,
-  KF_LN_BWD, KF_LN_REDUCE, KF_COUNT
+  KF_LN_BWD, KF_LN_REDUCE, KF_MX_QUANT, KF_MX_DEQUANT, KF_MX_GEMM, KF_COUNT
 };
 static const char* const kFamilyNames[KF_COUNT] = {
     "cast_f32_bf16", "zero_rows",     "gemm_fwd_lse", "lse_merge",
     "loss_finalize", "bwd_prep",      "gemm_bwd_grad", "gemm_bwd_dw",
     "gemm_bwd_dh",   "selftest_gemm", "selftest_wait", "gemm_bwd_fused",
-    "ce_logits_fwd", "ce_logits_bwd", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_reduce"};
+    "ce_logits_fwd", "ce_logits_bwd", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_reduce",
+    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm"};
 
 struct ProfRecord {
   int family;
@@ -1500,3 +1501,5 @@ extern "C" int flce_ce_backward(const void* logits, int dtype, const int64_t* la
 // ===================================== operators around the head
 
 #include "layer_norm.cuh"
+#include "mxfp4.cuh"
+#include "mxfp4_gemm.cuh"

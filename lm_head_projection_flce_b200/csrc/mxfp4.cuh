@@ -1,0 +1,292 @@
+// mxfp4.cuh - microscaled 4-bit floating point (MXFP4): every 32 consecutive
+// elements of a row share a power of two, and each element is an E2M1 number
+// (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) times it.
+//
+//   amax  = max |x| of the block
+//   e     = floor(log2 amax) - 2, at least -127     (E2M1's largest exponent is 2)
+//   code  = E2M1 nearest to x / 2^e, ties to the even code, saturating at 6
+//   scale = e + 127 (E8M0); 255 = NaN when the block holds an Inf or a NaN
+//
+// Dividing by a power of two is exact and the nearest code is unique, so the
+// codes are a function of the input alone, whatever computes them.
+//
+// Layout in memory.  Codes: row r at r * pitch, pitch = ceil(cols / 32) * 16
+// bytes, element 2i in the low half of byte i; a partly filled last block is
+// padded with zeros.  Scales: tiles of 128 rows x 4 blocks of columns, 512
+// bytes each, the tiles of 128 rows one after the other along the columns;
+// inside a tile the scale of row r, block k sits at (r % 32) * 16 +
+// (r / 32) * 4 + k.  That is the order in which the tensor core wants them in
+// tensor memory (32 lanes x 16 bytes), so a tile goes from HBM to shared memory
+// and on to tensor memory as one block of bytes, with no reshuffling.
+// Scales of blocks behind a row's last one (up to the multiple of 4) are 127;
+// rows behind the last one are left as they were, nothing reads their products.
+//
+// Both kernels are bound by HBM (quantising BF16 reads 2 bytes and writes
+// 17/32 of one per element).  Four threads share a block: each converts 8
+// elements (16 bytes of BF16, 32 of FP32), the block's maximum takes two
+// shuffles, and 4 bytes of codes per thread make whole sectors per warp.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp4.h>
+
+#include "epilogues.cuh"
+#include "layer_norm.cuh"  // LnIo: typed vector loads and stores
+
+namespace flce {
+
+constexpr int kMxBlock = 32;          // elements per scale
+constexpr int kMxTileRows = 128;      // rows of a scale tile
+constexpr int kMxTileBlocks = 4;      // column blocks of a scale tile
+constexpr int kMxTileBytes = kMxTileRows * kMxTileBlocks;
+constexpr int kMxThreads = 256;
+constexpr int kMxUnroll = 4;          // vectors of 8 elements in flight per thread
+
+__host__ __device__ __forceinline__ int64_t mx_blocks(int64_t cols) {
+  return (cols + kMxBlock - 1) / kMxBlock;
+}
+__host__ __device__ __forceinline__ int64_t mx_ktiles(int64_t cols) {
+  return (mx_blocks(cols) + kMxTileBlocks - 1) / kMxTileBlocks;
+}
+__host__ __device__ __forceinline__ int64_t mx_pitch(int64_t cols) { return mx_blocks(cols) * 16; }
+
+// Byte offset of the 4-byte word that holds row r's scales of column tile kt.
+__device__ __forceinline__ int64_t mx_scale_word(int64_t r, int64_t kt, int64_t ktiles) {
+  return ((r / kMxTileRows) * ktiles + kt) * kMxTileBytes + (r % 32) * 16 +
+         ((r % kMxTileRows) / 32) * 4;
+}
+
+// Four E2M1 pairs of 8 scaled values, the first value in the lowest bits.
+__device__ __forceinline__ uint32_t mx_pack8(const float (&x)[8]) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(x[2 * i], x[2 * i + 1]),
+                                                        __NV_E2M1, cudaRoundNearest))
+         << (8 * i);
+  return w;
+}
+
+struct MxQuantArgs {
+  const void* x;
+  int64_t rows, cols, ld;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t segs;  // pieces a row is cut into, a warp each (a multiple of 8 blocks per piece)
+};
+
+// A warp takes a piece of a row: 8 blocks (32 vectors of 8 elements) per step.
+// kVec: rows start on 16 bytes and hold whole vectors of 8.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const MxQuantArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = int64_t(gridDim.x) * (kMxThreads / 32);
+  const int64_t blocks = mx_blocks(a.cols), ktiles = mx_ktiles(a.cols), pitch = mx_pitch(a.cols);
+  const int64_t steps = (ktiles * kMxTileBlocks + 7) / 8;  // of 8 blocks each
+  const int64_t per = (steps + a.segs - 1) / a.segs;
+  for (int64_t u = int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5);
+       u < a.rows * a.segs; u += warps) {
+    const int64_t r = u / a.segs, s0 = (u - r * a.segs) * per, s1 = min(steps, s0 + per);
+    const T* row = static_cast<const T*>(a.x) + r * a.ld;
+    for (int64_t s = s0; s < s1; s += kMxUnroll) {
+      float v[kMxUnroll][8];
+#pragma unroll
+      for (int i = 0; i < kMxUnroll; ++i) {
+        const int64_t c = ((s + i) * 32 + lane) * 8;
+        if (kVec && s + i < s1 && c < a.cols) {
+          LnIo<T, 8>::load(row + c, v[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float one[1] = {0.0f};
+            if (!kVec && s + i < s1 && c + j < a.cols) LnIo<T, 1>::load(row + c + j, one);
+            v[i][j] = one[0];
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kMxUnroll; ++i) {
+        if (s + i >= s1) break;  // the same for the whole warp
+        // The largest magnitude as bits: NaN and Inf order above every number.
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7fffffffu);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int ex = static_cast<int>(m >> 23);
+        const int sc = ex == 255 ? 255 : max(ex - 2, 0);
+        const float inv = __uint_as_float(static_cast<uint32_t>(ex == 255 ? 127 : 254 - sc) << 23);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+        const uint32_t w = mx_pack8(v[i]);
+        const int64_t vec = (s + i) * 32 + lane, b = vec >> 2;
+        if (b < blocks) *reinterpret_cast<uint32_t*>(a.codes + r * pitch + vec * 4) = w;
+        // Four blocks' scales as one word, written by the first of 16 lanes.
+        uint32_t word = (b < blocks ? static_cast<uint32_t>(sc) : 127u) << (8 * ((lane >> 2) & 3));
+        word |= __shfl_xor_sync(0xffffffffu, word, 4);
+        word |= __shfl_xor_sync(0xffffffffu, word, 8);
+        if ((lane & 15) == 0 && (b >> 2) < ktiles)
+          *reinterpret_cast<uint32_t*>(a.scales + mx_scale_word(r, b >> 2, ktiles)) = word;
+      }
+    }
+  }
+}
+
+struct MxDequantArgs {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t rows, cols, ld;
+  void* out;
+  int64_t segs;
+};
+
+// 2^(sc - 127); 255 is NaN.  (2^-127 is subnormal in FP32.)
+__device__ __forceinline__ float mx_scale(uint32_t sc) {
+  return sc == 255u ? __uint_as_float(0x7fc00000u)
+                    : __uint_as_float(sc == 0u ? 0x00400000u : sc << 23);
+}
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const MxDequantArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = int64_t(gridDim.x) * (kMxThreads / 32);
+  const int64_t ktiles = mx_ktiles(a.cols), pitch = mx_pitch(a.cols);
+  const int64_t steps = (mx_blocks(a.cols) + 7) / 8;
+  const int64_t per = (steps + a.segs - 1) / a.segs;
+  for (int64_t u = int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5);
+       u < a.rows * a.segs; u += warps) {
+    const int64_t r = u / a.segs, s0 = (u - r * a.segs) * per, s1 = min(steps, s0 + per);
+    T* row = static_cast<T*>(a.out) + r * a.ld;
+    for (int64_t s = s0; s < s1; s += kMxUnroll) {
+      uint32_t w[kMxUnroll], sc[kMxUnroll];
+#pragma unroll
+      for (int i = 0; i < kMxUnroll; ++i) {
+        const int64_t vec = (s + i) * 32 + lane;
+        w[i] = sc[i] = 0;
+        if (s + i < s1 && vec * 8 < a.cols) {
+          w[i] = *reinterpret_cast<const uint32_t*>(a.codes + r * pitch + vec * 4);
+          sc[i] = a.scales[mx_scale_word(r, vec >> 4, ktiles) + ((vec >> 2) & 3)];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kMxUnroll; ++i) {
+        const int64_t c = ((s + i) * 32 + lane) * 8;
+        if (s + i >= s1 || c >= a.cols) continue;
+        const float k = mx_scale(sc[i]);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(
+              static_cast<__nv_fp4x2_storage_t>((w[i] >> (8 * j)) & 0xffu), __NV_E2M1);
+          const float2 f = __half22float2(__half2(h));
+          v[2 * j] = f.x * k;
+          v[2 * j + 1] = f.y * k;
+        }
+        if (kVec) {
+          LnIo<T, 8>::store(row + c, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float one[1] = {v[j]};
+            if (c + j < a.cols) LnIo<T, 1>::store(row + c + j, one);
+          }
+        }
+      }
+    }
+  }
+}
+
+static bool mx_sizes_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols > 0 && rows <= kMaxDim && cols <= kMaxDim &&
+         cols <= (int64_t(1) << 40) / std::max<int64_t>(rows, 1);
+}
+static size_t mx_scales_bytes(int64_t rows, int64_t cols) {
+  return size_t(cdiv(rows, kMxTileRows)) * size_t(mx_ktiles(cols)) * kMxTileBytes;
+}
+// Pieces per row (a warp each) and blocks: enough warps for the GPU when rows are few.
+static int64_t mx_segments(int64_t rows, int64_t cols, int sms, int64_t* grid) {
+  const int64_t steps = cdiv(mx_ktiles(cols) * kMxTileBlocks, 8);
+  const int64_t want = cdiv(int64_t(sms) * 32, std::max<int64_t>(rows, 1));
+  const int64_t segs = std::max<int64_t>(1, std::min(steps, want));
+  *grid = std::max<int64_t>(1, std::min<int64_t>(cdiv(rows * segs, kMxThreads / 32), int64_t(sms) * 16));
+  return segs;
+}
+static bool mx_vec_ok(const void* p, int64_t ld, int64_t cols, int esz) {
+  return aligned(p, 16) && (ld * esz) % 16 == 0 && cols % 8 == 0;
+}
+
+static int mx_quantize(const DeviceInfo& dev, const void* x, int dtype, int64_t rows, int64_t cols,
+                       int64_t ld, uint8_t* codes, uint8_t* scales, cudaStream_t cs) {
+  const int esz = dtype == FLCE_F32 ? 4 : 2;
+  int64_t grid = 0;
+  MxQuantArgs a{x, rows, cols, rows > 1 ? ld : cols, codes, scales, 0};
+  a.segs = mx_segments(rows, cols, dev.num_sms, &grid);
+  const bool vec = mx_vec_ok(x, rows > 1 ? ld : 0, cols, esz);
+  LaunchScope scope(KF_MX_QUANT, 0.0, double(rows) * double(cols) * (esz + 17.0 / 32.0), cs);
+  if (dtype == FLCE_BF16 && vec)
+    mx_quantize_kernel<__nv_bfloat16, true><<<unsigned(grid), kMxThreads, 0, cs>>>(a);
+  else if (dtype == FLCE_BF16)
+    mx_quantize_kernel<__nv_bfloat16, false><<<unsigned(grid), kMxThreads, 0, cs>>>(a);
+  else if (vec)
+    mx_quantize_kernel<float, true><<<unsigned(grid), kMxThreads, 0, cs>>>(a);
+  else
+    mx_quantize_kernel<float, false><<<unsigned(grid), kMxThreads, 0, cs>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
+}
+
+}  // namespace flce
+
+extern "C" size_t flce_mxfp4_codes_size(int64_t rows, int64_t cols) {
+  return mx_sizes_ok(rows, cols) ? size_t(rows) * size_t(mx_pitch(cols)) : 0;
+}
+extern "C" size_t flce_mxfp4_scales_size(int64_t rows, int64_t cols) {
+  return mx_sizes_ok(rows, cols) ? mx_scales_bytes(rows, cols) : 0;
+}
+
+extern "C" int flce_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                                   void* codes, void* scales, flce_stream_t stream) {
+  NvtxRange range("flce_mxfp4_quantize");
+  if (!mx_sizes_ok(rows, cols) || !ln_ld_ok(rows, cols, ld) || !ln_dtype_ok(dtype))
+    return FLCE_ERR_INVALID_ARG;
+  if (rows == 0) return FLCE_OK;
+  if (x == nullptr || codes == nullptr || scales == nullptr ||
+      !aligned(x, dtype == FLCE_F32 ? 4 : 2) || !aligned(codes, 16) || !aligned(scales, 16))
+    return FLCE_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  return mx_quantize(*dev, x, dtype, rows, cols, ld, static_cast<uint8_t*>(codes),
+                     static_cast<uint8_t*>(scales), static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int flce_mxfp4_dequantize(const void* codes, const void* scales, int64_t rows,
+                                     int64_t cols, void* out, int dtype, int64_t ld,
+                                     flce_stream_t stream) {
+  NvtxRange range("flce_mxfp4_dequantize");
+  if (!mx_sizes_ok(rows, cols) || !ln_ld_ok(rows, cols, ld) || !ln_dtype_ok(dtype))
+    return FLCE_ERR_INVALID_ARG;
+  if (rows == 0) return FLCE_OK;
+  const int esz = dtype == FLCE_F32 ? 4 : 2;
+  if (out == nullptr || codes == nullptr || scales == nullptr || !aligned(out, esz) ||
+      !aligned(codes, 16) || !aligned(scales, 16))
+    return FLCE_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  int64_t grid = 0;
+  MxDequantArgs a{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), rows,
+                  cols, rows > 1 ? ld : cols, out, 0};
+  a.segs = mx_segments(rows, cols, dev->num_sms, &grid);
+  const bool vec = mx_vec_ok(out, rows > 1 ? ld : 0, cols, esz);
+  LaunchScope scope(KF_MX_DEQUANT, 0.0, double(rows) * double(cols) * (esz + 17.0 / 32.0), cs);
+  if (dtype == FLCE_BF16 && vec)
+    mx_dequantize_kernel<__nv_bfloat16, true><<<unsigned(grid), kMxThreads, 0, cs>>>(a);
+  else if (dtype == FLCE_BF16)
+    mx_dequantize_kernel<__nv_bfloat16, false><<<unsigned(grid), kMxThreads, 0, cs>>>(a);
+  else if (vec)
+    mx_dequantize_kernel<float, true><<<unsigned(grid), kMxThreads, 0, cs>>>(a);
+  else
+    mx_dequantize_kernel<float, false><<<unsigned(grid), kMxThreads, 0, cs>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
+}

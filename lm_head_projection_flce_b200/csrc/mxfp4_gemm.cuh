@@ -1,0 +1,408 @@
+// mxfp4_gemm.cuh - the LM head's product with both operands in MXFP4:
+//   logits[n, v] = cap( sum_h A[n, h] W[v, h] ),   cap(z) = c tanh(z / c) or z
+// A = the hidden states quantised on the fly, W = the head quantised once.
+// The tensor core multiplies the 4-bit codes and applies both block scales
+// itself (tcgen05.mma kind::mxf4, one E8M0 scale per 32 elements), with FP32
+// accumulation in tensor memory.
+//
+// The head's rows are the M side of the tile (128 rows) and the tokens the N
+// side (16 to 192 columns): a decoding step has few tokens, and then the head's
+// codes, which are all of the traffic, fill whole tiles, while N shrinks to the
+// tokens that exist.  With few tokens the kernel is bound by HBM (the head is
+// read once); with many by the tensor core.
+//
+// Warp 0 loads: per stage of 256 elements of K a 128-byte-swizzled box of codes
+// per operand (TMA), and the scale tiles as plain bulk copies.  Warp 1 copies
+// the stage's scales to tensor memory (tcgen05.cp, 32 lanes x 16 bytes
+// replicated to the four lane quarters) and issues the MMAs; both run in issue
+// order, and each stage has scale columns of its own, rewritten only after
+// the MMAs that read them completed (the stage's empty barrier).  Warps 2..5
+// store the accumulator, of which there are two.  Every wait is bounded.
+#pragma once
+
+#include "mxfp4.cuh"
+
+namespace flce {
+
+constexpr int kMxgKBytes = 128;        // bytes of codes per row and stage
+constexpr int kMxgBlocks = 8;          // scale blocks (256 elements) per stage
+constexpr int kMxgM = 128;             // head rows per tile
+constexpr int kMxgMaxN = 192;          // tokens per tile: two accumulators and the scales fit
+constexpr int kMxgMaxStages = 12;
+constexpr int kMxgSmem = 225 * 1024;   // shared memory for the stages
+
+struct MxGemmArgs {
+  int64_t n, v, h;
+  const uint8_t* w_scales;
+  const uint8_t* a_scales;
+  int tile_n;         // tokens per tile, a multiple of 16
+  int n_tiles;        // token tiles
+  int64_t tiles;      // token tiles x head tiles, token tiles fastest
+  int stages;
+  float softcap, inv_softcap;
+  void* out;
+  int64_t ldo;
+  unsigned* err;
+  uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ void tmem_alloc_one(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
+               "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_one() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_one(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tc_commit_one(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+// 32 rows x 16 bytes of shared memory to 4 columns of all four lane quarters.
+__device__ __forceinline__ void tc_copy_scales_one(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+__device__ __forceinline__ void tc_mma_mxf4_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                                uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
+      "p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// Untiled bulk copy to this CTA's shared memory (16-byte aligned, whole 16s).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// Instruction descriptor of kind::mxf4: E2M1 A and B (K-major), E8M0 scales,
+// shape M x N; the scale words' first byte used (0 or 2) is added per MMA.
+__host__ __device__ constexpr uint32_t mma_idesc_mxf4(int m, int n) {
+  return (1u << 7)                                // A: E2M1
+         | (1u << 10)                             // B: E2M1
+         | (static_cast<uint32_t>(n >> 3) << 17)  // N / 8
+         | (1u << 23)                             // scales: E8M0
+         | (static_cast<uint32_t>(m >> 7) << 27); // M / 128
+}
+// A scale tile in shared memory: unswizzled, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t mx_scale_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+__host__ __device__ __forceinline__ int mxg_scale_tiles(int tile_n) { return tile_n > 128 ? 2 : 1; }
+// Bytes of a stage: codes of both operands, then 2 scale tiles (512 elements of
+// K = 2 x 128) per 128 rows of each.
+__host__ __device__ __forceinline__ uint32_t mxg_stage_bytes(int tile_n) {
+  return uint32_t((kMxgM + tile_n) * kMxgKBytes + (1 + mxg_scale_tiles(tile_n)) * 2 * kMxTileBytes);
+}
+
+template <typename TO>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
+                   const __grid_constant__ CUtensorMap map_a, const MxGemmArgs g) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kMxgMaxStages + 5];
+  __shared__ uint32_t tmem_slot;
+  __shared__ PipeCtl ctl_s;
+  PipeCtl* ctl = &ctl_s;
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t bar_base = smem_u32(bars);
+  const int stages = g.stages;
+  auto full_bar = [&](int s) { return bar_base + 8u * s; };
+  auto empty_bar = [&](int s) { return bar_base + 8u * (kMxgMaxStages + s); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * kMxgMaxStages + a); };
+  auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * kMxgMaxStages + 2 + a); };
+  const uint32_t drain_bar = bar_base + 8u * (2 * kMxgMaxStages + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sft = mxg_scale_tiles(g.tile_n);
+  const uint32_t stage_bytes = mxg_stage_bytes(g.tile_n);
+  const uint32_t off_b = kMxgM * kMxgKBytes;
+  const uint32_t off_sfa = off_b + uint32_t(g.tile_n) * kMxgKBytes;
+  const uint32_t off_sfb = off_sfa + 2 * kMxTileBytes;
+  const int64_t blocks = mx_blocks(g.h), ktiles = mx_ktiles(g.h);
+  const int num_kb = int((blocks + kMxgBlocks - 1) / kMxgBlocks);
+  const int64_t a_tiles = (g.n + kMxTileRows - 1) / kMxTileRows;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), kEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    ctl->abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&map_w);
+    tma_prefetch_desc(&map_a);
+  }
+  if (warp == 1) {
+    tmem_alloc_one(smem_u32(&tmem_slot), kTmemCols);
+    tmem_relinquish_one();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  grid_dependency_wait();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------ loads
+      const uint64_t pol_w = l2_policy_evict_normal();
+      const uint64_t pol_a = l2_policy_evict_last();
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
+        const int64_t mt = t / g.n_tiles;
+        const int64_t n0 = (t - mt * g.n_tiles) * g.tile_n;
+        const int64_t bt = n0 / kMxTileRows;
+        const int nbt = int(min(int64_t(sft), a_tiles - bt));
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!wait_phase(empty_bar(st), ph ^ 1u, ctl, g.err, g.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          const int kts = int(min(int64_t(2), ktiles - 2 * kb));  // scale tiles along K
+          const uint32_t sfb = uint32_t(kts) * kMxTileBytes;
+          const uint32_t base = smem_base + uint32_t(st) * stage_bytes;
+          mbar_arrive_expect_tx(full_bar(st),
+                                uint32_t(kMxgM + g.tile_n) * kMxgKBytes + sfb * uint32_t(1 + nbt));
+          tma_load_2d_hint(base, &map_w, full_bar(st), kb * kMxgKBytes, int(mt * kMxgM), pol_w);
+          tma_load_2d_hint(base + off_b, &map_a, full_bar(st), kb * kMxgKBytes, int(n0), pol_a);
+          bulk_load(base + off_sfa, g.w_scales + (mt * ktiles + 2 * kb) * kMxTileBytes, sfb,
+                    full_bar(st));
+          for (int j = 0; j < nbt; ++j)
+            bulk_load(base + off_sfb + uint32_t(j) * 2 * kMxTileBytes,
+                      g.a_scales + ((bt + j) * ktiles + 2 * kb) * kMxTileBytes, sfb, full_bar(st));
+          if (++st == stages) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        // Give the copies in flight time to land before the block can exit.
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 200000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------ scales to tensor memory, MMAs
+      const uint32_t idesc = mma_idesc_mxf4(kMxgM, g.tile_n);
+      constexpr uint64_t hi = desc_hi_sw128(16u, 1024u);
+      // Scale columns of stage s: [A tile of K half 0, of half 1][B the same, 4 per 128 tokens]
+      const uint32_t sf_cols = uint32_t(8 + 8 * sft);
+      const uint32_t sf_base = tmem + 2u * uint32_t(g.tile_n);
+      int st = 0, acc = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
+        const int64_t n0 = (t % g.n_tiles) * g.tile_n;
+        const uint32_t shift = uint32_t(n0 % kMxTileRows) / 32u;  // first token's scale column
+        if (!wait_phase(tempty_bar(acc), acc_ph ^ 1u, ctl, g.err, g.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d = tmem + uint32_t(acc) * uint32_t(g.tile_n);
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!wait_phase(full_bar(st), ph, ctl, g.err, g.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t base = smem_base + uint32_t(st) * stage_bytes;
+          const uint32_t sfa = sf_base + uint32_t(st) * sf_cols, sfb = sfa + 8u;
+          const int kts = int(min(int64_t(2), ktiles - 2 * kb));
+          for (int k = 0; k < kts; ++k) {
+            tc_copy_scales_one(sfa + 4u * k, mx_scale_desc(base + off_sfa + k * kMxTileBytes));
+            for (int j = 0; j < sft; ++j)
+              tc_copy_scales_one(sfb + uint32_t(k * 4 * sft + 4 * j),
+                                 mx_scale_desc(base + off_sfb + uint32_t(j * 2 + k) * kMxTileBytes));
+          }
+          const int mmas = int(min(int64_t(4), (blocks - int64_t(kb) * kMxgBlocks + 1) / 2));
+          const uint64_t da = hi | static_cast<uint64_t>((base & 0x3FFFFu) >> 4);
+          const uint64_t db = hi | static_cast<uint64_t>(((base + off_b) & 0x3FFFFu) >> 4);
+          for (int kk = 0; kk < mmas; ++kk) {
+            const uint32_t id = uint32_t(kk & 1) * 2u;  // bytes 0,1 or 2,3 of the scale word
+            tc_mma_mxf4_one(d, da + 2u * kk, db + 2u * kk, idesc | (id << 4) | (id << 29),
+                            sfa + 4u * (kk >> 1), sfb + uint32_t((kk >> 1) * 4 * sft) + shift,
+                            (kb | kk) != 0 ? 1u : 0u);
+          }
+          tc_commit_one(empty_bar(st));
+          if (++st == stages) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc_commit_one(tfull_bar(acc));
+        acc ^= 1;
+        if (acc == 0) acc_ph ^= 1u;
+      }
+      tc_commit_one(drain_bar);
+      drain_wait(drain_bar, 0, ok ? g.timeout_ns : 100000000ull);
+    }
+  } else {
+    // -------------------------------------------------- epilogue: lanes are head rows
+    const int quarter = warp & 3;
+    int acc = 0;
+    uint32_t acc_ph = 0;
+    const bool capped = g.softcap > 0.0f;
+    for (int64_t t = blockIdx.x; t < g.tiles; t += gridDim.x) {
+      const int64_t mt = t / g.n_tiles;
+      const int64_t n0 = (t - mt * g.n_tiles) * g.tile_n;
+      if (!wait_phase(tfull_bar(acc), acc_ph, ctl, g.err, g.timeout_ns)) break;
+      __syncwarp();
+      tc_fence_after_sync();
+      const int64_t v = mt * kMxgM + quarter * 32 + lane;
+      const int cols = int(min(int64_t(g.tile_n), g.n - n0));
+      const uint32_t taddr =
+          tmem + (static_cast<uint32_t>(quarter * 32) << 16) + uint32_t(acc) * uint32_t(g.tile_n);
+      for (int c0 = 0; c0 < cols; c0 += 32) {
+        float x[32];
+        tmem_load_32cols(taddr + c0, x);
+        TO* out = static_cast<TO*>(g.out) + (n0 + c0) * g.ldo + v;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (c0 + j < cols && v < g.v) {
+            float z = x[j];
+            if (capped) z = g.softcap * tanhf(z * g.inv_softcap);
+            const float one[1] = {z};
+            LnIo<TO, 1>::store(out + int64_t(j) * g.ldo, one);
+          }
+        }
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty_bar(acc));
+      acc ^= 1;
+      if (acc == 0) acc_ph ^= 1u;
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_one(tmem, kTmemCols);
+  }
+}
+
+// Codes [rows][pitch] as boxes of 128 bytes x box_rows, 128-byte swizzle.
+static bool mx_tmap(CUtensorMap* tm, const void* codes, int64_t rows, int64_t cols, int box_rows) {
+  cuuint64_t dims[2] = {cuuint64_t(mx_pitch(cols)), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(mx_pitch(cols))};
+  cuuint32_t box[2] = {cuuint32_t(kMxgKBytes), cuuint32_t(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename TO>
+static int mx_launch_gemm(const CUtensorMap& mw, const CUtensorMap& ma, const MxGemmArgs& g,
+                          int grid, cudaStream_t cs) {
+  auto kern = mx_gemm_kernel<TO>;
+  const size_t smem = 1024 + size_t(g.stages) * mxg_stage_bytes(g.tile_n);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
+      cudaSuccess)
+    return FLCE_ERR_CUDA;
+  kern<<<grid, kThreads, smem, cs>>>(mw, ma, g);
+  return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
+}
+
+struct MxLogitsPlan {
+  size_t off_scales, total;
+};
+static MxLogitsPlan plan_mx_logits(int64_t n, int64_t h) {
+  MxLogitsPlan p{};
+  p.off_scales = align_up(size_t(n) * size_t(mx_pitch(h)));
+  p.total = std::max(kAlign, align_up(p.off_scales + mx_scales_bytes(n, h)));
+  return p;
+}
+
+}  // namespace flce
+
+extern "C" size_t flce_mxfp4_logits_workspace_size(int64_t n, int64_t h) {
+  return mx_sizes_ok(n, h) ? plan_mx_logits(n, h).total : 0;
+}
+
+extern "C" int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n, int64_t h, int64_t ldh,
+                                 const void* w_codes, const void* w_scales, int64_t vp,
+                                 int64_t unpadded, float softcap, void* logits, int out_dtype,
+                                 int64_t ldo, void* workspace, size_t ws_bytes,
+                                 flce_stream_t stream) {
+  NvtxRange range("flce_mxfp4_logits");
+  const int64_t v = unpadded <= 0 ? vp : unpadded;
+  if (!mx_sizes_ok(n, h) || !mx_sizes_ok(vp, h) || vp <= 0 || v > vp || !ln_ld_ok(n, h, ldh) ||
+      !ln_ld_ok(n, v, ldo) || !ln_dtype_ok(dtype) || !ln_dtype_ok(out_dtype) ||
+      !(softcap >= 0.0f) || !std::isfinite(softcap) ||
+      (softcap > 0.0f && !std::isfinite(1.0f / softcap)))
+    return FLCE_ERR_INVALID_ARG;
+  if (w_codes == nullptr || w_scales == nullptr || !aligned(w_codes, 16) || !aligned(w_scales, 16))
+    return FLCE_ERR_INVALID_ARG;
+  if (n == 0) return FLCE_OK;
+  if (hidden == nullptr || logits == nullptr || !aligned(hidden, dtype == FLCE_F32 ? 4 : 2) ||
+      !aligned(logits, out_dtype == FLCE_F32 ? 4 : 2))
+    return FLCE_ERR_INVALID_ARG;
+  const MxLogitsPlan p = plan_mx_logits(n, h);
+  if (workspace == nullptr || !aligned(workspace, 16) || ws_bytes < p.total)
+    return FLCE_ERR_WORKSPACE;
+  DeviceInfo* dev = nullptr;
+  int st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  uint8_t* a_codes = static_cast<uint8_t*>(workspace);
+  uint8_t* a_scales = a_codes + p.off_scales;
+  st = mx_quantize(*dev, hidden, dtype, n, h, ldh, a_codes, a_scales, cs);
+  if (st != FLCE_OK) return st;
+  MxGemmArgs g{};
+  g.n = n;
+  g.v = v;
+  g.h = h;
+  g.w_scales = static_cast<const uint8_t*>(w_scales);
+  g.a_scales = a_scales;
+  g.tile_n = int(std::min<int64_t>(cdiv(n, 16) * 16, kMxgMaxN));
+  if (g.tile_n > 128) g.tile_n = kMxgMaxN;  // tiles start on a multiple of 64 tokens
+  g.n_tiles = int(cdiv(n, g.tile_n));
+  g.tiles = int64_t(g.n_tiles) * cdiv(v, kMxgM);
+  const int sf_stages = (kTmemCols - 2 * g.tile_n) / (8 + 8 * mxg_scale_tiles(g.tile_n));
+  g.stages = std::min({kMxgMaxStages, sf_stages, int(kMxgSmem / mxg_stage_bytes(g.tile_n))});
+  g.softcap = softcap;
+  g.inv_softcap = softcap > 0.0f ? 1.0f / softcap : 0.0f;
+  g.out = logits;
+  g.ldo = n > 1 ? ldo : v;
+  g.err = dev->err;
+  g.timeout_ns = kDefaultTimeoutNs;
+  CUtensorMap mw, ma;
+  if (!mx_tmap(&mw, w_codes, v, h, kMxgM) || !mx_tmap(&ma, a_codes, n, h, g.tile_n))
+    return FLCE_ERR_CUDA;
+  const int grid = int(std::min<int64_t>(g.tiles, dev->num_sms));
+  const double osz = out_dtype == FLCE_F32 ? 4.0 : 2.0;
+  LaunchScope scope(KF_MX_GEMM, 2.0 * double(n) * double(h) * double(v),
+                    double(n + v) * double(h) * 17.0 / 32.0 + osz * double(n) * double(v), cs);
+  return out_dtype == FLCE_BF16 ? mx_launch_gemm<__nv_bfloat16>(mw, ma, g, grid, cs)
+                                : mx_launch_gemm<float>(mw, ma, g, grid, cs);
+}

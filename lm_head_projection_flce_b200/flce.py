@@ -10,6 +10,7 @@ Entry points mirror include/flce.h:
   backward(hidden, weight, labels, lse, grad, ...) -> (dhidden, dweight)
   fused_linear_cross_entropy(...)                  autograd-aware convenience
   layer_norm(...)                                  the final norm, autograd-aware
+  mxfp4_quantize(...), mxfp4_logits(...)           the head in 4 bits and its product
 with the options of the NeMo-AutoModel loss pages
 ("nemo_automodel.components.loss.linear_ce", FusedLinearCrossEntropy:
 ignore_index=-100, logit_softcapping=0, reduction='sum', num_label_tokens;
@@ -20,6 +21,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import dataclasses
 import os
 
 import torch
@@ -85,6 +87,16 @@ SIGNATURES = {
     "flce_layer_norm_backward": (_c_int, [_c_ptr, _c_i64, _c_ptr, _c_int, _c_i64, _c_i64, _c_i64,
                                           _c_ptr, _c_int, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_ptr,
                                           _c_ptr, _c_ptr, _c_size, _c_ptr]),
+    "flce_mxfp4_codes_size": (_c_size, [_c_i64, _c_i64]),
+    "flce_mxfp4_scales_size": (_c_size, [_c_i64, _c_i64]),
+    "flce_mxfp4_quantize": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr,
+                                     _c_ptr]),
+    "flce_mxfp4_dequantize": (_c_int, [_c_ptr, _c_ptr, _c_i64, _c_i64, _c_ptr, _c_int, _c_i64,
+                                       _c_ptr]),
+    "flce_mxfp4_logits_workspace_size": (_c_size, [_c_i64, _c_i64]),
+    "flce_mxfp4_logits": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_i64,
+                                   _c_i64, ctypes.c_float, _c_ptr, _c_int, _c_i64, _c_ptr, _c_size,
+                                   _c_ptr]),
     "flce_launch_count": (ctypes.c_ulonglong, []),
     "flce_profile_start": (_c_int, []),
     "flce_profile_stop": (_c_int, [_c_ptr, _c_int, ctypes.POINTER(_c_int)]),
@@ -725,3 +737,127 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
     """Autograd-aware layer norm over the last dimension: ``(x - mean) * rstd *
     weight + bias``; gradients flow to ``x``, ``weight`` and ``bias``."""
     return _LayerNorm.apply(x, weight, bias, eps)
+
+
+# ---------------------------------------------------------------- the head in MXFP4
+
+@dataclasses.dataclass(frozen=True)
+class Mxfp4:
+    """A matrix [rows, cols] in microscaled 4-bit floating point (see include/flce.h):
+    ``codes`` uint8 [rows, ceil(cols / 32) * 16], two E2M1 codes per byte, and
+    ``scales`` uint8, one E8M0 exponent per 32 columns, in tiles of 128 rows x 4
+    blocks as the tensor core reads them."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    cols: int
+
+    @property
+    def shape(self) -> tuple[int, int]:
+        return self.rows, self.cols
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    def block_exponents(self) -> torch.Tensor:
+        """The biased exponents as [rows, ceil(cols / 32)] (a copy in row order)."""
+        blocks = -(-self.cols // 32)
+        t = self.scales.view(-(-self.rows // 128), -(-blocks // 4), 32, 4, 4)
+        t = t.permute(0, 3, 2, 1, 4).reshape(-1, -(-blocks // 4) * 4)
+        return t[:self.rows, :blocks].contiguous()
+
+
+def _mxfp4_operand(q: Mxfp4, name: str) -> None:
+    lib = load_library()
+    if not isinstance(q, Mxfp4):
+        raise TypeError(f"{name} must be an Mxfp4 (from mxfp4_quantize)")
+    _buffer(q.codes, int(lib.flce_mxfp4_codes_size(q.rows, q.cols)), torch.uint8, q.device,
+            f"{name}.codes")
+    _buffer(q.scales, int(lib.flce_mxfp4_scales_size(q.rows, q.cols)), torch.uint8, q.device,
+            f"{name}.scales")
+    if q.device.type != "cuda":
+        raise ValueError("tensors must be on one CUDA device")
+
+
+def mxfp4_quantize(x, *, out: Mxfp4 | None = None, stream=None) -> Mxfp4:
+    """``x`` [rows, cols] (bf16 or fp32, contiguous rows) in MXFP4: per 32 columns the
+    power of two 2^(floor(log2 max|x|) - 2), elements rounded to the nearest E2M1
+    number (ties to even, saturating).  ``out`` is overwritten if given.  No gradient
+    flows through it."""
+    lib = load_library()
+    _cuda_tensor(x, W_DTYPES, None, "x")
+    if x.dim() != 2 or x.shape[1] == 0:
+        raise ValueError("x must be [rows, cols] with cols >= 1")
+    rows, ld = _rows(x.detach(), x.shape[1], "x")
+    n, h = x.shape
+    dev = x.device
+    with _on(dev, stream):
+        if out is None:
+            codes = torch.empty(n, -(-h // 32) * 16, dtype=torch.uint8, device=dev)
+            scales = torch.empty(int(lib.flce_mxfp4_scales_size(n, h)), dtype=torch.uint8,
+                                 device=dev)
+            out = Mxfp4(codes, scales, n, h)
+        else:
+            _mxfp4_operand(out, "out")
+            if out.shape != (n, h) or out.device != dev:
+                raise ValueError("out must have x's shape and device")
+        st = lib.flce_mxfp4_quantize(_ptr(rows), W_DTYPES[x.dtype], n, h, ld, _ptr(out.codes),
+                                     _ptr(out.scales), _stream_handle(dev, stream))
+    _check("flce_mxfp4_quantize", st)
+    return out
+
+
+def mxfp4_dequantize(q: Mxfp4, dtype: torch.dtype = torch.bfloat16, *,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The numbers ``q`` stands for, [rows, cols] in bf16 or fp32 (both hold them exactly)."""
+    lib = load_library()
+    _mxfp4_operand(q, "q")
+    if dtype not in W_DTYPES:
+        raise TypeError("dtype must be bf16 or fp32")
+    dev = q.device
+    with _on(dev, stream):
+        out = torch.empty(q.rows, q.cols, dtype=dtype, device=dev) if out is None else out
+        if tuple(out.shape) != q.shape or out.dtype != dtype or out.device != dev:
+            raise ValueError("out must be [rows, cols] of dtype on q's device")
+        rows, ld = _rows(out, q.cols, "out")
+        st = lib.flce_mxfp4_dequantize(_ptr(q.codes), _ptr(q.scales), q.rows, q.cols, _ptr(rows),
+                                       W_DTYPES[dtype], ld, _stream_handle(dev, stream))
+    _check("flce_mxfp4_dequantize", st)
+    return out
+
+
+def mxfp4_logits(hidden, head: Mxfp4, *, softcap: float = 0.0, unpadded_vocab: int | None = None,
+                 dtype: torch.dtype = torch.bfloat16, logits: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``softcap * tanh(z / softcap)`` (softcap 0: ``z``) of ``z = q(hidden) . head^T``,
+    [..., V] in ``dtype``: the hidden states [..., H] (bf16 or fp32) are put into MXFP4
+    in the workspace, the product runs on 4-bit tensor cores with FP32 accumulation.
+    For serving and evaluation: no gradient flows through it."""
+    lib = load_library()
+    _mxfp4_operand(head, "head")
+    _cuda_tensor(hidden, W_DTYPES, head.device, "hidden")
+    if dtype not in W_DTYPES:
+        raise TypeError("dtype must be bf16 or fp32")
+    if hidden.dim() == 0 or hidden.shape[-1] != head.cols:
+        raise ValueError("hidden must be [..., H] with the head's H")
+    dev, h, vp = hidden.device, head.cols, head.rows
+    v = vp if unpadded_vocab is None or unpadded_vocab <= 0 else int(unpadded_vocab)
+    rows, ldh = _rows(hidden.detach(), h, "hidden")
+    n = rows.shape[0]
+    shape = (*hidden.shape[:-1], v)
+    with _on(dev, stream):
+        logits = torch.empty(shape, dtype=dtype, device=dev) if logits is None else logits
+        if tuple(logits.shape) != shape or logits.dtype != dtype or logits.device != dev:
+            raise ValueError("logits must be [..., V] of dtype on hidden's device")
+        out, ldo = _rows(logits, v, "logits")
+        if out.data_ptr() != logits.data_ptr():
+            raise ValueError("the logits' rows must have one stride")
+        ws, ws_bytes = _workspace(workspace, int(lib.flce_mxfp4_logits_workspace_size(n, h)), dev)
+        st = lib.flce_mxfp4_logits(_ptr(rows), W_DTYPES[hidden.dtype], n, h, ldh, _ptr(head.codes),
+                                   _ptr(head.scales), vp, v, float(softcap), _ptr(out),
+                                   W_DTYPES[dtype], ldo, _ptr(ws), ws_bytes,
+                                   _stream_handle(dev, stream))
+    _check("flce_mxfp4_logits", st)
+    return logits
