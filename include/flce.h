@@ -62,7 +62,8 @@ typedef enum {
   FLCE_ERR_UNSUPPORTED = 3, /* no sm_100a device, or more tiles than supported */
   FLCE_ERR_CUDA = 4,        /* a CUDA runtime call or kernel launch failed   */
   FLCE_ERR_BAD_LABEL = 5,   /* (flce_get_error) a label outside [0,V) seen   */
-  FLCE_ERR_TIMEOUT = 6      /* (flce_get_error) a pipeline wait ran out      */
+  FLCE_ERR_TIMEOUT = 6,     /* (flce_get_error) a pipeline wait ran out      */
+  FLCE_ERR_BAD_INDEX = 7    /* (flce_get_error) a parent outside [0, beams)  */
 } flce_status;
 
 typedef enum { FLCE_SUM = 0, FLCE_MEAN = 1, FLCE_NONE = 2 } flce_reduction;
@@ -197,7 +198,8 @@ int flce_backward_ex(const void* hidden, const void* weight, int w_dtype,
 /*
  * Synchronises `stream`, then reads and clears the calling device's error word:
  * FLCE_ERR_BAD_LABEL if a kernel saw a label outside [0, V) that was not
- * ignore_index, FLCE_ERR_TIMEOUT if a pipeline wait gave up (the affected
+ * ignore_index, FLCE_ERR_BAD_INDEX if flce_beam_reorder saw a parent outside
+ * [0, beams), FLCE_ERR_TIMEOUT if a pipeline wait gave up (the affected
  * output is then incomplete), FLCE_ERR_CUDA if the synchronisation failed,
  * else FLCE_OK.  The word is shared by every call on the device since the
  * last read.
@@ -328,6 +330,60 @@ int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n_tokens, int64_t h
                       int64_t padded_vocab, int64_t unpadded_vocab, float softcap, void* logits,
                       int out_dtype, int64_t ldo, void* workspace, size_t ws_bytes,
                       flce_stream_t stream);
+
+/*
+ * Beam search behind the head: which continuations are kept.
+ *   score(k, v) = scores[b, k] + logits[b, k, v] - logsumexp_v logits[b, k, v]
+ *   and the num_select best (k, v) of each batch item in descending order,
+ *   ties to the lowest k * vocab + v.
+ *   logits     row (b, k) at (b * beams + k) * ld elements, BF16 (dtype 0) or
+ *              FP32 (1), the first vocab entries of it; any alignment of whole
+ *              elements.  -inf excludes a token.
+ *   scores     FP32 [batch, beams], cumulative log-probabilities.  A beam whose
+ *              score is not finite has no candidates (give the beams beyond the
+ *              first -inf in the first step); its logits are not read.
+ *   finished   uint8 [batch, beams] or NULL; a non-zero entry's beam has the one
+ *              candidate (k, eos_token) with its score unchanged, and its logits
+ *              are not read.  eos_token is only looked at with finished.
+ *   num_select 1 .. 64, <= beams * vocab; beams 1 .. 64; beams * vocab < 2^31.
+ *   out_scores FP32, parents and tokens int64, all [batch, num_select].
+ *              Candidates with a NaN score (a NaN or +inf in the row) count as
+ *              -inf; where fewer than num_select are above -inf, the rest are
+ *              the lowest unused k * vocab + v with score -inf.
+ *   workspace  >= flce_beam_select_workspace_size(...) bytes, 16-byte aligned.
+ * The logits are read once; sums of exponentials are held in FP32 per thread and
+ * FP64 beyond, scores are compared in FP64 and rounded once.
+ */
+size_t flce_beam_select_workspace_size(int64_t batch, int64_t beams, int64_t vocab,
+                                       int64_t num_select);
+int flce_beam_select(const void* logits, int dtype, int64_t batch, int64_t beams, int64_t vocab,
+                     int64_t ld, const float* scores, const uint8_t* finished, int64_t eos_token,
+                     int64_t num_select, float* out_scores, int64_t* parents, int64_t* tokens,
+                     void* workspace, size_t ws_bytes, flce_stream_t stream);
+
+/*
+ * ... and the states (key / value caches and the like) that follow their beams:
+ *   dst[b, k] = src[b, parents[b, k]] for every state.
+ *   states   host array of `count` descriptions; a state's (b, k) entry is `outer`
+ *            pieces of `inner` bytes, outer_stride bytes apart, at src + b *
+ *            src_batch_stride + k * src_beam_stride (bytes), likewise dst.  What
+ *            lies between and behind the pieces is left as it was.
+ *            dst == src (with the same strides): in place, without scratch.
+ *            Otherwise dst must not overlap any src.  Entries of dst must not
+ *            overlap one another; the same dst twice is refused.
+ *   parents  int64 [batch, beams], any map (the same parent may repeat).  An
+ *            entry outside [0, beams) leaves its beam's own state and raises
+ *            FLCE_ERR_BAD_INDEX in the error word (flce_get_error).
+ */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t src_batch_stride, src_beam_stride;
+  int64_t dst_batch_stride, dst_beam_stride;
+  int64_t outer, outer_stride, inner;
+} flce_beam_state;
+int flce_beam_reorder(const flce_beam_state* states, int64_t count, const int64_t* parents,
+                      int64_t batch, int64_t beams, flce_stream_t stream);
 
 /*
  * Forward that allocates nothing and takes no workspace (the pages have no

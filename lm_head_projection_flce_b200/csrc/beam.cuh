@@ -1,0 +1,651 @@
+// beam.cuh - beam search behind the LM head: which continuations of the K beams
+// of each batch item are kept, and the reordering of the beams' states.
+//
+// Selection.  For item b with logits z[k, v] and cumulative log-probabilities s_k:
+//   score(k, v) = s_k + z[k, v] - lse_k,   lse_k = log sum_v exp z[k, v]
+// the M best of the K V candidates, ties to the lowest k V + v.  A finished beam
+// has one candidate, (k, eos) with score s_k.  A beam whose s_k is not finite,
+// and a candidate whose score is NaN, count as -inf; where fewer than M
+// candidates are above -inf, the lowest unused k V + v fill up with -inf.
+//
+// One pass over the logits finds both sums and candidates: a block streams a
+// segment of a beam's row, each thread keeping its running maximum and sum of
+// exponentials, and its largest element with the vector that held it.  The
+// M-th largest of the 256 threads' maxima bounds the M-th largest element from
+// below, so the M best elements of the segment all lie with the at most M
+// threads above the bound; only those threads' vectors (M / 256 of the
+// segment, now in L2) are looked at again and the few elements above the bound
+// sorted by counting.  The pass costs one exponential per element and one
+// comparison per vector, like a plain logsumexp, and is bound by HBM.
+// A second kernel merges an item's segments: lse_k, the candidates' scores in
+// FP64 (scores of different beams lie next to one another; in FP32 their
+// rounding would decide), and the M best, by the same bound.
+//
+// Elements are dealt to threads by their index in the row, never by address,
+// so equal rows give equal sums bit for bit and their ties stay ties.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "chunked_ce.cuh"
+#include "layer_norm.cuh"
+
+namespace flce {
+
+constexpr int kBeamThreads = 256;
+constexpr int kBeamMaxBeams = 64;
+constexpr int kBeamMaxSelect = 64;
+constexpr int kBeamUnroll = 4;            // vectors in flight per thread
+constexpr int kBeamList = 1024;           // elements above the bound that are sorted in one go
+constexpr int64_t kBeamMinSegment = 4096; // elements
+constexpr int kBeamMaxItems = 4096;       // candidates merged per batch item: K x segments x M
+
+// Total order of (value, index): larger value first, then the lower index; a key
+// of 0 is below every element.  -0 and +0 are equal values.
+__device__ __forceinline__ uint32_t beam_order(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float beam_value(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+__device__ __forceinline__ uint64_t beam_key(float x, uint32_t index) {
+  return (static_cast<uint64_t>(beam_order(x)) << 32) | (0xffffffffu - index);
+}
+
+// VN elements at row + c, c + j < end only.
+template <typename T, int VN>
+__device__ __forceinline__ void beam_load(const T* row, int64_t c, int64_t end, bool vec,
+                                          float (&x)[VN]) {
+  if (vec && c + VN <= end) {
+    LnIo<T, VN>::load(row + c, x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VN; ++j) {
+      float one[1] = {-INFINITY};
+      if (c + j < end) LnIo<T, 1>::load(row + c + j, one);
+      x[j] = one[0];
+    }
+  }
+}
+
+struct BeamPartArgs {
+  const void* logits;
+  int64_t ld, vocab, segment;
+  int splits, select;
+  int64_t rows;
+  const float* scores;      // [rows]
+  const uint8_t* finished;  // [rows] or nullptr
+  float* part_m;            // [rows][splits]: maximum, and sum of exp(z - maximum)
+  double* part_s;
+  float* cand_z;            // [rows][splits][select], best first; index -1: none
+  int* cand_v;
+};
+
+__device__ __forceinline__ bool beam_is_live(float score) {
+  return fabsf(score) <= 3.402823466e38f;  // finite
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads) beam_partials_kernel(const BeamPartArgs a) {
+  constexpr int VN = 16 / int(sizeof(T));
+  __shared__ uint64_t keys[kBeamThreads];
+  __shared__ uint64_t list[kBeamList];
+  __shared__ int owners[kBeamMaxSelect];
+  __shared__ uint64_t bound_s;
+  __shared__ int n_owners, n_list;
+  __shared__ float red_m[kBeamThreads / 32];
+  __shared__ double red_s[kBeamThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = blockIdx.x / a.splits;
+  const int part = int(blockIdx.x - row * a.splits);
+  if (!beam_is_live(a.scores[row]) || (a.finished && a.finished[row])) return;
+  const T* z = static_cast<const T*>(a.logits) + row * a.ld;
+  const bool vec = (reinterpret_cast<uintptr_t>(z) & 15) == 0;
+  const int64_t begin = int64_t(part) * a.segment, end = min(a.vocab, begin + a.segment);
+  const int64_t count = max(int64_t(0), (end - begin + VN - 1) / VN);  // vectors
+
+  float m = -INFINITY, s = 0.0f, best = -INFINITY;
+  uint32_t best_at = 0;  // first element of the vector that holds `best`
+  for (int64_t j0 = tid; j0 < count; j0 += int64_t(kBeamUnroll) * kBeamThreads) {
+    float x[kBeamUnroll][VN];
+#pragma unroll
+    for (int u = 0; u < kBeamUnroll; ++u) {
+      const int64_t c = begin + (j0 + int64_t(u) * kBeamThreads) * VN;
+      beam_load<T, VN>(z, min(c, end), end, vec, x[u]);
+    }
+    float bm = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kBeamUnroll; ++u) {
+      float vm = x[u][0];
+#pragma unroll
+      for (int j = 1; j < VN; ++j) vm = fmaxf(vm, x[u][j]);
+      if (vm > best) {
+        best = vm;
+        best_at = uint32_t(begin + (j0 + int64_t(u) * kBeamThreads) * VN);
+      }
+      bm = fmaxf(bm, vm);
+    }
+    if (bm > m) {
+      s *= fast_exp2((m - bm) * kLog2e);
+      m = bm;
+    }
+    if (m == -INFINITY) {
+      // nothing but -inf so far; a NaN must still reach the sum
+#pragma unroll
+      for (int u = 0; u < kBeamUnroll; ++u)
+#pragma unroll
+        for (int j = 0; j < VN; ++j)
+          if (x[u][j] != x[u][j]) s = x[u][j];
+      continue;
+    }
+#pragma unroll
+    for (int u = 0; u < kBeamUnroll; ++u)
+#pragma unroll
+      for (int j = 0; j < VN; ++j) s += fast_exp2((x[u][j] - m) * kLog2e);
+  }
+
+  // The segment's maximum and sum, added in a fixed order.
+  float bm = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+  if (lane == 0) red_m[warp] = bm;
+  keys[tid] = best > -INFINITY ? beam_key(best, best_at) : 0;
+  if (tid == 0) {
+    bound_s = 0;
+    n_owners = n_list = 0;
+  }
+  __syncthreads();
+  bm = red_m[0];
+#pragma unroll
+  for (int w = 1; w < kBeamThreads / 32; ++w) bm = fmaxf(bm, red_m[w]);
+  double ds = m == -INFINITY ? double(s) : double(s) * double(fast_exp2((m - bm) * kLog2e));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
+  if (lane == 0) red_s[warp] = ds;
+
+  // The bound: the select-th largest of the threads' keys (0: fewer hold anything).
+  const uint64_t mine = keys[tid];
+  int rank = 0;
+  for (int i = 0; i < kBeamThreads; ++i) rank += keys[i] > mine ? 1 : 0;
+  if (mine != 0 && rank == a.select - 1) bound_s = mine;
+  __syncthreads();
+  const uint64_t bound = bound_s;
+  if (mine != 0 && mine >= bound) owners[atomicAdd(&n_owners, 1)] = tid;  // at most `select`
+  if (tid == 0) {
+    double t = 0.0;
+    for (int w = 0; w < kBeamThreads / 32; ++w) t += red_s[w];
+    const int64_t at = row * a.splits + part;
+    a.part_m[at] = bm;
+    a.part_s[at] = t;
+  }
+  __syncthreads();
+
+  // Elements of the owners' vectors whose (value, vector) is not below the bound.
+  const int64_t per = (count + kBeamThreads - 1) / kBeamThreads;  // vectors per thread
+  const int64_t work = int64_t(n_owners) * per;
+  auto scan = [&](auto&& take) {
+    for (int64_t w = tid; w < work; w += kBeamThreads) {
+      const int64_t j = owners[w / per] + (w % per) * kBeamThreads;
+      if (j >= count) continue;
+      float x[VN];
+      beam_load<T, VN>(z, begin + j * VN, end, vec, x);
+#pragma unroll
+      for (int i = 0; i < VN; ++i) {
+        const uint32_t at = uint32_t(begin + j * VN);
+        if (x[i] > -INFINITY && beam_key(x[i], at) >= bound) take(beam_key(x[i], at + i));
+      }
+    }
+  };
+  scan([&](uint64_t key) {
+    const int at = atomicAdd(&n_list, 1);
+    if (at < kBeamList) list[at] = key;
+  });
+  __syncthreads();
+  const int n = n_list;
+  const int64_t out = (row * a.splits + part) * a.select;
+  auto put = [&](int slot, uint64_t key) {
+    a.cand_z[out + slot] = beam_value(uint32_t(key >> 32));
+    a.cand_v[out + slot] = int(0xffffffffu - uint32_t(key));
+  };
+  if (n <= kBeamList) {
+    // The list's order is that of the atomics; the keys are distinct, so their
+    // ranks are not.
+    for (int i = tid; i < n; i += kBeamThreads) {
+      const uint64_t key = list[i];
+      int r = 0;
+      for (int j = 0; j < n; ++j) r += list[j] > key ? 1 : 0;
+      if (r < a.select) put(r, key);
+    }
+    for (int i = n + tid; i < a.select; i += kBeamThreads) a.cand_v[out + i] = -1;
+    return;
+  }
+  // More elements above the bound than the list holds (a few threads own nearly
+  // all large elements): the largest one below the last, `select` times over.
+  uint64_t last = ~uint64_t(0);
+  for (int slot = 0; slot < a.select; ++slot) {
+    uint64_t top = 0;
+    scan([&](uint64_t key) {
+      if (key < last && key > top) top = key;
+    });
+    __syncthreads();
+    keys[tid] = top;
+    __syncthreads();
+    for (int h = kBeamThreads / 2; h > 0; h >>= 1) {
+      if (tid < h) keys[tid] = max(keys[tid], keys[tid + h]);
+      __syncthreads();
+    }
+    last = keys[0];  // never 0: more than kBeamList >= select elements qualify
+    if (tid == 0) put(slot, last);
+  }
+}
+
+struct BeamMergeArgs {
+  int beams, splits, select;
+  int64_t vocab, eos;
+  const float* scores;
+  const uint8_t* finished;
+  const float* part_m;
+  const double* part_s;
+  const float* cand_z;
+  const int* cand_v;
+  float* out_scores;  // [batch][select]
+  int64_t* parents;
+  int64_t* tokens;
+};
+
+// Totals in FP64 as ordered integers (NaN: 0, below -inf); flat candidate index.
+__device__ __forceinline__ uint64_t beam_order64(double x) {
+  if (x != x) return 0;
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
+  return (u >> 63) ? ~u : (u | (uint64_t(1) << 63));
+}
+__device__ __forceinline__ double beam_value64(uint64_t o) {
+  return __longlong_as_double(static_cast<long long>((o >> 63) ? (o & ~(uint64_t(1) << 63)) : ~o));
+}
+__device__ __forceinline__ bool beam_above(uint64_t ta, uint32_t ia, uint64_t tb, uint32_t ib) {
+  return ta > tb || (ta == tb && ia < ib);
+}
+
+// One block per batch item.
+__global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMergeArgs a) {
+  extern __shared__ uint64_t dyn[];
+  __shared__ double lse[kBeamMaxBeams];
+  __shared__ uint64_t head_t[kBeamThreads];
+  __shared__ uint32_t head_i[kBeamThreads];
+  __shared__ uint64_t bound_t;
+  __shared__ uint32_t bound_i;
+  __shared__ int n_list, n_out;
+  __shared__ uint32_t chosen[kBeamMaxSelect];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per_beam = a.splits * a.select;
+  const int items = a.beams * per_beam;
+  uint64_t* tot = dyn;                                          // [items]
+  uint32_t* idx = reinterpret_cast<uint32_t*>(tot + items);     // [items]
+  uint32_t* list = idx + items;                                 // [items]: positions above the bound
+  const int64_t b = blockIdx.x;
+  const float* scores = a.scores + b * a.beams;
+  const uint8_t* finished = a.finished ? a.finished + b * a.beams : nullptr;
+  grid_dependency_wait();
+  if (tid == 0) {
+    bound_t = 0;
+    bound_i = 0xffffffffu;
+    n_list = n_out = 0;
+  }
+  const double ninf = -static_cast<double>(INFINITY);
+  for (int k = warp; k < a.beams; k += kBeamThreads / 32) {
+    if (!beam_is_live(scores[k]) || (finished && finished[k])) continue;
+    const int64_t at = (b * a.beams + k) * a.splits;
+    float m = -INFINITY;
+    for (int p = lane; p < a.splits; p += 32) m = fmaxf(m, a.part_m[at + p]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    double s = 0.0;
+    for (int p = lane; p < a.splits; p += 32) {
+      const double ps = a.part_s[at + p];
+      const float pm = a.part_m[at + p];
+      s += pm == m || pm == -INFINITY ? ps : ps * exp(double(pm) - double(m));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) lse[k] = double(m) + log(s);
+  }
+  __syncthreads();
+
+  uint64_t ht = 0;
+  uint32_t hi = 0xffffffffu;
+  for (int i = tid; i < items; i += kBeamThreads) {
+    const int k = i / per_beam, j = i - k * per_beam;
+    double t = ninf;
+    uint32_t f = 0xffffffffu;
+    const float s = scores[k];
+    if (beam_is_live(s)) {
+      if (finished && finished[k]) {
+        if (j == 0) {
+          t = double(s);
+          f = uint32_t(k * a.vocab + a.eos);
+        }
+      } else {
+        const int64_t at = (b * a.beams + k) * per_beam + j;
+        const int v = a.cand_v[at];
+        if (v >= 0) {
+          t = double(s) + double(a.cand_z[at]) - lse[k];
+          f = uint32_t(k * a.vocab + v);
+        }
+      }
+    }
+    const uint64_t o = f != 0xffffffffu && t > ninf ? beam_order64(t) : 0;  // NaN and -inf: none
+    tot[i] = o;
+    idx[i] = f;
+    if (o != 0 && beam_above(o, f, ht, hi)) {
+      ht = o;
+      hi = f;
+    }
+  }
+  head_t[tid] = ht;
+  head_i[tid] = hi;
+  __syncthreads();
+  if (ht != 0) {
+    int rank = 0;
+    for (int i = 0; i < kBeamThreads; ++i)
+      rank += head_t[i] != 0 && beam_above(head_t[i], head_i[i], ht, hi) ? 1 : 0;
+    if (rank == a.select - 1) {
+      bound_t = ht;
+      bound_i = hi;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < items; i += kBeamThreads)
+    if (tot[i] != 0 && !beam_above(bound_t, bound_i, tot[i], idx[i])) list[atomicAdd(&n_list, 1)] = i;
+  __syncthreads();
+  const int n = n_list;
+  for (int i = tid; i < n; i += kBeamThreads) {
+    const uint64_t t = tot[list[i]];
+    const uint32_t f = idx[list[i]];
+    int r = 0;
+    for (int j = 0; j < n; ++j) r += beam_above(tot[list[j]], idx[list[j]], t, f) ? 1 : 0;
+    if (r < a.select) {
+      const int64_t at = b * a.select + r;
+      a.out_scores[at] = float(beam_value64(t));
+      a.parents[at] = int64_t(f / a.vocab);
+      a.tokens[at] = int64_t(f % a.vocab);
+      chosen[r] = f;
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && n < a.select) {  // fewer candidates than wanted: the lowest unused indices
+    uint32_t f = 0;
+    for (int r = n; r < a.select; ++r, ++f) {
+      for (int j = 0; j < n; ++j)
+        if (chosen[j] == f) {
+          ++f;
+          j = -1;
+        }
+      const int64_t at = b * a.select + r;
+      a.out_scores[at] = -INFINITY;
+      a.parents[at] = int64_t(f / a.vocab);
+      a.tokens[at] = int64_t(f % a.vocab);
+    }
+  }
+}
+
+struct BeamPlan {
+  int splits;
+  int64_t segment;
+  size_t off_s, off_m, off_z, off_v, total;
+};
+
+// Segments per row: enough blocks for the GPU when there are few rows, none
+// shorter than kBeamMinSegment, and no more candidates per item than one block merges.
+static BeamPlan plan_beam(int64_t batch, int64_t beams, int64_t vocab, int64_t select) {
+  BeamPlan p{};
+  const int64_t rows = std::max<int64_t>(1, batch * beams);
+  int64_t s = cdiv(4 * kLnSms, rows);
+  s = std::min({s, std::max<int64_t>(1, vocab / kBeamMinSegment),
+                std::max<int64_t>(1, kBeamMaxItems / (beams * select))});
+  p.segment = cdiv(cdiv(vocab, s), 8) * 8;
+  p.splits = int(cdiv(vocab, p.segment));
+  const size_t units = size_t(rows) * size_t(p.splits);
+  size_t o = 0;
+  p.off_s = o;  o = align_up(o + units * 8);
+  p.off_m = o;  o = align_up(o + units * 4);
+  p.off_z = o;  o = align_up(o + units * size_t(select) * 4);
+  p.off_v = o;  o = align_up(o + units * size_t(select) * 4);
+  p.total = o;
+  return p;
+}
+
+static bool beam_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t select) {
+  return batch >= 0 && beams >= 1 && beams <= kBeamMaxBeams && vocab >= 1 && select >= 1 &&
+         select <= kBeamMaxSelect && batch <= kMaxDim / kBeamMaxItems &&
+         vocab <= kMaxDim / kBeamMaxBeams && select <= beams * vocab;
+}
+
+// ---------------------------------------------------------------- reordering of states
+
+constexpr int kReorderStates = 16;  // per launch
+constexpr int kReorderThreads = 256;
+
+struct ReorderState {
+  const uint8_t* src;
+  uint8_t* dst;
+  int64_t src_batch, src_beam, dst_batch, dst_beam;  // strides in bytes
+  int64_t outer, outer_stride, inner;                // pieces of `inner` bytes
+};
+struct ReorderArgs {
+  ReorderState st[kReorderStates];
+  const int64_t* parents;
+  int64_t batch;
+  int beams;
+  unsigned* err;
+};
+
+// dst[b, k] = src[b, parents[b, k]].  A thread takes one vector position of all
+// K beams: it loads the parents' values, then stores.  In place (kInPlace) that
+// makes the permutation safe without scratch memory, as no other thread touches
+// this position; beams that keep their own state are neither read nor written.
+// Otherwise groups of KM beams at a time; a parent shared by several beams is
+// read from HBM once, by whichever load comes first.  Bound by HBM.
+template <typename V, int KM, bool kInPlace>
+__global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(const __grid_constant__ ReorderArgs a) {
+  __shared__ int parent[kBeamMaxBeams];
+  const ReorderState& st = a.st[blockIdx.z];
+  const int64_t per = st.inner / int64_t(sizeof(V)), total = st.outer * per;
+  for (int64_t b = blockIdx.y; b < a.batch; b += gridDim.y) {
+    __syncthreads();
+    if (threadIdx.x < a.beams) {
+      int64_t p = a.parents[b * a.beams + threadIdx.x];
+      if (p < 0 || p >= a.beams) {
+        if (blockIdx.x == 0) atomicOr(a.err, kDevErrBadIndex);
+        p = threadIdx.x;
+      }
+      parent[threadIdx.x] = int(p);
+    }
+    __syncthreads();
+    for (int64_t i = int64_t(blockIdx.x) * kReorderThreads + threadIdx.x; i < total;
+         i += int64_t(gridDim.x) * kReorderThreads) {
+      const int64_t o = i / per, c = i - o * per;
+      const uint8_t* src = st.src + b * st.src_batch + o * st.outer_stride + c * int64_t(sizeof(V));
+      uint8_t* dst = st.dst + b * st.dst_batch + o * st.outer_stride + c * int64_t(sizeof(V));
+      for (int k0 = 0; k0 < a.beams; k0 += KM) {
+        V v[KM];
+#pragma unroll
+        for (int j = 0; j < KM; ++j)
+          if (k0 + j < a.beams && !(kInPlace && parent[k0 + j] == k0 + j))
+            v[j] = *reinterpret_cast<const V*>(src + parent[k0 + j] * st.src_beam);
+#pragma unroll
+        for (int j = 0; j < KM; ++j)
+          if (k0 + j < a.beams && !(kInPlace && parent[k0 + j] == k0 + j))
+            *reinterpret_cast<V*>(dst + (k0 + j) * st.dst_beam) = v[j];
+      }
+    }
+  }
+}
+
+}  // namespace flce
+
+extern "C" size_t flce_beam_select_workspace_size(int64_t batch, int64_t beams, int64_t vocab,
+                                                  int64_t select) {
+  return beam_sizes_ok(batch, beams, vocab, select) ? plan_beam(batch, beams, vocab, select).total
+                                                    : 0;
+}
+
+extern "C" int flce_beam_select(const void* logits, int dtype, int64_t batch, int64_t beams,
+                                int64_t vocab, int64_t ld, const float* scores,
+                                const uint8_t* finished, int64_t eos_token, int64_t num_select,
+                                float* out_scores, int64_t* parents, int64_t* tokens,
+                                void* workspace, size_t ws_bytes, flce_stream_t stream) {
+  NvtxRange range("flce_beam_select");
+  if (!beam_sizes_ok(batch, beams, vocab, num_select) || !ln_dtype_ok(dtype) ||
+      !ln_ld_ok(batch * beams, vocab, ld))
+    return FLCE_ERR_INVALID_ARG;
+  if (finished != nullptr && (eos_token < 0 || eos_token >= vocab)) return FLCE_ERR_INVALID_ARG;
+  if (batch == 0) return FLCE_OK;
+  if (logits == nullptr || scores == nullptr || out_scores == nullptr || parents == nullptr ||
+      tokens == nullptr || !aligned(logits, dtype == FLCE_F32 ? 4 : 2) || !aligned(scores, 4) ||
+      !aligned(out_scores, 4) || !aligned(parents, 8) || !aligned(tokens, 8))
+    return FLCE_ERR_INVALID_ARG;
+  const BeamPlan p = plan_beam(batch, beams, vocab, num_select);
+  if (workspace == nullptr || !aligned(workspace, 16) || ws_bytes < p.total)
+    return FLCE_ERR_WORKSPACE;
+  DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int64_t rows = batch * beams;
+  BeamPartArgs a{};
+  a.logits = logits;
+  a.ld = ld;
+  a.vocab = vocab;
+  a.segment = p.segment;
+  a.splits = p.splits;
+  a.select = int(num_select);
+  a.rows = rows;
+  a.scores = scores;
+  a.finished = finished;
+  a.part_s = reinterpret_cast<double*>(ws + p.off_s);
+  a.part_m = reinterpret_cast<float*>(ws + p.off_m);
+  a.cand_z = reinterpret_cast<float*>(ws + p.off_z);
+  a.cand_v = reinterpret_cast<int*>(ws + p.off_v);
+  {
+    LaunchScope scope(KF_BEAM_PART, 0.0, double(rows) * double(vocab) * (dtype == FLCE_F32 ? 4 : 2), cs);
+    const unsigned grid = unsigned(rows * p.splits);
+    if (dtype == FLCE_BF16)
+      beam_partials_kernel<__nv_bfloat16><<<grid, kBeamThreads, 0, cs>>>(a);
+    else
+      beam_partials_kernel<float><<<grid, kBeamThreads, 0, cs>>>(a);
+  }
+  if (cudaGetLastError() != cudaSuccess) return FLCE_ERR_CUDA;
+  BeamMergeArgs g{};
+  g.beams = int(beams);
+  g.splits = p.splits;
+  g.select = int(num_select);
+  g.vocab = vocab;
+  g.eos = eos_token;
+  g.scores = scores;
+  g.finished = finished;
+  g.part_m = a.part_m;
+  g.part_s = a.part_s;
+  g.cand_z = a.cand_z;
+  g.cand_v = a.cand_v;
+  g.out_scores = out_scores;
+  g.parents = parents;
+  g.tokens = tokens;
+  const size_t smem = size_t(beams) * size_t(p.splits) * size_t(num_select) * 16;
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kBeamMaxItems * 16) != cudaSuccess)
+    return FLCE_ERR_CUDA;
+  LaunchScope scope(KF_BEAM_MERGE, 0.0, double(rows) * p.splits * (12.0 + 8.0 * double(num_select)), cs);
+  beam_merge_kernel<<<unsigned(batch), kBeamThreads, smem, cs>>>(g);
+  return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
+}
+
+extern "C" int flce_beam_reorder(const flce_beam_state* states, int64_t count,
+                                 const int64_t* parents, int64_t batch, int64_t beams,
+                                 flce_stream_t stream) {
+  NvtxRange range("flce_beam_reorder");
+  if (count < 0 || batch < 0 || batch > kMaxDim || beams < 1 || beams > kBeamMaxBeams ||
+      (count > 0 && states == nullptr))
+    return FLCE_ERR_INVALID_ARG;
+  if (count == 0 || batch == 0) return FLCE_OK;
+  if (parents == nullptr || !aligned(parents, 8)) return FLCE_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < count; ++i) {
+    const flce_beam_state& s = states[i];
+    if (s.src == nullptr || s.dst == nullptr || s.outer < 0 || s.inner < 0 || s.outer_stride < 0 ||
+        s.src_batch_stride < 0 || s.src_beam_stride < 0 || s.dst_batch_stride < 0 ||
+        s.dst_beam_stride < 0 || (s.outer > 1 && s.outer_stride < s.inner) ||
+        (s.inner > 0 && s.outer > (int64_t(1) << 46) / s.inner))
+      return FLCE_ERR_INVALID_ARG;
+    // the same buffer: in place, so the same layout
+    if (s.src == s.dst && (s.src_batch_stride != s.dst_batch_stride ||
+                           s.src_beam_stride != s.dst_beam_stride))
+      return FLCE_ERR_INVALID_ARG;
+    for (int64_t j = 0; j < i; ++j)  // a state given twice would be written by two blocks at once
+      if (states[j].dst == s.dst) return FLCE_ERR_INVALID_ARG;
+  }
+  DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != FLCE_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  // States of one kind (in place or not, the same widest vector) share launches.
+  for (int in_place = 0; in_place < 2; ++in_place) {
+    // In place a thread holds a position of all beams, so more beams mean narrower vectors.
+    const int widest = !in_place || beams <= 16 ? 16 : (beams <= 32 ? 8 : 4);
+    for (int vb = 16; vb >= 1; vb >>= 1) {
+      ReorderArgs a{};
+      a.parents = parents;
+      a.batch = batch;
+      a.beams = int(beams);
+      a.err = dev->err;
+      int n = 0;
+      int64_t most = 0;
+      double bytes = 0.0;
+      for (int64_t i = 0; i <= count; ++i) {
+        if (i < count) {
+          const flce_beam_state& s = states[i];
+          const uint64_t bits = reinterpret_cast<uint64_t>(s.src) | reinterpret_cast<uint64_t>(s.dst) |
+                                uint64_t(s.src_batch_stride) | uint64_t(s.src_beam_stride) |
+                                uint64_t(s.dst_batch_stride) | uint64_t(s.dst_beam_stride) |
+                                uint64_t(s.outer > 1 ? s.outer_stride : 0) | uint64_t(s.inner);
+          int v = widest;
+          while (bits % uint64_t(v) != 0) v >>= 1;
+          if ((s.src == s.dst) != (in_place == 1) || v != vb || s.outer * s.inner == 0) continue;
+          a.st[n++] = ReorderState{static_cast<const uint8_t*>(s.src), static_cast<uint8_t*>(s.dst),
+                                   s.src_batch_stride, s.src_beam_stride, s.dst_batch_stride,
+                                   s.dst_beam_stride, s.outer, s.outer_stride, s.inner};
+          most = std::max(most, s.outer * (s.inner / vb));
+          bytes += 2.0 * double(batch) * double(beams) * double(s.outer) * double(s.inner);
+          if (n < kReorderStates) continue;
+        }
+        if (n == 0) continue;
+        const unsigned gy = unsigned(std::min<int64_t>(batch, 65535));
+        const int64_t want = std::max<int64_t>(1, int64_t(dev->num_sms) * 16 / (int64_t(gy) * n));
+        const dim3 grid(unsigned(std::min<int64_t>(cdiv(most, kReorderThreads), want)), gy, unsigned(n));
+        LaunchScope scope(KF_BEAM_REORDER, 0.0, bytes, cs);
+        auto go = [&](auto kern) { kern<<<grid, kReorderThreads, 0, cs>>>(a); };
+        if (in_place) {
+          if (vb == 16 && beams <= 4) go(beam_reorder_kernel<uint4, 4, true>);
+          else if (vb == 16 && beams <= 8) go(beam_reorder_kernel<uint4, 8, true>);
+          else if (vb == 16) go(beam_reorder_kernel<uint4, 16, true>);
+          else if (vb == 8 && beams <= 32) go(beam_reorder_kernel<uint2, 32, true>);
+          else if (vb == 4) go(beam_reorder_kernel<uint32_t, 64, true>);
+          else if (vb == 2) go(beam_reorder_kernel<uint16_t, 64, true>);
+          else go(beam_reorder_kernel<uint8_t, 64, true>);
+        } else {
+          if (vb == 16) go(beam_reorder_kernel<uint4, 8, false>);
+          else if (vb == 8) go(beam_reorder_kernel<uint2, 8, false>);
+          else if (vb == 4) go(beam_reorder_kernel<uint32_t, 8, false>);
+          else if (vb == 2) go(beam_reorder_kernel<uint16_t, 8, false>);
+          else go(beam_reorder_kernel<uint8_t, 8, false>);
+        }
+        if (cudaGetLastError() != cudaSuccess) return FLCE_ERR_CUDA;
+        n = 0;
+        most = 0;
+        bytes = 0.0;
+      }
+    }
+  }
+  return FLCE_OK;
+}

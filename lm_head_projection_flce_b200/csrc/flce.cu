@@ -27,7 +27,8 @@
 // Cross entropy on given logits (chunked_ce page) is at the end of this file,
 // its row kernels in chunked_ce.cuh, and the forward without allocation.  The
 // operators around the head have their kernels and entry points in files of
-// their own, included last: layer_norm.cuh, mxfp4.cuh and mxfp4_gemm.cuh.
+// their own, included last: layer_norm.cuh, mxfp4.cuh, mxfp4_gemm.cuh
+// and beam.cuh.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -357,14 +358,16 @@ static int device_info(DeviceInfo** out) {
 enum KernelFamily {
   KF_CAST = 0, KF_ZERO, KF_GEMM_FWD, KF_MERGE, KF_FINAL, KF_BWD_PREP, KF_GEMM_GRAD, KF_GEMM_DW,
   KF_GEMM_DH, KF_SELFTEST_GEMM, KF_SELFTEST_WAIT, KF_GEMM_BWD, KF_CE_FWD, KF_CE_BWD, KF_LN_FWD,
-  KF_LN_BWD, KF_LN_REDUCE, KF_MX_QUANT, KF_MX_DEQUANT, KF_MX_GEMM, KF_COUNT
+  KF_LN_BWD, KF_LN_REDUCE, KF_MX_QUANT, KF_MX_DEQUANT, KF_MX_GEMM,
+  KF_BEAM_PART, KF_BEAM_MERGE, KF_BEAM_REORDER, KF_COUNT
 };
 static const char* const kFamilyNames[KF_COUNT] = {
     "cast_f32_bf16", "zero_rows",     "gemm_fwd_lse", "lse_merge",
     "loss_finalize", "bwd_prep",      "gemm_bwd_grad", "gemm_bwd_dw",
     "gemm_bwd_dh",   "selftest_gemm", "selftest_wait", "gemm_bwd_fused",
     "ce_logits_fwd", "ce_logits_bwd", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_reduce",
-    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm"};
+    "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_gemm", "beam_partials", "beam_merge",
+    "beam_reorder"};
 
 struct ProfRecord {
   int family;
@@ -800,6 +803,7 @@ extern "C" const char* flce_status_string(int status) {
     case FLCE_ERR_UNSUPPORTED: return "unsupported device or size (needs sm_100)";
     case FLCE_ERR_CUDA: return "CUDA runtime error";
     case FLCE_ERR_BAD_LABEL: return "label outside [0, unpadded_vocab) that is not ignore_index";
+    case FLCE_ERR_BAD_INDEX: return "parent beam outside [0, beams)";
     case FLCE_ERR_TIMEOUT: return "a pipeline wait timed out";
     default: return "unknown status";
   }
@@ -1131,6 +1135,7 @@ extern "C" int flce_get_error(flce_stream_t stream) {
     return FLCE_ERR_CUDA;
   if (host & kDevErrTimeout) return FLCE_ERR_TIMEOUT;
   if (host & kDevErrBadLabel) return FLCE_ERR_BAD_LABEL;
+  if (host & kDevErrBadIndex) return FLCE_ERR_BAD_INDEX;
   return FLCE_OK;
 }
 
@@ -1503,3 +1508,4 @@ extern "C" int flce_ce_backward(const void* logits, int dtype, const int64_t* la
 #include "layer_norm.cuh"
 #include "mxfp4.cuh"
 #include "mxfp4_gemm.cuh"
+#include "beam.cuh"

@@ -28,6 +28,7 @@ constexpr uint32_t kMnBlockBytes = 64 * kBK * 2;  // one 64-wide MN block x 64 K
 
 constexpr unsigned kDevErrBadLabel = 1u;
 constexpr unsigned kDevErrTimeout = 2u;
+constexpr unsigned kDevErrBadIndex = 4u;
 
 // Linear tile index -> (m tile, n tile).  Tiles are taken in groups of `group`
 // m-tiles (n_fast == 0) or n-tiles (n_fast == 1); inside a group the grouped

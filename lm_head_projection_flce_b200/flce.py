@@ -11,6 +11,7 @@ Entry points mirror include/flce.h:
   fused_linear_cross_entropy(...)                  autograd-aware convenience
   layer_norm(...)                                  the final norm, autograd-aware
   mxfp4_quantize(...), mxfp4_logits(...)           the head in 4 bits and its product
+  beam_select(...), beam_reorder(...)              beam search behind the head
 with the options of the NeMo-AutoModel loss pages
 ("nemo_automodel.components.loss.linear_ce", FusedLinearCrossEntropy:
 ignore_index=-100, logit_softcapping=0, reduction='sum', num_label_tokens;
@@ -33,9 +34,10 @@ LIB_PATH = _build.LIB_PATH
 FLCE_OK = 0
 FLCE_ERR_BAD_LABEL = 5
 FLCE_ERR_TIMEOUT = 6
+FLCE_ERR_BAD_INDEX = 7
 STATUS = {0: "FLCE_OK", 1: "FLCE_ERR_INVALID_ARG", 2: "FLCE_ERR_WORKSPACE",
           3: "FLCE_ERR_UNSUPPORTED", 4: "FLCE_ERR_CUDA", 5: "FLCE_ERR_BAD_LABEL",
-          6: "FLCE_ERR_TIMEOUT"}
+          6: "FLCE_ERR_TIMEOUT", 7: "FLCE_ERR_BAD_INDEX"}
 REDUCTIONS = {"sum": 0, "mean": 1, "none": 2}
 FLCE_BWD_HEAD_COPY_VALID = 1
 FLCE_FUSED_HEAD_CAST = 2
@@ -97,6 +99,11 @@ SIGNATURES = {
     "flce_mxfp4_logits": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_i64,
                                    _c_i64, ctypes.c_float, _c_ptr, _c_int, _c_i64, _c_ptr, _c_size,
                                    _c_ptr]),
+    "flce_beam_select_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64]),
+    "flce_beam_select": (_c_int, [_c_ptr, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr,
+                                  _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_size,
+                                  _c_ptr]),
+    "flce_beam_reorder": (_c_int, [_c_ptr, _c_i64, _c_ptr, _c_i64, _c_i64, _c_ptr]),
     "flce_launch_count": (ctypes.c_ulonglong, []),
     "flce_profile_start": (_c_int, []),
     "flce_profile_stop": (_c_int, [_c_ptr, _c_int, ctypes.POINTER(_c_int)]),
@@ -107,6 +114,14 @@ class KernelStat(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int64),
                 ("total_ms", ctypes.c_double), ("flops", ctypes.c_double),
                 ("bytes", ctypes.c_double)]
+
+
+class BeamState(ctypes.Structure):
+    _fields_ = [("src", _c_ptr), ("dst", _c_ptr),
+                ("src_batch_stride", _c_i64), ("src_beam_stride", _c_i64),
+                ("dst_batch_stride", _c_i64), ("dst_beam_stride", _c_i64),
+                ("outer", _c_i64), ("outer_stride", _c_i64), ("inner", _c_i64)]
+
 
 _LIB = None
 
@@ -861,3 +876,118 @@ def mxfp4_logits(hidden, head: Mxfp4, *, softcap: float = 0.0, unpadded_vocab: i
                                    _stream_handle(dev, stream))
     _check("flce_mxfp4_logits", st)
     return logits
+
+
+# ---------------------------------------------------------------- beam search
+
+def beam_select(logits, scores, *, num_select: int | None = None, finished=None,
+                eos_token: int | None = None, unpadded_vocab: int | None = None,
+                workspace: torch.Tensor | None = None, stream=None):
+    """The ``num_select`` (default: as many as beams) best continuations of each item.
+
+    ``logits`` [B, K, V'] (bf16 or fp32; the first ``unpadded_vocab`` of V' count),
+    ``scores`` FP32 [B, K] cumulative log-probabilities; a candidate's score is
+    ``scores + log_softmax(logits)``.  A beam whose score is not finite has no
+    candidates.  ``finished`` [B, K] (bool or uint8, with ``eos_token``): such a beam
+    continues with ``eos_token`` alone, its score unchanged.  Returns ``(scores FP32,
+    parents int64, tokens int64)``, each [B, num_select], best first, ties to the lowest
+    ``parent * V + token``; where too few candidates are above -inf, the lowest unused
+    ones with score -inf.
+    """
+    lib = load_library()
+    _cuda_tensor(logits, W_DTYPES, None, "logits")
+    if logits.dim() != 3 or 0 in logits.shape[1:]:
+        raise ValueError("logits must be [batch, beams, vocab]")
+    b, k, vp = logits.shape
+    v = vp if unpadded_vocab is None or unpadded_vocab <= 0 else int(unpadded_vocab)
+    if v > vp:
+        raise ValueError("unpadded_vocab exceeds the logits' vocabulary")
+    dev = logits.device
+    _cuda_tensor(scores, (torch.float32,), dev, "scores")
+    if scores.shape != (b, k) or not scores.is_contiguous():
+        raise ValueError("scores must be a contiguous [batch, beams] tensor")
+    if (finished is None) != (eos_token is None):
+        raise ValueError("finished and eos_token go together")
+    m = k if num_select is None else int(num_select)
+    rows, ld = _rows(logits.detach(), vp, "logits")
+    with _on(dev, stream):
+        done = None
+        if finished is not None:
+            _cuda_tensor(finished, (torch.bool, torch.uint8), dev, "finished")
+            if finished.shape != (b, k) or not finished.is_contiguous():
+                raise ValueError("finished must be a contiguous [batch, beams] tensor")
+            done = finished.view(torch.uint8)
+        out = torch.empty(b, m, dtype=torch.float32, device=dev)
+        parents = torch.empty(b, m, dtype=torch.int64, device=dev)
+        tokens = torch.empty(b, m, dtype=torch.int64, device=dev)
+        ws, ws_bytes = _workspace(
+            workspace, int(lib.flce_beam_select_workspace_size(b, k, v, m)), dev)
+        st = lib.flce_beam_select(_ptr(rows), W_DTYPES[logits.dtype], b, k, v, ld, _ptr(scores),
+                                  _ptr(done), -1 if eos_token is None else int(eos_token), m,
+                                  _ptr(out), _ptr(parents), _ptr(tokens), _ptr(ws), ws_bytes,
+                                  _stream_handle(dev, stream))
+    _check("flce_beam_select", st)
+    return out, parents, tokens
+
+
+def beam_reorder(states, parents, *, length: int | None = None, length_dim: int = 2, out=None,
+                 stream=None):
+    """``state[b, k] <- state[b, parents[b, k]]`` for one state or a list of them.
+
+    Each state is [B, K, ...], any dtype, contiguous behind the first two dimensions.
+    With ``length`` only the first ``length`` positions along ``length_dim`` follow (a
+    cache filled so far); the others are left as they were.  Without ``out`` the
+    states are reordered in place, with no scratch memory; with ``out`` (the same
+    structure, not overlapping the states) they are gathered into it.  ``parents``
+    int64 [B, K]; entries outside [0, K) keep the beam's own state and raise
+    FLCE_ERR_BAD_INDEX (``get_error``).  Returns what was written.
+    """
+    lib = load_library()
+    single = isinstance(states, torch.Tensor)
+    srcs = [states] if single else list(states)
+    dsts = srcs if out is None else ([out] if isinstance(out, torch.Tensor) else list(out))
+    if len(dsts) != len(srcs):
+        raise ValueError("out must have as many tensors as states")
+    _cuda_tensor(parents, (torch.int64,), None, "parents")
+    if parents.dim() != 2 or not parents.is_contiguous():
+        raise ValueError("parents must be a contiguous int64 [batch, beams] tensor")
+    b, k = parents.shape
+    dev = parents.device
+    arr = (BeamState * max(len(srcs), 1))()
+    for entry, src, dst in zip(arr, srcs, dsts):
+        for t in (src, dst):
+            _cuda_tensor(t, (src.dtype,), dev, "states")
+            if t.dim() < 2 or t.shape != src.shape or t.shape[:2] != (b, k):
+                raise ValueError("states must be [batch, beams, ...]; out must have their shapes")
+            if t.numel() and not t[0, 0].is_contiguous():
+                raise ValueError("states must be contiguous behind [batch, beams]")
+        if any(n > 1 and s == 0 for n, s in zip(dst.shape[:2], dst.stride()[:2])):
+            raise ValueError("a state's beams must not share memory")
+        if out is not None and dst.data_ptr() == src.data_ptr() and src.numel():
+            raise ValueError("out must not overlap the states; leave it out to reorder in place")
+        e = src.element_size()
+        outer, outer_stride, inner = 1, 0, e
+        for n in src.shape[2:]:
+            inner *= n
+        if length is not None:
+            if not 2 <= length_dim < src.dim() or not 0 <= length <= src.shape[length_dim]:
+                raise ValueError("length must lie within the states' length_dim")
+            for n in src.shape[2:length_dim]:
+                outer *= n
+            outer_stride = e
+            for n in src.shape[length_dim:]:
+                outer_stride *= n
+            inner = outer_stride // max(src.shape[length_dim], 1) * length
+        entry.src, entry.dst = src.data_ptr(), dst.data_ptr()
+        entry.src_batch_stride, entry.src_beam_stride = src.stride(0) * e, src.stride(1) * e
+        entry.dst_batch_stride, entry.dst_beam_stride = dst.stride(0) * e, dst.stride(1) * e
+        entry.outer, entry.outer_stride, entry.inner = outer, outer_stride, inner
+        if outer * inner == 0 or b == 0:  # nothing to move; the pointer may be null
+            entry.src = entry.dst = parents.data_ptr() or 1
+            entry.outer = 0
+    live = [e for e in arr[:len(srcs)] if e.outer]
+    with _on(dev, stream):
+        st = lib.flce_beam_reorder((BeamState * max(len(live), 1))(*live), len(live),
+                                   _ptr(parents), b, max(k, 1), _stream_handle(dev, stream))
+    _check("flce_beam_reorder", st)
+    return dsts[0] if single else dsts

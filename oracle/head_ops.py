@@ -1,5 +1,6 @@
 """FP64 definitions of the operators around the LM head (test infrastructure):
-layer norm with its gradients, MXFP4 quantisation and its product.  numpy only; shares no code with the CUDA path."""
+layer norm with its gradients, MXFP4 quantisation and its product, beam
+selection.  numpy only; shares no code with the CUDA path."""
 from __future__ import annotations
 
 import numpy as np
@@ -66,3 +67,26 @@ def mxfp4_logits(hidden, weight, softcap=0.0):
     a, w = mxfp4(hidden)[2], mxfp4(weight)[2]
     z = a @ w.T
     return (softcap * np.tanh(z / softcap) if softcap > 0 else z), np.abs(a) @ np.abs(w).T
+
+
+def beam_select(logits, scores, m, finished=None, eos=None):
+    """(scores, parents, tokens) [B, m] of the m best continuations."""
+    z, s = np.asarray(logits, np.float64), np.asarray(scores, np.float64)
+    b, k, v = z.shape
+    out = np.zeros((b, m)), np.zeros((b, m), np.int64), np.zeros((b, m), np.int64)
+    for i in range(b):
+        total = np.full((k, v), -np.inf)
+        for j in range(k):
+            if not np.isfinite(s[i, j]):
+                continue
+            if finished is not None and finished[i, j]:
+                total[j, eos] = s[i, j]
+                continue
+            with np.errstate(invalid="ignore", divide="ignore"):
+                top = z[i, j].max()
+                lse = top + np.log(np.exp(z[i, j] - top).sum())
+                t = s[i, j] + z[i, j] - lse
+            total[j] = np.where(np.isnan(t), -np.inf, t)
+        order = np.argsort(-total.ravel(), kind="stable")[:m]
+        out[0][i], out[1][i], out[2][i] = total.ravel()[order], order // v, order % v
+    return out
