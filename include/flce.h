@@ -271,7 +271,8 @@ int flce_ce_backward(const void* logits, int dtype, const int64_t* labels, const
  *                  whole elements (16-byte aligned rows are loaded fastest).
  *   weight, bias   [H] in w_dtype; either may be NULL (ones, zeros).
  *   eps            finite, >= 0.
- *   mean, rstd     FP32 [N], written by the forward, read by the backward.
+ *   mean, rstd     FP32 [N], written by the forward (either may be NULL there),
+ *                  read by the backward.
  *   dx, dweight, dbias (backward) each may be NULL: not computed.  dweight and
  *                  dbias are [H] in w_dtype, overwritten, summed over the rows
  *                  in FP32 in a fixed order (zeros when N = 0).

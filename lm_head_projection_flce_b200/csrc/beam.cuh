@@ -69,6 +69,57 @@ __device__ __forceinline__ void beam_load(const T* row, int64_t c, int64_t end, 
   }
 }
 
+// A bound from below on the select-th largest of the block's items, from one key
+// per thread, the largest of its items (0: none); keys may be equal.  The
+// select-th largest key is such a bound.  Ranking all keys against one another
+// would cost more than the pass over a short segment, so first every group of
+// 256 / P threads (P groups, a power of two >= select) gives its maximum: at
+// least `select` keys are no smaller than the least of those, and few keys are
+// larger; only they are ranked.  Returns 0 where fewer than `select` threads hold
+// a key.  Every thread of the block calls it.
+struct BeamBound {
+  uint64_t warp_min[kBeamThreads / 32];
+  uint64_t keys[kBeamThreads];
+  uint64_t bound;
+  int n;
+};
+__device__ __forceinline__ uint64_t beam_bound(uint64_t mine, int select, BeamBound& sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    sm.n = 0;
+    sm.bound = 0;
+  }
+  uint64_t top = mine;
+  for (int o = 1; o < 32 && o * 2 * select <= kBeamThreads; o <<= 1)
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = min(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) sm.warp_min[warp] = top;
+  __syncthreads();
+  top = sm.warp_min[0];
+#pragma unroll
+  for (int w = 1; w < kBeamThreads / 32; ++w) top = min(top, sm.warp_min[w]);
+  const bool in = mine != 0 && mine >= top;
+  const unsigned vote = __ballot_sync(0xffffffffu, in);
+  int at = 0;
+  if (lane == 0 && vote != 0) at = atomicAdd(&sm.n, __popc(vote));
+  at = __shfl_sync(0xffffffffu, at, 0) + __popc(vote & ((1u << lane) - 1u));
+  if (in) sm.keys[at] = mine;
+  __syncthreads();
+  if (in) {
+    const int n = sm.n;
+    int above = 0, same = 0;
+    for (int i = 0; i < n; ++i) {
+      const uint64_t k = sm.keys[i];
+      above += k > mine ? 1 : 0;
+      same += k == mine ? 1 : 0;
+    }
+    if (above < select && above + same >= select) sm.bound = mine;
+  }
+  __syncthreads();
+  return sm.bound;
+}
+
 struct BeamPartArgs {
   const void* logits;
   int64_t ld, vocab, segment;
@@ -89,10 +140,9 @@ __device__ __forceinline__ bool beam_is_live(float score) {
 template <typename T>
 __global__ void __launch_bounds__(kBeamThreads) beam_partials_kernel(const BeamPartArgs a) {
   constexpr int VN = 16 / int(sizeof(T));
-  __shared__ uint64_t keys[kBeamThreads];
+  __shared__ BeamBound bs;
   __shared__ uint64_t list[kBeamList];
   __shared__ int owners[kBeamMaxSelect];
-  __shared__ uint64_t bound_s;
   __shared__ int n_owners, n_list;
   __shared__ float red_m[kBeamThreads / 32];
   __shared__ double red_s[kBeamThreads / 32];
@@ -100,6 +150,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_partials_kernel(const BeamP
   const int64_t row = blockIdx.x / a.splits;
   const int part = int(blockIdx.x - row * a.splits);
   if (!beam_is_live(a.scores[row]) || (a.finished && a.finished[row])) return;
+  grid_launch_dependents();
   const T* z = static_cast<const T*>(a.logits) + row * a.ld;
   const bool vec = (reinterpret_cast<uintptr_t>(z) & 15) == 0;
   const int64_t begin = int64_t(part) * a.segment, end = min(a.vocab, begin + a.segment);
@@ -150,11 +201,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_partials_kernel(const BeamP
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
   if (lane == 0) red_m[warp] = bm;
-  keys[tid] = best > -INFINITY ? beam_key(best, best_at) : 0;
-  if (tid == 0) {
-    bound_s = 0;
-    n_owners = n_list = 0;
-  }
+  const uint64_t mine = best > -INFINITY ? beam_key(best, best_at) : 0;
+  if (tid == 0) n_owners = n_list = 0;
   __syncthreads();
   bm = red_m[0];
 #pragma unroll
@@ -163,14 +211,9 @@ __global__ void __launch_bounds__(kBeamThreads) beam_partials_kernel(const BeamP
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
   if (lane == 0) red_s[warp] = ds;
-
-  // The bound: the select-th largest of the threads' keys (0: fewer hold anything).
-  const uint64_t mine = keys[tid];
-  int rank = 0;
-  for (int i = 0; i < kBeamThreads; ++i) rank += keys[i] > mine ? 1 : 0;
-  if (mine != 0 && rank == a.select - 1) bound_s = mine;
-  __syncthreads();
-  const uint64_t bound = bound_s;
+  // Threads' keys are distinct (no two hold the same vector), so at most
+  // `select` threads reach the bound.
+  const uint64_t bound = beam_bound(mine, a.select, bs);
   if (mine != 0 && mine >= bound) owners[atomicAdd(&n_owners, 1)] = tid;  // at most `select`
   if (tid == 0) {
     double t = 0.0;
@@ -229,13 +272,13 @@ __global__ void __launch_bounds__(kBeamThreads) beam_partials_kernel(const BeamP
       if (key < last && key > top) top = key;
     });
     __syncthreads();
-    keys[tid] = top;
+    bs.keys[tid] = top;
     __syncthreads();
     for (int h = kBeamThreads / 2; h > 0; h >>= 1) {
-      if (tid < h) keys[tid] = max(keys[tid], keys[tid + h]);
+      if (tid < h) bs.keys[tid] = max(bs.keys[tid], bs.keys[tid + h]);
       __syncthreads();
     }
-    last = keys[0];  // never 0: more than kBeamList >= select elements qualify
+    last = bs.keys[0];  // never 0: more than kBeamList >= select elements qualify
     if (tid == 0) put(slot, last);
   }
 }
@@ -263,47 +306,54 @@ __device__ __forceinline__ uint64_t beam_order64(double x) {
 __device__ __forceinline__ double beam_value64(uint64_t o) {
   return __longlong_as_double(static_cast<long long>((o >> 63) ? (o & ~(uint64_t(1) << 63)) : ~o));
 }
-__device__ __forceinline__ bool beam_above(uint64_t ta, uint32_t ia, uint64_t tb, uint32_t ib) {
-  return ta > tb || (ta == tb && ia < ib);
-}
 
 // One block per batch item.
 __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMergeArgs a) {
   extern __shared__ uint64_t dyn[];
+  __shared__ BeamBound bs;
   __shared__ double lse[kBeamMaxBeams];
-  __shared__ uint64_t head_t[kBeamThreads];
-  __shared__ uint32_t head_i[kBeamThreads];
-  __shared__ uint64_t bound_t;
-  __shared__ uint32_t bound_i;
-  __shared__ int n_list, n_out;
+  __shared__ int n_list;
   __shared__ uint32_t chosen[kBeamMaxSelect];
+  constexpr int kAhead = 4;  // items per thread loaded before the sums are known
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per_beam = a.splits * a.select;
   const int items = a.beams * per_beam;
-  uint64_t* tot = dyn;                                          // [items]
-  uint32_t* idx = reinterpret_cast<uint32_t*>(tot + items);     // [items]
-  uint32_t* list = idx + items;                                 // [items]: positions above the bound
+  const uint32_t vocab = uint32_t(a.vocab);
+  uint64_t* tot = dyn;                                       // [items]
+  uint32_t* idx = reinterpret_cast<uint32_t*>(tot + items);  // [items]
+  uint32_t* list = idx + items;                              // [items]: positions above the bound
   const int64_t b = blockIdx.x;
   const float* scores = a.scores + b * a.beams;
   const uint8_t* finished = a.finished ? a.finished + b * a.beams : nullptr;
+  const int64_t at0 = b * items;
   grid_dependency_wait();
-  if (tid == 0) {
-    bound_t = 0;
-    bound_i = 0xffffffffu;
-    n_list = n_out = 0;
+  float az[kAhead];
+  int av[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int i = tid + u * kBeamThreads;
+    // dead and finished beams' entries were never written: loaded, not used
+    az[u] = i < items ? a.cand_z[at0 + i] : 0.0f;
+    av[u] = i < items ? a.cand_v[at0 + i] : -1;
   }
+  if (tid == 0) n_list = 0;
   const double ninf = -static_cast<double>(INFINITY);
   for (int k = warp; k < a.beams; k += kBeamThreads / 32) {
-    if (!beam_is_live(scores[k]) || (finished && finished[k])) continue;
     const int64_t at = (b * a.beams + k) * a.splits;
-    float m = -INFINITY;
-    for (int p = lane; p < a.splits; p += 32) m = fmaxf(m, a.part_m[at + p]);
+    float pm = lane < a.splits ? a.part_m[at + lane] : -INFINITY;
+    double ps = lane < a.splits ? a.part_s[at + lane] : 0.0;
+    if (!beam_is_live(scores[k]) || (finished && finished[k])) continue;
+    float m = pm;
+    for (int p = lane + 32; p < a.splits; p += 32) m = fmaxf(m, a.part_m[at + p]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // an all -inf segment's sum is 0, or NaN where it holds one
     double s = 0.0;
     for (int p = lane; p < a.splits; p += 32) {
-      const double ps = a.part_s[at + p];
-      const float pm = a.part_m[at + p];
+      if (p != lane) {
+        pm = a.part_m[at + p];
+        ps = a.part_s[at + p];
+      }
       s += pm == m || pm == -INFINITY ? ps : ps * exp(double(pm) - double(m));
     }
 #pragma unroll
@@ -312,63 +362,47 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
   }
   __syncthreads();
 
-  uint64_t ht = 0;
-  uint32_t hi = 0xffffffffu;
-  for (int i = tid; i < items; i += kBeamThreads) {
-    const int k = i / per_beam, j = i - k * per_beam;
+  uint64_t top = 0;
+  auto item = [&](int i, float z, int v) {
+    const int k = i / per_beam;
     double t = ninf;
-    uint32_t f = 0xffffffffu;
     const float s = scores[k];
     if (beam_is_live(s)) {
       if (finished && finished[k]) {
-        if (j == 0) {
-          t = double(s);
-          f = uint32_t(k * a.vocab + a.eos);
-        }
-      } else {
-        const int64_t at = (b * a.beams + k) * per_beam + j;
-        const int v = a.cand_v[at];
-        if (v >= 0) {
-          t = double(s) + double(a.cand_z[at]) - lse[k];
-          f = uint32_t(k * a.vocab + v);
-        }
+        v = int(a.eos);
+        if (i == k * per_beam) t = double(s);
+      } else if (v >= 0) {
+        t = double(s) + double(z) - lse[k];
       }
     }
-    const uint64_t o = f != 0xffffffffu && t > ninf ? beam_order64(t) : 0;  // NaN and -inf: none
+    const uint64_t o = t > ninf ? beam_order64(t) : 0;  // NaN and -inf: none
     tot[i] = o;
-    idx[i] = f;
-    if (o != 0 && beam_above(o, f, ht, hi)) {
-      ht = o;
-      hi = f;
-    }
-  }
-  head_t[tid] = ht;
-  head_i[tid] = hi;
-  __syncthreads();
-  if (ht != 0) {
-    int rank = 0;
-    for (int i = 0; i < kBeamThreads; ++i)
-      rank += head_t[i] != 0 && beam_above(head_t[i], head_i[i], ht, hi) ? 1 : 0;
-    if (rank == a.select - 1) {
-      bound_t = ht;
-      bound_i = hi;
-    }
-  }
-  __syncthreads();
+    idx[i] = uint32_t(k) * vocab + uint32_t(v);
+    top = max(top, o);
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (tid + u * kBeamThreads < items) item(tid + u * kBeamThreads, az[u], av[u]);
+  for (int i = tid + kAhead * kBeamThreads; i < items; i += kBeamThreads)
+    item(i, a.cand_z[at0 + i], a.cand_v[at0 + i]);
+  const uint64_t bound = beam_bound(top, a.select, bs);
   for (int i = tid; i < items; i += kBeamThreads)
-    if (tot[i] != 0 && !beam_above(bound_t, bound_i, tot[i], idx[i])) list[atomicAdd(&n_list, 1)] = i;
+    if (tot[i] != 0 && tot[i] >= bound) list[atomicAdd(&n_list, 1)] = i;
   __syncthreads();
   const int n = n_list;
   for (int i = tid; i < n; i += kBeamThreads) {
     const uint64_t t = tot[list[i]];
     const uint32_t f = idx[list[i]];
     int r = 0;
-    for (int j = 0; j < n; ++j) r += beam_above(tot[list[j]], idx[list[j]], t, f) ? 1 : 0;
+    for (int j = 0; j < n; ++j) {
+      const uint64_t tj = tot[list[j]];
+      r += tj > t || (tj == t && idx[list[j]] < f) ? 1 : 0;
+    }
     if (r < a.select) {
       const int64_t at = b * a.select + r;
       a.out_scores[at] = float(beam_value64(t));
-      a.parents[at] = int64_t(f / a.vocab);
-      a.tokens[at] = int64_t(f % a.vocab);
+      a.parents[at] = int64_t(f / vocab);
+      a.tokens[at] = int64_t(f % vocab);
       chosen[r] = f;
     }
   }
@@ -383,8 +417,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
         }
       const int64_t at = b * a.select + r;
       a.out_scores[at] = -INFINITY;
-      a.parents[at] = int64_t(f / a.vocab);
-      a.tokens[at] = int64_t(f % a.vocab);
+      a.parents[at] = int64_t(f / vocab);
+      a.tokens[at] = int64_t(f % vocab);
     }
   }
 }
@@ -558,8 +592,9 @@ extern "C" int flce_beam_select(const void* logits, int dtype, int64_t batch, in
                            kBeamMaxItems * 16) != cudaSuccess)
     return FLCE_ERR_CUDA;
   LaunchScope scope(KF_BEAM_MERGE, 0.0, double(rows) * p.splits * (12.0 + 8.0 * double(num_select)), cs);
-  beam_merge_kernel<<<unsigned(batch), kBeamThreads, smem, cs>>>(g);
-  return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
+  // Launched while the first kernel still runs; its blocks wait for that kernel's
+  // end (griddepcontrol.wait) before they read anything.
+  return launch_dependent(beam_merge_kernel, dim3(unsigned(batch)), dim3(kBeamThreads), smem, cs, g);
 }
 
 extern "C" int flce_beam_reorder(const flce_beam_state* states, int64_t count,

@@ -647,6 +647,25 @@ static int launch_group(const GemmProblem* probs, const CUtensorMap* maps_a,
   return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 
+// A launch that may begin before the previous kernel of the stream has ended
+// (programmatic dependent launch); the kernel waits for it itself.
+template <typename... KArgs, typename... Args>
+static int launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                            cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) return FLCE_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
+}
+
 static int launch_zero(void* p, size_t bytes, const DeviceInfo& dev, cudaStream_t st) {
   if (bytes == 0) return FLCE_OK;
   const int64_t n16 = int64_t(bytes / 16);

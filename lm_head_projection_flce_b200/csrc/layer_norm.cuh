@@ -146,7 +146,7 @@ struct LnArgs {
   float eps;
   void* y;
   int64_t ldy;
-  float* mean;
+  float* mean;  // either may be nullptr
   float* rstd;
 };
 
@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(ln_block(VN * NV, kWarpRow))
     }
     const float rstd = 1.0f / sqrtf(ln_row_sum<kWarpRow>(s, red, buf).x * inv_h + a.eps);
     if (t == 0) {
-      a.mean[r] = mean;
-      a.rstd[r] = rstd;
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
     }
     T* y = static_cast<T*>(a.y) + r * a.ldy;
 #pragma unroll
@@ -238,8 +238,8 @@ __global__ void __launch_bounds__(1024) ln_forward_long_kernel(const LnArgs a) {
     }
     const float rstd = 1.0f / sqrtf(ln_row_sum<false>(s, red, buf).x / float(a.h) + a.eps);
     if (threadIdx.x == 0) {
-      a.mean[r] = mean;
-      a.rstd[r] = rstd;
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
     }
     for (int64_t c = threadIdx.x; c < a.h; c += blockDim.x) {
       LnIo<T, 1>::load(x + c, v);
@@ -558,8 +558,8 @@ extern "C" int flce_layer_norm_forward(const void* x, int dtype, int64_t n, int6
   const int esz = dtype == FLCE_F32 ? 4 : 2, wsz = w_dtype == FLCE_F32 ? 4 : 2;
   if (!aligned(weight, wsz) || !aligned(bias, wsz)) return FLCE_ERR_INVALID_ARG;
   if (n == 0) return FLCE_OK;
-  if (x == nullptr || y == nullptr || mean == nullptr || rstd == nullptr || !aligned(x, esz) ||
-      !aligned(y, esz) || !aligned(mean, 4) || !aligned(rstd, 4))
+  if (x == nullptr || y == nullptr || !aligned(x, esz) || !aligned(y, esz) ||
+      !aligned(mean, 4) || !aligned(rstd, 4))
     return FLCE_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;
   const int st = device_info(&dev);

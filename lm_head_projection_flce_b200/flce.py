@@ -153,9 +153,21 @@ def _check(where: str, status: int) -> None:
         raise FlceError(where, status)
 
 
-def _stream_handle(device: torch.device, stream=None):
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+# The current stream's handle without building a torch.cuda.Stream around it
+# (several microseconds of a small call); newer or older builds of torch that
+# lack the function take the long way.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(device: torch.device, stream=None) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None and device.index is not None:
+        return _current_raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(device: torch.device, stream=None):
@@ -166,12 +178,13 @@ def _on(device: torch.device, stream=None):
             raise ValueError("stream must belong to the tensors' device")
         return torch.cuda.stream(stream)
     if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.device(device)
 
 
-def _ptr(t: torch.Tensor | None):
-    return ctypes.c_void_p(t.data_ptr() if t is not None and t.numel() > 0 else 0)
+def _ptr(t: torch.Tensor | None) -> int:
+    """Address for a c_void_p argument (0: none, or nothing in it)."""
+    return t.data_ptr() if t is not None and t.numel() > 0 else 0
 
 
 def _vocab(weight: torch.Tensor, unpadded_vocab: int | None) -> int:
@@ -606,21 +619,40 @@ def ce_backward(logits, labels, lse, grad_loss, *, mask=None, ignore_index: int 
 
 def _rows(t, h: int, name: str) -> tuple[torch.Tensor, int]:
     """`t` [..., h] as rows [N, h] of unit stride, and their distance in elements."""
-    rows = t.reshape(-1, h)
-    if h > 1 and rows.stride(1) != 1:
+    rows = t if t.dim() == 2 else t.reshape(-1, h)
+    n = rows.shape[0]
+    step, unit = rows.stride()
+    if unit != 1 and h > 1:
         raise ValueError(f"{name} rows must be contiguous")
-    if rows.shape[0] <= 1:
+    if n <= 1:
         return rows, h
-    if rows.stride(0) < h:
+    if step < h:
         raise ValueError(f"{name} rows must not overlap")
-    return rows, rows.stride(0)
+    return rows, step
 
 
 def _cuda_tensor(t, dtypes, dev, name: str) -> None:
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {tuple(dtypes)}")
-    if t.device.type != "cuda" or (dev is not None and t.device != dev):
+    if not t.is_cuda or (dev is not None and t.device != dev):
         raise ValueError("tensors must be on one CUDA device")
+
+
+def _result(t, like, shape, dtype, name: str) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one on `like`'s device."""
+    if t is None:
+        return like.new_empty(shape, dtype=dtype)
+    if t.shape != torch.Size(shape) or t.dtype != dtype or t.device != like.device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {like.device}")
+    return t
+
+
+def _result_rows(t, h: int, name: str) -> tuple[int, int]:
+    """Address and row distance of an output, which must be rows of one stride in place."""
+    rows, ld = _rows(t, h, name)
+    if rows is not t and rows.data_ptr() != t.data_ptr():
+        raise ValueError(f"{name}'s rows must have one stride")
+    return _ptr(rows), ld
 
 
 def _norm_params(weight, bias, h: int, dev, param_dtype=None) -> torch.dtype:
@@ -639,37 +671,43 @@ def _norm_params(weight, bias, h: int, dev, param_dtype=None) -> torch.dtype:
     return dtype
 
 
+def _norm_rows(x) -> tuple[torch.Tensor, int, int, int]:
+    _cuda_tensor(x, W_DTYPES, None, "x")
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x must be [..., hidden] with hidden >= 1")
+    h = x.shape[-1]
+    rows, ldx = _rows(x, h, "x")
+    return rows, rows.shape[0], h, ldx
+
+
 def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5,
                        y: torch.Tensor | None = None, mean: torch.Tensor | None = None,
-                       rstd: torch.Tensor | None = None, stream=None):
+                       rstd: torch.Tensor | None = None, stats: bool = True, stream=None):
     """Layer norm over the last dimension (flce_layer_norm_forward).
 
     ``x`` [..., H] bf16 or fp32 (rows contiguous, any row stride); ``weight`` and
     ``bias`` [H] bf16 or fp32, either may be None.  Returns ``(y, mean, rstd)``:
-    y in x's dtype and shape, the row statistics FP32 [N] for the backward.
+    y in x's dtype and shape, the row statistics FP32 [N] for the backward
+    (``stats=False``: None for statistics that were not given, and not written).
     """
-    lib = load_library()
-    _cuda_tensor(x, W_DTYPES, None, "x")
-    if x.dim() == 0 or x.shape[-1] == 0:
-        raise ValueError("x must be [..., hidden] with hidden >= 1")
-    dev, h = x.device, x.shape[-1]
+    lib = _LIB or load_library()
+    rows, n, h, ldx = _norm_rows(x)
+    dev = x.device
     w_dtype = _norm_params(weight, bias, h, dev)
-    rows, ldx = _rows(x, h, "x")
-    n = rows.shape[0]
     with _on(dev, stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else y
-        if y.shape != x.shape or y.dtype != x.dtype or y.device != dev:
-            raise ValueError("y must have x's shape, dtype and device")
-        out, ldy = _rows(y, h, "y")
-        if out.data_ptr() != y.data_ptr():
-            raise ValueError("y's rows must have one stride")
-        mean = (torch.empty(n, dtype=torch.float32, device=dev) if mean is None
-                else _buffer(mean, n, torch.float32, dev, "mean"))
-        rstd = (torch.empty(n, dtype=torch.float32, device=dev) if rstd is None
-                else _buffer(rstd, n, torch.float32, dev, "rstd"))
+        y = _result(y, x, x.shape, x.dtype, "y")
+        out, ldy = _result_rows(y, h, "y")
+        if mean is not None:
+            _buffer(mean, n, torch.float32, dev, "mean")
+        elif stats:
+            mean = x.new_empty(n, dtype=torch.float32)
+        if rstd is not None:
+            _buffer(rstd, n, torch.float32, dev, "rstd")
+        elif stats:
+            rstd = x.new_empty(n, dtype=torch.float32)
         st = lib.flce_layer_norm_forward(_ptr(rows), W_DTYPES[x.dtype], n, h, ldx, _ptr(weight),
-                                         _ptr(bias), W_DTYPES[w_dtype], float(eps), _ptr(out), ldy,
-                                         _ptr(mean), _ptr(rstd), _stream_handle(dev, stream))
+                                         _ptr(bias), W_DTYPES[w_dtype], eps, out, ldy, _ptr(mean),
+                                         _ptr(rstd), _stream_handle(dev, stream))
     _check("flce_layer_norm_forward", st)
     return y, mean, rstd
 
@@ -681,52 +719,45 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, want=("dx", "dweight"
     """Gradients ``(dx, dweight, dbias)`` of layer_norm_forward; None for what is
     not in ``want``.  ``dx`` has x's dtype, the other two the weight's
     (``param_dtype`` where there is no weight; FP32 by default)."""
-    lib = load_library()
-    _cuda_tensor(x, W_DTYPES, None, "x")
-    if x.dim() == 0 or x.shape[-1] == 0:
-        raise ValueError("x must be [..., hidden] with hidden >= 1")
+    lib = _LIB or load_library()
+    rows, n, h, ldx = _norm_rows(x)
     unknown = set(want) - {"dx", "dweight", "dbias"}
     if unknown:
         raise ValueError(f"unknown gradients {sorted(unknown)}")
-    dev, h = x.device, x.shape[-1]
+    dev = x.device
     _cuda_tensor(dy, (x.dtype,), dev, "dy")
     if dy.shape != x.shape:
         raise ValueError("dy must have x's shape")
     w_dtype = _norm_params(weight, None, h, dev, param_dtype)
-    rows, ldx = _rows(x, h, "x")
     grads, lddy = _rows(dy, h, "dy")
-    n = rows.shape[0]
-    mean = _buffer(mean, n, torch.float32, dev, "mean")
-    rstd = _buffer(rstd, n, torch.float32, dev, "rstd")
+    _buffer(mean, n, torch.float32, dev, "mean")
+    _buffer(rstd, n, torch.float32, dev, "rstd")
     with _on(dev, stream):
-        lddx = h
-        out = None
+        out, lddx = 0, h
         if "dx" in want:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
-            if dx.shape != x.shape or dx.dtype != x.dtype or dx.device != dev:
-                raise ValueError("dx must have x's shape, dtype and device")
-            out, lddx = _rows(dx, h, "dx")
-            if out.data_ptr() != dx.data_ptr():
-                raise ValueError("dx's rows must have one stride")
+            dx = _result(dx, x, x.shape, x.dtype, "dx")
+            out, lddx = _result_rows(dx, h, "dx")
         else:
             dx = None
-        params = []
-        for name, given in (("dweight", dweight), ("dbias", dbias)):
-            if name not in want:
-                params.append(None)
-            else:
-                params.append(torch.empty(h, dtype=w_dtype, device=dev) if given is None
-                              else _buffer(given, h, w_dtype, dev, name))
+        if "dweight" in want:
+            dweight = (x.new_empty(h, dtype=w_dtype) if dweight is None
+                       else _buffer(dweight, h, w_dtype, dev, "dweight"))
+        else:
+            dweight = None
+        if "dbias" in want:
+            dbias = (x.new_empty(h, dtype=w_dtype) if dbias is None
+                     else _buffer(dbias, h, w_dtype, dev, "dbias"))
+        else:
+            dbias = None
         ws, ws_bytes = None, 0
-        if params[0] is not None or params[1] is not None:
-            ws, ws_bytes = _workspace(workspace, int(lib.flce_layer_norm_workspace_size(n, h)), dev)
+        if dweight is not None or dbias is not None:
+            ws, ws_bytes = _workspace(workspace, lib.flce_layer_norm_workspace_size(n, h), dev)
         st = lib.flce_layer_norm_backward(_ptr(grads), lddy, _ptr(rows), W_DTYPES[x.dtype], n, h,
                                           ldx, _ptr(weight), W_DTYPES[w_dtype], _ptr(mean),
-                                          _ptr(rstd), _ptr(out), lddx, _ptr(params[0]),
-                                          _ptr(params[1]), _ptr(ws), ws_bytes,
-                                          _stream_handle(dev, stream))
+                                          _ptr(rstd), out, lddx, _ptr(dweight), _ptr(dbias),
+                                          _ptr(ws), ws_bytes, _stream_handle(dev, stream))
     _check("flce_layer_norm_backward", st)
-    return dx, params[0], params[1]
+    return dx, dweight, dbias
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -751,6 +782,10 @@ class _LayerNorm(torch.autograd.Function):
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
     """Autograd-aware layer norm over the last dimension: ``(x - mean) * rstd *
     weight + bias``; gradients flow to ``x``, ``weight`` and ``bias``."""
+    if not (torch.is_grad_enabled() and (x.requires_grad
+                                         or (weight is not None and weight.requires_grad)
+                                         or (bias is not None and bias.requires_grad))):
+        return layer_norm_forward(x, weight, bias, eps=eps, stats=False)[0]
     return _LayerNorm.apply(x, weight, bias, eps)
 
 
@@ -785,7 +820,7 @@ class Mxfp4:
 
 
 def _mxfp4_operand(q: Mxfp4, name: str) -> None:
-    lib = load_library()
+    lib = _LIB or load_library()
     if not isinstance(q, Mxfp4):
         raise TypeError(f"{name} must be an Mxfp4 (from mxfp4_quantize)")
     _buffer(q.codes, int(lib.flce_mxfp4_codes_size(q.rows, q.cols)), torch.uint8, q.device,
@@ -801,11 +836,11 @@ def mxfp4_quantize(x, *, out: Mxfp4 | None = None, stream=None) -> Mxfp4:
     power of two 2^(floor(log2 max|x|) - 2), elements rounded to the nearest E2M1
     number (ties to even, saturating).  ``out`` is overwritten if given.  No gradient
     flows through it."""
-    lib = load_library()
+    lib = _LIB or load_library()
     _cuda_tensor(x, W_DTYPES, None, "x")
     if x.dim() != 2 or x.shape[1] == 0:
         raise ValueError("x must be [rows, cols] with cols >= 1")
-    rows, ld = _rows(x.detach(), x.shape[1], "x")
+    rows, ld = _rows(x, x.shape[1], "x")
     n, h = x.shape
     dev = x.device
     with _on(dev, stream):
@@ -827,17 +862,15 @@ def mxfp4_quantize(x, *, out: Mxfp4 | None = None, stream=None) -> Mxfp4:
 def mxfp4_dequantize(q: Mxfp4, dtype: torch.dtype = torch.bfloat16, *,
                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The numbers ``q`` stands for, [rows, cols] in bf16 or fp32 (both hold them exactly)."""
-    lib = load_library()
+    lib = _LIB or load_library()
     _mxfp4_operand(q, "q")
     if dtype not in W_DTYPES:
         raise TypeError("dtype must be bf16 or fp32")
     dev = q.device
     with _on(dev, stream):
-        out = torch.empty(q.rows, q.cols, dtype=dtype, device=dev) if out is None else out
-        if tuple(out.shape) != q.shape or out.dtype != dtype or out.device != dev:
-            raise ValueError("out must be [rows, cols] of dtype on q's device")
-        rows, ld = _rows(out, q.cols, "out")
-        st = lib.flce_mxfp4_dequantize(_ptr(q.codes), _ptr(q.scales), q.rows, q.cols, _ptr(rows),
+        out = _result(out, q.codes, q.shape, dtype, "out")
+        rows, ld = _result_rows(out, q.cols, "out")
+        st = lib.flce_mxfp4_dequantize(_ptr(q.codes), _ptr(q.scales), q.rows, q.cols, rows,
                                        W_DTYPES[dtype], ld, _stream_handle(dev, stream))
     _check("flce_mxfp4_dequantize", st)
     return out
@@ -850,7 +883,7 @@ def mxfp4_logits(hidden, head: Mxfp4, *, softcap: float = 0.0, unpadded_vocab: i
     [..., V] in ``dtype``: the hidden states [..., H] (bf16 or fp32) are put into MXFP4
     in the workspace, the product runs on 4-bit tensor cores with FP32 accumulation.
     For serving and evaluation: no gradient flows through it."""
-    lib = load_library()
+    lib = _LIB or load_library()
     _mxfp4_operand(head, "head")
     _cuda_tensor(hidden, W_DTYPES, head.device, "hidden")
     if dtype not in W_DTYPES:
@@ -859,19 +892,15 @@ def mxfp4_logits(hidden, head: Mxfp4, *, softcap: float = 0.0, unpadded_vocab: i
         raise ValueError("hidden must be [..., H] with the head's H")
     dev, h, vp = hidden.device, head.cols, head.rows
     v = vp if unpadded_vocab is None or unpadded_vocab <= 0 else int(unpadded_vocab)
-    rows, ldh = _rows(hidden.detach(), h, "hidden")
+    rows, ldh = _rows(hidden, h, "hidden")
     n = rows.shape[0]
     shape = (*hidden.shape[:-1], v)
     with _on(dev, stream):
-        logits = torch.empty(shape, dtype=dtype, device=dev) if logits is None else logits
-        if tuple(logits.shape) != shape or logits.dtype != dtype or logits.device != dev:
-            raise ValueError("logits must be [..., V] of dtype on hidden's device")
-        out, ldo = _rows(logits, v, "logits")
-        if out.data_ptr() != logits.data_ptr():
-            raise ValueError("the logits' rows must have one stride")
-        ws, ws_bytes = _workspace(workspace, int(lib.flce_mxfp4_logits_workspace_size(n, h)), dev)
+        logits = _result(logits, hidden, shape, dtype, "logits")
+        out, ldo = _result_rows(logits, v, "logits")
+        ws, ws_bytes = _workspace(workspace, lib.flce_mxfp4_logits_workspace_size(n, h), dev)
         st = lib.flce_mxfp4_logits(_ptr(rows), W_DTYPES[hidden.dtype], n, h, ldh, _ptr(head.codes),
-                                   _ptr(head.scales), vp, v, float(softcap), _ptr(out),
+                                   _ptr(head.scales), vp, v, softcap, out,
                                    W_DTYPES[dtype], ldo, _ptr(ws), ws_bytes,
                                    _stream_handle(dev, stream))
     _check("flce_mxfp4_logits", st)
@@ -894,7 +923,7 @@ def beam_select(logits, scores, *, num_select: int | None = None, finished=None,
     ``parent * V + token``; where too few candidates are above -inf, the lowest unused
     ones with score -inf.
     """
-    lib = load_library()
+    lib = _LIB or load_library()
     _cuda_tensor(logits, W_DTYPES, None, "logits")
     if logits.dim() != 3 or 0 in logits.shape[1:]:
         raise ValueError("logits must be [batch, beams, vocab]")
@@ -909,7 +938,7 @@ def beam_select(logits, scores, *, num_select: int | None = None, finished=None,
     if (finished is None) != (eos_token is None):
         raise ValueError("finished and eos_token go together")
     m = k if num_select is None else int(num_select)
-    rows, ld = _rows(logits.detach(), vp, "logits")
+    rows, ld = _rows(logits, vp, "logits")
     with _on(dev, stream):
         done = None
         if finished is not None:
@@ -917,11 +946,10 @@ def beam_select(logits, scores, *, num_select: int | None = None, finished=None,
             if finished.shape != (b, k) or not finished.is_contiguous():
                 raise ValueError("finished must be a contiguous [batch, beams] tensor")
             done = finished.view(torch.uint8)
-        out = torch.empty(b, m, dtype=torch.float32, device=dev)
-        parents = torch.empty(b, m, dtype=torch.int64, device=dev)
-        tokens = torch.empty(b, m, dtype=torch.int64, device=dev)
-        ws, ws_bytes = _workspace(
-            workspace, int(lib.flce_beam_select_workspace_size(b, k, v, m)), dev)
+        out = scores.new_empty((b, m))
+        parents = scores.new_empty((b, m), dtype=torch.int64)
+        tokens = scores.new_empty((b, m), dtype=torch.int64)
+        ws, ws_bytes = _workspace(workspace, lib.flce_beam_select_workspace_size(b, k, v, m), dev)
         st = lib.flce_beam_select(_ptr(rows), W_DTYPES[logits.dtype], b, k, v, ld, _ptr(scores),
                                   _ptr(done), -1 if eos_token is None else int(eos_token), m,
                                   _ptr(out), _ptr(parents), _ptr(tokens), _ptr(ws), ws_bytes,
@@ -942,7 +970,7 @@ def beam_reorder(states, parents, *, length: int | None = None, length_dim: int 
     int64 [B, K]; entries outside [0, K) keep the beam's own state and raise
     FLCE_ERR_BAD_INDEX (``get_error``).  Returns what was written.
     """
-    lib = load_library()
+    lib = _LIB or load_library()
     single = isinstance(states, torch.Tensor)
     srcs = [states] if single else list(states)
     dsts = srcs if out is None else ([out] if isinstance(out, torch.Tensor) else list(out))

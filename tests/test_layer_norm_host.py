@@ -55,7 +55,7 @@ def _bwd(lib, **kw):
 
 
 @pytest.mark.parametrize("bad", [dict(n=-1), dict(h=0), dict(ldx=63), dict(dtype=2), dict(w_dtype=2),
-                                 dict(x=0), dict(x=FAKE + 1), dict(w=FAKE + 1), dict(mean=0),
+                                 dict(x=0), dict(x=FAKE + 1), dict(w=FAKE + 1),
                                  dict(rstd=FAKE + 2)])
 def test_bad_arguments_of_both(lib, bad):
     assert _fwd(lib, **bad) == 1
@@ -69,7 +69,7 @@ def test_bad_arguments_forward(lib, bad):
 
 
 @pytest.mark.parametrize("bad", [dict(dy=0), dict(lddy=1), dict(lddx=1), dict(dx=FAKE + 1),
-                                 dict(dw=FAKE + 1), dict(db=FAKE + 1)])
+                                 dict(dw=FAKE + 1), dict(db=FAKE + 1), dict(mean=0), dict(rstd=0)])
 def test_bad_arguments_backward(lib, bad):
     assert _bwd(lib, **bad) == 1
 
