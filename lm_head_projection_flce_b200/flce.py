@@ -981,41 +981,42 @@ def beam_reorder(states, parents, *, length: int | None = None, length_dim: int 
         raise ValueError("parents must be a contiguous int64 [batch, beams] tensor")
     b, k = parents.shape
     dev = parents.device
-    arr = (BeamState * max(len(srcs), 1))()
-    for entry, src, dst in zip(arr, srcs, dsts):
-        for t in (src, dst):
-            _cuda_tensor(t, (src.dtype,), dev, "states")
-            if t.dim() < 2 or t.shape != src.shape or t.shape[:2] != (b, k):
-                raise ValueError("states must be [batch, beams, ...]; out must have their shapes")
-            if t.numel() and not t[0, 0].is_contiguous():
-                raise ValueError("states must be contiguous behind [batch, beams]")
-        if any(n > 1 and s == 0 for n, s in zip(dst.shape[:2], dst.stride()[:2])):
-            raise ValueError("a state's beams must not share memory")
-        if out is not None and dst.data_ptr() == src.data_ptr() and src.numel():
-            raise ValueError("out must not overlap the states; leave it out to reorder in place")
+    live = []
+    for src, dst in zip(srcs, dsts):
+        shape, stride = src.shape, src.stride()
+        _cuda_tensor(src, (src.dtype,), dev, "states")
+        if len(shape) < 2 or shape[0] != b or shape[1] != k:
+            raise ValueError("states must be [batch, beams, ...]")
+        if dst is not src:
+            _cuda_tensor(dst, (src.dtype,), dev, "out")
+            if dst.shape != shape:
+                raise ValueError("out must have the states' shapes")
         e = src.element_size()
-        outer, outer_stride, inner = 1, 0, e
-        for n in src.shape[2:]:
+        inner, outer, outer_stride = e, 1, 0
+        into = dst.stride()
+        for i in range(len(shape) - 1, 1, -1):
+            n = shape[i]
+            if n > 1 and (stride[i] * e != inner or into[i] * e != inner):
+                raise ValueError("states must be contiguous behind [batch, beams]")
             inner *= n
+        if (b > 1 and into[0] == 0) or (k > 1 and into[1] == 0):
+            raise ValueError("a state's beams must not share memory")
         if length is not None:
-            if not 2 <= length_dim < src.dim() or not 0 <= length <= src.shape[length_dim]:
+            if not 2 <= length_dim < len(shape) or not 0 <= length <= shape[length_dim]:
                 raise ValueError("length must lie within the states' length_dim")
-            for n in src.shape[2:length_dim]:
+            for n in shape[2:length_dim]:
                 outer *= n
-            outer_stride = e
-            for n in src.shape[length_dim:]:
-                outer_stride *= n
-            inner = outer_stride // max(src.shape[length_dim], 1) * length
-        entry.src, entry.dst = src.data_ptr(), dst.data_ptr()
-        entry.src_batch_stride, entry.src_beam_stride = src.stride(0) * e, src.stride(1) * e
-        entry.dst_batch_stride, entry.dst_beam_stride = dst.stride(0) * e, dst.stride(1) * e
-        entry.outer, entry.outer_stride, entry.inner = outer, outer_stride, inner
-        if outer * inner == 0 or b == 0:  # nothing to move; the pointer may be null
-            entry.src = entry.dst = parents.data_ptr() or 1
-            entry.outer = 0
-    live = [e for e in arr[:len(srcs)] if e.outer]
+            outer_stride = inner // outer if outer else 0
+            inner = outer_stride // max(shape[length_dim], 1) * length
+        if outer * inner * b * k == 0:
+            continue
+        at, to = src.data_ptr(), dst.data_ptr()
+        if out is not None and at == to:
+            raise ValueError("out must not overlap the states; leave it out to reorder in place")
+        live.append((at, to, stride[0] * e, stride[1] * e, into[0] * e, into[1] * e, outer,
+                     outer_stride, inner))
     with _on(dev, stream):
-        st = lib.flce_beam_reorder((BeamState * max(len(live), 1))(*live), len(live),
-                                   _ptr(parents), b, max(k, 1), _stream_handle(dev, stream))
+        st = lib.flce_beam_reorder((BeamState * len(live))(*live), len(live), _ptr(parents), b,
+                                   max(k, 1), _stream_handle(dev, stream))
     _check("flce_beam_reorder", st)
     return dsts[0] if single else dsts
