@@ -302,13 +302,16 @@ int flce_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int dt
  *   nearest E2M1 number (0, .5, 1, 1.5, 2, 3, 4, 6; ties to the even code;
  *   saturating at 6) times 2^e, with x's sign.  A block that holds an Inf or a
  *   NaN becomes NaN as a whole.
- *   codes   flce_mxfp4_codes_size(rows, cols) bytes: row r at r * ceil(cols/32)
- *           * 16, element 2i in the low half of byte i (a partly filled last
- *           block is padded with zeros).
+ *   codes   flce_mxfp4_codes_size(rows, cols) bytes: tiles of 128 rows x 256
+ *           columns (16 KB; tiles of one 128 rows follow one another along the
+ *           columns).  In a tile row r is 128 bytes at r * 128, element 2i in the
+ *           low half of byte i, with its 16-byte piece q stored at q ^ (r % 8).
+ *           Columns behind the last one are zeros.
  *   scales  flce_mxfp4_scales_size(rows, cols) bytes: e + 127 (255 = NaN) per
- *           block, in tiles of 128 rows x 4 blocks of 512 bytes (tiles of one
- *           128 rows follow one another along the columns); row r, block k of
- *           a tile at (r % 32) * 16 + (r / 32) * 4 + k.
+ *           block, in tiles of 128 rows x 4 blocks (512 bytes, in the same order,
+ *           two per tile of codes); row r, block k of a tile at (r % 32) * 16 +
+ *           (r / 32) * 4 + k.  Blocks behind the last one are 127.
+ *           Rows behind the last one are not written in either.
  *   x / out [rows, cols], rows ld elements apart, BF16 (dtype 0) or FP32 (1);
  *           any alignment of whole elements.  Both types hold the dequantised
  *           numbers exactly.  codes and scales must be 16-byte aligned.

@@ -10,16 +10,18 @@
 // Dividing by a power of two is exact and the nearest code is unique, so the
 // codes are a function of the input alone, whatever computes them.
 //
-// Layout in memory.  Codes: row r at r * pitch, pitch = ceil(cols / 32) * 16
-// bytes, element 2i in the low half of byte i; a partly filled last block is
-// padded with zeros.  Scales: tiles of 128 rows x 4 blocks of columns, 512
-// bytes each, the tiles of 128 rows one after the other along the columns;
-// inside a tile the scale of row r, block k sits at (r % 32) * 16 +
-// (r / 32) * 4 + k.  That is the order in which the tensor core wants them in
-// tensor memory (32 lanes x 16 bytes), so a tile goes from HBM to shared memory
-// and on to tensor memory as one block of bytes, with no reshuffling.
-// Scales of blocks behind a row's last one (up to the multiple of 4) are 127;
-// rows behind the last one are left as they were, nothing reads their products.
+// Layout in memory, as the tensor core reads it, so that a stage of the product
+// is a few contiguous copies (a row-major matrix would be read in 128-byte
+// pieces a row's pitch apart, which HBM serves at about half its bandwidth).
+// Codes: tiles of 128 rows x 256 columns, 16 KB, the tiles of 128 rows one after
+// the other along the columns.  Inside a tile a row is 128 bytes, element 2i in
+// the low half of byte i, and the 16-byte piece q of row r sits at q ^ (r % 8)
+// (the 128-byte swizzle).  Columns behind the last one are zeros.
+// Scales: tiles of 128 rows x 4 blocks, 512 bytes, in the same order, two per
+// tile of codes; the scale of row r, block k sits at (r % 32) * 16 + (r / 32) * 4
+// + k, which tensor memory wants (32 lanes x 16 bytes).  Blocks behind a row's
+// last one have scale 127 (up to a multiple of 8 blocks).
+// Rows behind the last one are left as they were; nothing reads their products.
 //
 // Both kernels are bound by HBM (quantising BF16 reads 2 bytes and writes
 // 17/32 of one per element).  Four threads share a block: each converts 8
@@ -39,16 +41,26 @@ constexpr int kMxBlock = 32;          // elements per scale
 constexpr int kMxTileRows = 128;      // rows of a scale tile
 constexpr int kMxTileBlocks = 4;      // column blocks of a scale tile
 constexpr int kMxTileBytes = kMxTileRows * kMxTileBlocks;
+constexpr int kMxTileCols = 256;      // columns of a tile of codes
+constexpr int kMxCodeBytes = kMxTileRows * kMxTileCols / 2;
 constexpr int kMxThreads = 256;
 constexpr int kMxUnroll = 4;          // vectors of 8 elements in flight per thread
 
 __host__ __device__ __forceinline__ int64_t mx_blocks(int64_t cols) {
   return (cols + kMxBlock - 1) / kMxBlock;
 }
-__host__ __device__ __forceinline__ int64_t mx_ktiles(int64_t cols) {
-  return (mx_blocks(cols) + kMxTileBlocks - 1) / kMxTileBlocks;
+// Tiles of codes (256 columns) along a row; twice as many tiles of scales.
+__host__ __device__ __forceinline__ int64_t mx_ctiles(int64_t cols) {
+  return (cols + kMxTileCols - 1) / kMxTileCols;
 }
-__host__ __device__ __forceinline__ int64_t mx_pitch(int64_t cols) { return mx_blocks(cols) * 16; }
+__host__ __device__ __forceinline__ int64_t mx_ktiles(int64_t cols) { return 2 * mx_ctiles(cols); }
+
+// Byte offset of the 4 bytes of codes of row r, columns [8 vec, 8 vec + 8).
+__device__ __forceinline__ int64_t mx_code_word(int64_t r, int64_t vec, int64_t ctiles) {
+  const int64_t tile = (r / kMxTileRows) * ctiles + (vec >> 5);
+  const int row = int(r % kMxTileRows), v = int(vec & 31);
+  return tile * kMxCodeBytes + row * 128 + (((v >> 2) ^ (row & 7)) << 4) + (v & 3) * 4;
+}
 
 // Byte offset of the 4-byte word that holds row r's scales of column tile kt.
 __device__ __forceinline__ int64_t mx_scale_word(int64_t r, int64_t kt, int64_t ktiles) {
@@ -72,7 +84,7 @@ struct MxQuantArgs {
   int64_t rows, cols, ld;
   uint8_t* codes;
   uint8_t* scales;
-  int64_t segs;  // pieces a row is cut into, a warp each (a multiple of 8 blocks per piece)
+  int64_t segs;  // pieces a row is cut into, a warp each (whole tiles of 256 columns)
 };
 
 // A warp takes a piece of a row: 8 blocks (32 vectors of 8 elements) per step.
@@ -81,8 +93,8 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const MxQuantArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = int64_t(gridDim.x) * (kMxThreads / 32);
-  const int64_t blocks = mx_blocks(a.cols), ktiles = mx_ktiles(a.cols), pitch = mx_pitch(a.cols);
-  const int64_t steps = (ktiles * kMxTileBlocks + 7) / 8;  // of 8 blocks each
+  const int64_t blocks = mx_blocks(a.cols), ctiles = mx_ctiles(a.cols), ktiles = 2 * ctiles;
+  const int64_t steps = ctiles;  // of 8 blocks each
   const int64_t per = (steps + a.segs - 1) / a.segs;
   for (int64_t u = int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5);
        u < a.rows * a.segs; u += warps) {
@@ -120,12 +132,12 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const MxQuantAr
         for (int j = 0; j < 8; ++j) v[i][j] *= inv;
         const uint32_t w = mx_pack8(v[i]);
         const int64_t vec = (s + i) * 32 + lane, b = vec >> 2;
-        if (b < blocks) *reinterpret_cast<uint32_t*>(a.codes + r * pitch + vec * 4) = w;
+        *reinterpret_cast<uint32_t*>(a.codes + mx_code_word(r, vec, ctiles)) = w;
         // Four blocks' scales as one word, written by the first of 16 lanes.
         uint32_t word = (b < blocks ? static_cast<uint32_t>(sc) : 127u) << (8 * ((lane >> 2) & 3));
         word |= __shfl_xor_sync(0xffffffffu, word, 4);
         word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        if ((lane & 15) == 0 && (b >> 2) < ktiles)
+        if ((lane & 15) == 0)
           *reinterpret_cast<uint32_t*>(a.scales + mx_scale_word(r, b >> 2, ktiles)) = word;
       }
     }
@@ -150,8 +162,7 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const MxDequantArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = int64_t(gridDim.x) * (kMxThreads / 32);
-  const int64_t ktiles = mx_ktiles(a.cols), pitch = mx_pitch(a.cols);
-  const int64_t steps = (mx_blocks(a.cols) + 7) / 8;
+  const int64_t ctiles = mx_ctiles(a.cols), ktiles = 2 * ctiles, steps = ctiles;
   const int64_t per = (steps + a.segs - 1) / a.segs;
   for (int64_t u = int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5);
        u < a.rows * a.segs; u += warps) {
@@ -164,7 +175,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const MxDequa
         const int64_t vec = (s + i) * 32 + lane;
         w[i] = sc[i] = 0;
         if (s + i < s1 && vec * 8 < a.cols) {
-          w[i] = *reinterpret_cast<const uint32_t*>(a.codes + r * pitch + vec * 4);
+          w[i] = *reinterpret_cast<const uint32_t*>(a.codes + mx_code_word(r, vec, ctiles));
           sc[i] = a.scales[mx_scale_word(r, vec >> 4, ktiles) + ((vec >> 2) & 3)];
         }
       }
@@ -200,12 +211,15 @@ static bool mx_sizes_ok(int64_t rows, int64_t cols) {
   return rows >= 0 && cols > 0 && rows <= kMaxDim && cols <= kMaxDim &&
          cols <= (int64_t(1) << 40) / std::max<int64_t>(rows, 1);
 }
+static size_t mx_codes_bytes(int64_t rows, int64_t cols) {
+  return size_t(cdiv(rows, kMxTileRows)) * size_t(mx_ctiles(cols)) * kMxCodeBytes;
+}
 static size_t mx_scales_bytes(int64_t rows, int64_t cols) {
   return size_t(cdiv(rows, kMxTileRows)) * size_t(mx_ktiles(cols)) * kMxTileBytes;
 }
 // Pieces per row (a warp each) and blocks: enough warps for the GPU when rows are few.
 static int64_t mx_segments(int64_t rows, int64_t cols, int sms, int64_t* grid) {
-  const int64_t steps = cdiv(mx_ktiles(cols) * kMxTileBlocks, 8);
+  const int64_t steps = mx_ctiles(cols);
   const int64_t want = cdiv(int64_t(sms) * 32, std::max<int64_t>(rows, 1));
   const int64_t segs = std::max<int64_t>(1, std::min(steps, want));
   *grid = std::max<int64_t>(1, std::min<int64_t>(cdiv(rows * segs, kMxThreads / 32), int64_t(sms) * 16));
@@ -237,7 +251,7 @@ static int mx_quantize(const DeviceInfo& dev, const void* x, int dtype, int64_t 
 }  // namespace flce
 
 extern "C" size_t flce_mxfp4_codes_size(int64_t rows, int64_t cols) {
-  return mx_sizes_ok(rows, cols) ? size_t(rows) * size_t(mx_pitch(cols)) : 0;
+  return mx_sizes_ok(rows, cols) ? mx_codes_bytes(rows, cols) : 0;
 }
 extern "C" size_t flce_mxfp4_scales_size(int64_t rows, int64_t cols) {
   return mx_sizes_ok(rows, cols) ? mx_scales_bytes(rows, cols) : 0;

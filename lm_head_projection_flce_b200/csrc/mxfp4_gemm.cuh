@@ -11,8 +11,9 @@
 // tokens that exist.  With few tokens the kernel is bound by HBM (the head is
 // read once); with many by the tensor core.
 //
-// Warp 0 loads: per stage of 256 elements of K a 128-byte-swizzled box of codes
-// per operand (TMA), and the scale tiles as plain bulk copies.  Warp 1 copies
+// Warp 0 loads: per stage of 256 elements of K the head's tile of codes (16 KB),
+// the tokens' rows of theirs, and both operands' scale tiles, each a contiguous
+// bulk copy.  Warp 1 copies
 // the stage's scales to tensor memory (tcgen05.cp, 32 lanes x 16 bytes
 // replicated to the four lane quarters) and issues the MMAs; both run in issue
 // order, and each stage has scale columns of its own, rewritten only after
@@ -33,6 +34,8 @@ constexpr int kMxgSmem = 225 * 1024;   // shared memory for the stages
 
 struct MxGemmArgs {
   int64_t n, v, h;
+  const uint8_t* w_codes;
+  const uint8_t* a_codes;
   const uint8_t* w_scales;
   const uint8_t* a_scales;
   int tile_n;         // tokens per tile, a multiple of 16
@@ -80,11 +83,11 @@ __device__ __forceinline__ void tc_mma_mxf4_one(uint32_t d, uint64_t a, uint64_t
 }
 // Untiled bulk copy to this CTA's shared memory (16-byte aligned, whole 16s).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
+                                          uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -104,16 +107,15 @@ __device__ __forceinline__ uint64_t mx_scale_desc(uint32_t addr) {
 }
 
 __host__ __device__ __forceinline__ int mxg_scale_tiles(int tile_n) { return tile_n > 128 ? 2 : 1; }
-// Bytes of a stage: codes of both operands, then 2 scale tiles (512 elements of
-// K = 2 x 128) per 128 rows of each.
+// Bytes of a stage: codes of both operands, then 2 scale tiles (2 x 128 elements
+// of K) per 128 rows of each.
 __host__ __device__ __forceinline__ uint32_t mxg_stage_bytes(int tile_n) {
   return uint32_t((kMxgM + tile_n) * kMxgKBytes + (1 + mxg_scale_tiles(tile_n)) * 2 * kMxTileBytes);
 }
 
 template <typename TO>
 __global__ void __launch_bounds__(kThreads, 1)
-    mx_gemm_kernel(const __grid_constant__ CUtensorMap map_w,
-                   const __grid_constant__ CUtensorMap map_a, const MxGemmArgs g) {
+    mx_gemm_kernel(const MxGemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kMxgMaxStages + 5];
   __shared__ uint32_t tmem_slot;
@@ -133,8 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t off_b = kMxgM * kMxgKBytes;
   const uint32_t off_sfa = off_b + uint32_t(g.tile_n) * kMxgKBytes;
   const uint32_t off_sfb = off_sfa + 2 * kMxTileBytes;
-  const int64_t blocks = mx_blocks(g.h), ktiles = mx_ktiles(g.h);
-  const int num_kb = int((blocks + kMxgBlocks - 1) / kMxgBlocks);
+  const int64_t blocks = mx_blocks(g.h);
+  const int num_kb = int(mx_ctiles(g.h));
   const int64_t a_tiles = (g.n + kMxTileRows - 1) / kMxTileRows;
 
   if (threadIdx.x == 0) {
@@ -149,8 +151,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain_bar, 1);
     ctl->abort = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&map_w);
-    tma_prefetch_desc(&map_a);
   }
   if (warp == 1) {
     tmem_alloc_one(smem_u32(&tmem_slot), kTmemCols);
@@ -173,25 +173,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int64_t t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
         const int64_t mt = t / g.n_tiles;
         const int64_t n0 = (t - mt * g.n_tiles) * g.tile_n;
+        // The tokens' rows: from row n0 % 128 of row tile bt, up to two row tiles.
         const int64_t bt = n0 / kMxTileRows;
         const int nbt = int(min(int64_t(sft), a_tiles - bt));
+        const int r0 = int(n0 % kMxTileRows), first = min(g.tile_n, kMxTileRows - r0);
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!wait_phase(empty_bar(st), ph ^ 1u, ctl, g.err, g.timeout_ns)) {
             ok = false;
             break;
           }
-          const int kts = int(min(int64_t(2), ktiles - 2 * kb));  // scale tiles along K
-          const uint32_t sfb = uint32_t(kts) * kMxTileBytes;
           const uint32_t base = smem_base + uint32_t(st) * stage_bytes;
-          mbar_arrive_expect_tx(full_bar(st),
-                                uint32_t(kMxgM + g.tile_n) * kMxgKBytes + sfb * uint32_t(1 + nbt));
-          tma_load_2d_hint(base, &map_w, full_bar(st), kb * kMxgKBytes, int(mt * kMxgM), pol_w);
-          tma_load_2d_hint(base + off_b, &map_a, full_bar(st), kb * kMxgKBytes, int(n0), pol_a);
-          bulk_load(base + off_sfa, g.w_scales + (mt * ktiles + 2 * kb) * kMxTileBytes, sfb,
-                    full_bar(st));
-          for (int j = 0; j < nbt; ++j)
+          const int rows = nbt > 1 ? g.tile_n : first;
+          mbar_arrive_expect_tx(full_bar(st), kMxCodeBytes + uint32_t(rows) * kMxgKBytes +
+                                                  uint32_t(1 + nbt) * 2 * kMxTileBytes);
+          const int64_t wt = mt * num_kb + kb;
+          bulk_load(base, g.w_codes + wt * kMxCodeBytes, kMxCodeBytes, full_bar(st), pol_w);
+          bulk_load(base + off_sfa, g.w_scales + wt * 2 * kMxTileBytes, 2 * kMxTileBytes,
+                    full_bar(st), pol_w);
+          for (int j = 0; j < nbt; ++j) {
+            const int64_t at = (bt + j) * num_kb + kb;
+            bulk_load(base + off_b + uint32_t(j * first) * kMxgKBytes,
+                      g.a_codes + at * kMxCodeBytes + (j == 0 ? r0 * kMxgKBytes : 0),
+                      uint32_t(j == 0 ? first : g.tile_n - first) * kMxgKBytes, full_bar(st), pol_a);
             bulk_load(base + off_sfb + uint32_t(j) * 2 * kMxTileBytes,
-                      g.a_scales + ((bt + j) * ktiles + 2 * kb) * kMxTileBytes, sfb, full_bar(st));
+                      g.a_scales + at * 2 * kMxTileBytes, 2 * kMxTileBytes, full_bar(st), pol_a);
+          }
           if (++st == stages) {
             st = 0;
             ph ^= 1u;
@@ -233,8 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after_sync();
           const uint32_t base = smem_base + uint32_t(st) * stage_bytes;
           const uint32_t sfa = sf_base + uint32_t(st) * sf_cols, sfb = sfa + 8u;
-          const int kts = int(min(int64_t(2), ktiles - 2 * kb));
-          for (int k = 0; k < kts; ++k) {
+          for (int k = 0; k < 2; ++k) {
             tc_copy_scales_one(sfa + 4u * k, mx_scale_desc(base + off_sfa + k * kMxTileBytes));
             for (int j = 0; j < sft; ++j)
               tc_copy_scales_one(sfb + uint32_t(k * 4 * sft + 4 * j),
@@ -309,27 +314,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Codes [rows][pitch] as boxes of 128 bytes x box_rows, 128-byte swizzle.
-static bool mx_tmap(CUtensorMap* tm, const void* codes, int64_t rows, int64_t cols, int box_rows) {
-  cuuint64_t dims[2] = {cuuint64_t(mx_pitch(cols)), cuuint64_t(rows)};
-  cuuint64_t strides[1] = {cuuint64_t(mx_pitch(cols))};
-  cuuint32_t box[2] = {cuuint32_t(kMxgKBytes), cuuint32_t(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  return g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <typename TO>
-static int mx_launch_gemm(const CUtensorMap& mw, const CUtensorMap& ma, const MxGemmArgs& g,
-                          int grid, cudaStream_t cs) {
+static int mx_launch_gemm(const MxGemmArgs& g, int grid, cudaStream_t cs) {
   auto kern = mx_gemm_kernel<TO>;
   const size_t smem = 1024 + size_t(g.stages) * mxg_stage_bytes(g.tile_n);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
       cudaSuccess)
     return FLCE_ERR_CUDA;
-  kern<<<grid, kThreads, smem, cs>>>(mw, ma, g);
+  kern<<<grid, kThreads, smem, cs>>>(g);
   return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 
@@ -338,7 +330,7 @@ struct MxLogitsPlan {
 };
 static MxLogitsPlan plan_mx_logits(int64_t n, int64_t h) {
   MxLogitsPlan p{};
-  p.off_scales = align_up(size_t(n) * size_t(mx_pitch(h)));
+  p.off_scales = align_up(mx_codes_bytes(n, h));
   p.total = std::max(kAlign, align_up(p.off_scales + mx_scales_bytes(n, h)));
   return p;
 }
@@ -382,6 +374,8 @@ extern "C" int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n, int64
   g.n = n;
   g.v = v;
   g.h = h;
+  g.w_codes = static_cast<const uint8_t*>(w_codes);
+  g.a_codes = a_codes;
   g.w_scales = static_cast<const uint8_t*>(w_scales);
   g.a_scales = a_scales;
   g.tile_n = int(std::min<int64_t>(cdiv(n, 16) * 16, kMxgMaxN));
@@ -396,13 +390,10 @@ extern "C" int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n, int64
   g.ldo = n > 1 ? ldo : v;
   g.err = dev->err;
   g.timeout_ns = kDefaultTimeoutNs;
-  CUtensorMap mw, ma;
-  if (!mx_tmap(&mw, w_codes, v, h, kMxgM) || !mx_tmap(&ma, a_codes, n, h, g.tile_n))
-    return FLCE_ERR_CUDA;
   const int grid = int(std::min<int64_t>(g.tiles, dev->num_sms));
   const double osz = out_dtype == FLCE_F32 ? 4.0 : 2.0;
   LaunchScope scope(KF_MX_GEMM, 2.0 * double(n) * double(h) * double(v),
                     double(n + v) * double(h) * 17.0 / 32.0 + osz * double(n) * double(v), cs);
-  return out_dtype == FLCE_BF16 ? mx_launch_gemm<__nv_bfloat16>(mw, ma, g, grid, cs)
-                                : mx_launch_gemm<float>(mw, ma, g, grid, cs);
+  return out_dtype == FLCE_BF16 ? mx_launch_gemm<__nv_bfloat16>(g, grid, cs)
+                                : mx_launch_gemm<float>(g, grid, cs);
 }

@@ -225,8 +225,9 @@ def _prepare(hidden, weight, labels):
 def _workspace(ws, need: int, device) -> tuple[torch.Tensor, int]:
     """The workspace tensor and its size in bytes (any dtype; contiguous, on `device`)."""
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    elif ws.device != device or not ws.is_contiguous():
+        need = max(need, 16)
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if ws.device != device or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     return ws, ws.numel() * ws.element_size()
 
@@ -733,10 +734,9 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, want=("dx", "dweight"
     _buffer(mean, n, torch.float32, dev, "mean")
     _buffer(rstd, n, torch.float32, dev, "rstd")
     with _on(dev, stream):
-        out, lddx = 0, h
         if "dx" in want:
             dx = _result(dx, x, x.shape, x.dtype, "dx")
-            out, lddx = _result_rows(dx, h, "dx")
+            _result_rows(dx, h, "dx")
         else:
             dx = None
         if "dweight" in want:
@@ -749,15 +749,23 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, want=("dx", "dweight"
                      else _buffer(dbias, h, w_dtype, dev, "dbias"))
         else:
             dbias = None
-        ws, ws_bytes = None, 0
-        if dweight is not None or dbias is not None:
-            ws, ws_bytes = _workspace(workspace, lib.flce_layer_norm_workspace_size(n, h), dev)
-        st = lib.flce_layer_norm_backward(_ptr(grads), lddy, _ptr(rows), W_DTYPES[x.dtype], n, h,
-                                          ldx, _ptr(weight), W_DTYPES[w_dtype], _ptr(mean),
-                                          _ptr(rstd), out, lddx, _ptr(dweight), _ptr(dbias),
-                                          _ptr(ws), ws_bytes, _stream_handle(dev, stream))
-    _check("flce_layer_norm_backward", st)
+        _norm_grads(lib, grads, lddy, rows, n, h, ldx, weight, w_dtype, mean, rstd, dx,
+                    h if dx is None else _rows(dx, h, "dx")[1], dweight, dbias, workspace,
+                    _stream_handle(dev, stream))
     return dx, dweight, dbias
+
+
+def _norm_grads(lib, dy, lddy, x, n, h, ldx, weight, w_dtype, mean, rstd, dx, lddx, dweight, dbias,
+                workspace, stream) -> None:
+    """flce_layer_norm_backward on checked tensors."""
+    ws, ws_bytes = None, 0
+    if dweight is not None or dbias is not None:
+        ws, ws_bytes = _workspace(workspace, lib.flce_layer_norm_workspace_size(n, h), x.device)
+    st = lib.flce_layer_norm_backward(_ptr(dy), lddy, _ptr(x), W_DTYPES[x.dtype], n, h, ldx,
+                                      _ptr(weight), W_DTYPES[w_dtype], _ptr(mean), _ptr(rstd),
+                                      _ptr(dx), lddx, _ptr(dweight), _ptr(dbias), _ptr(ws),
+                                      ws_bytes, stream)
+    _check("flce_layer_norm_backward", st)
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -765,17 +773,27 @@ class _LayerNorm(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps):
         y, mean, rstd = layer_norm_forward(x, weight, bias, eps=eps)
         ctx.save_for_backward(x, weight, mean, rstd)
-        ctx.param_dtype = bias.dtype if bias is not None else None
+        ctx.w_dtype = (weight if weight is not None else x if bias is None else bias).dtype
         return y
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
+        if torch.is_grad_enabled():
+            raise RuntimeError("layer_norm's gradient has no gradient of its own (create_graph)")
+        # What the forward checked is not checked again: this runs in autograd's own
+        # thread, where a small call's time is mostly Python.
         x, weight, mean, rstd = ctx.saved_tensors
-        want = [g for g, need in zip(("dx", "dweight", "dbias"), ctx.needs_input_grad) if need]
-        # a gradient that autograd broadcast (a sum's) has rows of stride 0
-        dx, dw, db = layer_norm_backward(dy.contiguous(), x, mean, rstd, weight, want=want,
-                                         param_dtype=ctx.param_dtype)
+        need_x, need_w, need_b, _ = ctx.needs_input_grad
+        h = x.shape[-1]
+        dev = x.device
+        dy = dy.contiguous()  # a gradient that autograd broadcast (a sum's) has rows of stride 0
+        rows, ldx = _rows(x, h, "x")
+        with _on(dev):
+            dx = x.new_empty(x.shape) if need_x else None
+            dw = x.new_empty(h, dtype=ctx.w_dtype) if need_w else None
+            db = x.new_empty(h, dtype=ctx.w_dtype) if need_b else None
+            _norm_grads(_LIB, dy, h, rows, rows.shape[0], h, ldx, weight, ctx.w_dtype, mean, rstd,
+                        dx, h, dw, db, None, _stream_handle(dev))
         return dx, dw, db, None
 
 
@@ -794,9 +812,9 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
 @dataclasses.dataclass(frozen=True)
 class Mxfp4:
     """A matrix [rows, cols] in microscaled 4-bit floating point (see include/flce.h):
-    ``codes`` uint8 [rows, ceil(cols / 32) * 16], two E2M1 codes per byte, and
+    ``codes`` uint8, two E2M1 codes per byte, in tiles of 128 rows x 256 columns, and
     ``scales`` uint8, one E8M0 exponent per 32 columns, in tiles of 128 rows x 4
-    blocks as the tensor core reads them."""
+    blocks, both as the tensor core reads them."""
 
     codes: torch.Tensor
     scales: torch.Tensor
@@ -811,12 +829,19 @@ class Mxfp4:
     def device(self) -> torch.device:
         return self.codes.device
 
+    def element_codes(self) -> torch.Tensor:
+        """The 4-bit codes (sign and E2M1 index) as uint8 [rows, cols] (a copy in row order)."""
+        t = self.codes.view(-(-self.rows // 128), -(-self.cols // 256), 16, 8, 8, 16)
+        row = torch.arange(8, device=t.device)[:, None]
+        t = t[:, :, :, row, row ^ torch.arange(8, device=t.device)]  # undo the swizzle of a row's 16-byte pieces
+        t = t.permute(0, 2, 3, 1, 4, 5).reshape(-(-self.rows // 128) * 128, -1)
+        return torch.stack([t & 15, t >> 4], dim=-1).view(t.shape[0], -1)[:self.rows, :self.cols].contiguous()
+
     def block_exponents(self) -> torch.Tensor:
         """The biased exponents as [rows, ceil(cols / 32)] (a copy in row order)."""
-        blocks = -(-self.cols // 32)
-        t = self.scales.view(-(-self.rows // 128), -(-blocks // 4), 32, 4, 4)
-        t = t.permute(0, 3, 2, 1, 4).reshape(-1, -(-blocks // 4) * 4)
-        return t[:self.rows, :blocks].contiguous()
+        tiles = -(-self.rows // 128), 2 * -(-self.cols // 256)
+        t = self.scales.view(*tiles, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(tiles[0] * 128, -1)
+        return t[:self.rows, :-(-self.cols // 32)].contiguous()
 
 
 def _mxfp4_operand(q: Mxfp4, name: str) -> None:
@@ -845,9 +870,8 @@ def mxfp4_quantize(x, *, out: Mxfp4 | None = None, stream=None) -> Mxfp4:
     dev = x.device
     with _on(dev, stream):
         if out is None:
-            codes = torch.empty(n, -(-h // 32) * 16, dtype=torch.uint8, device=dev)
-            scales = torch.empty(int(lib.flce_mxfp4_scales_size(n, h)), dtype=torch.uint8,
-                                 device=dev)
+            codes = x.new_empty(lib.flce_mxfp4_codes_size(n, h), dtype=torch.uint8)
+            scales = x.new_empty(lib.flce_mxfp4_scales_size(n, h), dtype=torch.uint8)
             out = Mxfp4(codes, scales, n, h)
         else:
             _mxfp4_operand(out, "out")

@@ -45,9 +45,7 @@ def test_quantise(dev, dtype, r, c):
     x = _matrix(r * 31 + c, r, c, dtype)
     q = flce.mxfp4_quantize(x.to(dev))
     codes, exps, values = HO.mxfp4(_np(x))
-    got = q.codes.cpu().numpy()
-    both = np.stack([got & 15, got >> 4], axis=-1).reshape(r, -1)
-    assert np.array_equal(both[:, :c], codes) and np.all(both[:, c:] == 0)
+    assert np.array_equal(q.element_codes().cpu().numpy(), codes)
     assert np.array_equal(q.block_exponents().cpu().numpy(), exps)
     for out in (torch.bfloat16, torch.float32):
         assert np.array_equal(_np(flce.mxfp4_dequantize(q, out)), values)
@@ -70,7 +68,7 @@ def test_special_blocks(dev):
 def test_row_strides(dev, c, ld):
     full = _matrix(c + ld, 33, c, torch.bfloat16, ld=ld).to(dev)
     q = flce.mxfp4_quantize(full[:, :c])
-    assert torch.equal(q.codes, flce.mxfp4_quantize(full[:, :c].contiguous()).codes)
+    assert torch.equal(q.element_codes(), flce.mxfp4_quantize(full[:, :c].contiguous()).element_codes())
     out = torch.full((33, ld), 7.0, dtype=torch.bfloat16, device=dev)
     flce.mxfp4_dequantize(q, out=out[:, :c])
     assert torch.equal(out[:, :c], flce.mxfp4_dequantize(q)) and torch.all(out[:, c:] == 7.0)

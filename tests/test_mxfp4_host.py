@@ -35,8 +35,9 @@ def test_definition():
 
 def test_sizes(lib):
     codes, scales = lib.flce_mxfp4_codes_size, lib.flce_mxfp4_scales_size
-    assert codes(5, 32) == 80 and codes(5, 33) == 160 and codes(0, 8) == 0
-    assert scales(1, 1) == 512 and scales(128, 128) == 512 and scales(129, 129) == 2048
+    assert codes(1, 1) == 16384 and codes(128, 256) == 16384 and codes(129, 257) == 65536
+    assert scales(1, 1) == 1024 and scales(128, 256) == 1024 and scales(129, 257) == 4096
+    assert codes(0, 8) == 0 and scales(0, 8) == 0
     assert codes(-1, 8) == 0 and scales(4, 0) == 0 and scales(1 << 31, 8) == 0
     assert lib.flce_mxfp4_logits_workspace_size(8, 4096) >= codes(8, 4096) + scales(8, 4096)
     assert lib.flce_mxfp4_logits_workspace_size(-1, 4096) == 0
