@@ -61,6 +61,16 @@ __device__ __forceinline__ void tmem_dealloc_one(uint32_t taddr, uint32_t ncols)
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
 }
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void tc_commit_one(uint32_t bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
@@ -113,7 +123,8 @@ __host__ __device__ __forceinline__ uint32_t mxg_stage_bytes(int tile_n) {
   return uint32_t((kMxgM + tile_n) * kMxgKBytes + (1 + mxg_scale_tiles(tile_n)) * 2 * kMxTileBytes);
 }
 
-template <typename TO>
+// kSft: scale tiles of 128 tokens that a tile's columns touch (2 above 128 columns).
+template <typename TO, int kSft>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const MxGemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
@@ -130,7 +141,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * kMxgMaxStages + 2 + a); };
   const uint32_t drain_bar = bar_base + 8u * (2 * kMxgMaxStages + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sft = mxg_scale_tiles(g.tile_n);
   const uint32_t stage_bytes = mxg_stage_bytes(g.tile_n);
   const uint32_t off_b = kMxgM * kMxgKBytes;
   const uint32_t off_sfa = off_b + uint32_t(g.tile_n) * kMxgKBytes;
@@ -162,112 +172,153 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   const uint32_t tmem = tmem_slot;
 
+  // Warps 0 and 1 run their loops with all lanes, so that addresses and
+  // descriptors stay in uniform registers; one elected lane issues.  The loops
+  // keep running values: with the multiplications in them, the two issuing
+  // threads themselves were the bound (1690 instead of XX us at 4096 tokens).
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------ loads
-      const uint64_t pol_w = l2_policy_evict_normal();
-      const uint64_t pol_a = l2_policy_evict_last();
-      int st = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
-        const int64_t mt = t / g.n_tiles;
-        const int64_t n0 = (t - mt * g.n_tiles) * g.tile_n;
-        // The tokens' rows: from row n0 % 128 of row tile bt, up to two row tiles.
-        const int64_t bt = n0 / kMxTileRows;
-        const int nbt = int(min(int64_t(sft), a_tiles - bt));
-        const int r0 = int(n0 % kMxTileRows), first = min(g.tile_n, kMxTileRows - r0);
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!wait_phase(empty_bar(st), ph ^ 1u, ctl, g.err, g.timeout_ns)) {
-            ok = false;
-            break;
-          }
-          const uint32_t base = smem_base + uint32_t(st) * stage_bytes;
-          const int rows = nbt > 1 ? g.tile_n : first;
-          mbar_arrive_expect_tx(full_bar(st), kMxCodeBytes + uint32_t(rows) * kMxgKBytes +
-                                                  uint32_t(1 + nbt) * 2 * kMxTileBytes);
-          const int64_t wt = mt * num_kb + kb;
-          bulk_load(base, g.w_codes + wt * kMxCodeBytes, kMxCodeBytes, full_bar(st), pol_w);
-          bulk_load(base + off_sfa, g.w_scales + wt * 2 * kMxTileBytes, 2 * kMxTileBytes,
-                    full_bar(st), pol_w);
-          for (int j = 0; j < nbt; ++j) {
-            const int64_t at = (bt + j) * num_kb + kb;
-            bulk_load(base + off_b + uint32_t(j * first) * kMxgKBytes,
-                      g.a_codes + at * kMxCodeBytes + (j == 0 ? r0 * kMxgKBytes : 0),
-                      uint32_t(j == 0 ? first : g.tile_n - first) * kMxgKBytes, full_bar(st), pol_a);
-            bulk_load(base + off_sfb + uint32_t(j) * 2 * kMxTileBytes,
-                      g.a_scales + at * 2 * kMxTileBytes, 2 * kMxTileBytes, full_bar(st), pol_a);
-          }
-          if (++st == stages) {
-            st = 0;
-            ph ^= 1u;
+    // -------------------------------------------------- loads
+    const bool leader = elect_one();
+    const uint64_t pol_w = l2_policy_evict_normal();
+    const uint64_t pol_a = l2_policy_evict_last();
+    int st = 0;
+    uint32_t ph = 0, base = smem_base, full = full_bar(0);
+    bool ok = true;
+    for (int64_t t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
+      const int64_t mt = t / g.n_tiles;
+      const int64_t n0 = (t - mt * g.n_tiles) * g.tile_n;
+      // The tokens' rows: from row n0 % 128 of row tile bt, up to two row tiles.
+      const int64_t bt = n0 / kMxTileRows;
+      const bool two = kSft == 2 && bt + 1 < a_tiles;
+      const int r0 = int(n0 % kMxTileRows), first = min(g.tile_n, kMxTileRows - r0);
+      const uint32_t bytes0 = uint32_t(first) * kMxgKBytes;
+      const uint32_t bytes1 = uint32_t(g.tile_n - first) * kMxgKBytes;
+      const uint32_t expect = kMxCodeBytes + 4 * kMxTileBytes + bytes0 +
+                              (two ? bytes1 + 2 * kMxTileBytes : 0u);
+      const uint8_t* wc = g.w_codes + mt * num_kb * kMxCodeBytes;
+      const uint8_t* ws = g.w_scales + mt * num_kb * (2 * kMxTileBytes);
+      const uint8_t* ac = g.a_codes + bt * num_kb * kMxCodeBytes + r0 * kMxgKBytes;
+      const uint8_t* as = g.a_scales + bt * num_kb * (2 * kMxTileBytes);
+      // ... and of the second row tile, from its first row
+      const uint8_t* ac1 = g.a_codes + (bt + 1) * num_kb * kMxCodeBytes;
+      const uint8_t* as1 = as + num_kb * (2 * kMxTileBytes);
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (!wait_phase(full + 8u * kMxgMaxStages, ph ^ 1u, ctl, g.err, g.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        if (leader) {
+          mbar_arrive_expect_tx(full, expect);
+          bulk_load(base, wc, kMxCodeBytes, full, pol_w);
+          bulk_load(base + off_sfa, ws, 2 * kMxTileBytes, full, pol_w);
+          bulk_load(base + off_b, ac, bytes0, full, pol_a);
+          bulk_load(base + off_sfb, as, 2 * kMxTileBytes, full, pol_a);
+          if (two) {
+            bulk_load(base + off_b + bytes0, ac1, bytes1, full, pol_a);
+            bulk_load(base + off_sfb + 2 * kMxTileBytes, as1, 2 * kMxTileBytes, full, pol_a);
           }
         }
-      }
-      if (!ok) {
-        // Give the copies in flight time to land before the block can exit.
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 200000ull) {
+        wc += kMxCodeBytes;
+        ws += 2 * kMxTileBytes;
+        ac += kMxCodeBytes;
+        as += 2 * kMxTileBytes;
+        ac1 += kMxCodeBytes;
+        as1 += 2 * kMxTileBytes;
+        base += stage_bytes;
+        full += 8u;
+        if (++st == stages) {
+          st = 0;
+          ph ^= 1u;
+          base = smem_base;
+          full = full_bar(0);
         }
       }
     }
+    if (!ok) {
+      // Give the copies in flight time to land before the block can exit.
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 200000ull) {
+      }
+    }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------ scales to tensor memory, MMAs
-      const uint32_t idesc = mma_idesc_mxf4(kMxgM, g.tile_n);
-      constexpr uint64_t hi = desc_hi_sw128(16u, 1024u);
-      // Scale columns of stage s: [A tile of K half 0, of half 1][B the same, 4 per 128 tokens]
-      const uint32_t sf_cols = uint32_t(8 + 8 * sft);
-      const uint32_t sf_base = tmem + 2u * uint32_t(g.tile_n);
-      int st = 0, acc = 0;
-      uint32_t ph = 0, acc_ph = 0;
-      bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
-        const int64_t n0 = (t % g.n_tiles) * g.tile_n;
-        const uint32_t shift = uint32_t(n0 % kMxTileRows) / 32u;  // first token's scale column
-        if (!wait_phase(tempty_bar(acc), acc_ph ^ 1u, ctl, g.err, g.timeout_ns)) {
+    // -------------------------------------------------- scales to tensor memory, MMAs
+    const bool leader = elect_one();
+    const uint32_t idesc = mma_idesc_mxf4(kMxgM, g.tile_n);
+    constexpr uint32_t kIdOdd = (2u << 4) | (2u << 29);  // bytes 2, 3 of the scale words
+    constexpr uint64_t hi = desc_hi_sw128(16u, 1024u);
+    const uint64_t da0 = hi | static_cast<uint64_t>((smem_base & 0x3FFFFu) >> 4);
+    const uint64_t step = stage_bytes >> 4;
+    const uint64_t db_off = off_b >> 4;
+    const uint64_t dsa0 = mx_scale_desc(smem_base + off_sfa);
+    // Scale columns of a stage: the head's first and second half of K, 4 each;
+    // then the tokens' first half (4 per 128 tokens) and second half.
+    constexpr uint32_t kSfCols = 8 + 8 * kSft;
+    const uint32_t sf0 = tmem + 2u * uint32_t(g.tile_n);
+    int st = 0, acc = 0;
+    uint32_t ph = 0, acc_ph = 0, full = full_bar(0), sfa = sf0;
+    uint64_t da = da0, dsa = dsa0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
+      const int64_t n0 = (t % g.n_tiles) * g.tile_n;
+      const uint32_t shift = uint32_t(n0 % kMxTileRows) / 32u;  // first token's scale column
+      if (!wait_phase(tempty_bar(acc), acc_ph ^ 1u, ctl, g.err, g.timeout_ns)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t d = tmem + uint32_t(acc) * uint32_t(g.tile_n);
+      int left = int(blocks);  // scale blocks still to multiply
+      uint32_t more = 0;
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (!wait_phase(full, ph, ctl, g.err, g.timeout_ns)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t d = tmem + uint32_t(acc) * uint32_t(g.tile_n);
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!wait_phase(full_bar(st), ph, ctl, g.err, g.timeout_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t base = smem_base + uint32_t(st) * stage_bytes;
-          const uint32_t sfa = sf_base + uint32_t(st) * sf_cols, sfb = sfa + 8u;
-          for (int k = 0; k < 2; ++k) {
-            tc_copy_scales_one(sfa + 4u * k, mx_scale_desc(base + off_sfa + k * kMxTileBytes));
-            for (int j = 0; j < sft; ++j)
-              tc_copy_scales_one(sfb + uint32_t(k * 4 * sft + 4 * j),
-                                 mx_scale_desc(base + off_sfb + uint32_t(j * 2 + k) * kMxTileBytes));
-          }
-          const int mmas = int(min(int64_t(4), (blocks - int64_t(kb) * kMxgBlocks + 1) / 2));
-          const uint64_t da = hi | static_cast<uint64_t>((base & 0x3FFFFu) >> 4);
-          const uint64_t db = hi | static_cast<uint64_t>(((base + off_b) & 0x3FFFFu) >> 4);
-          for (int kk = 0; kk < mmas; ++kk) {
-            const uint32_t id = uint32_t(kk & 1) * 2u;  // bytes 0,1 or 2,3 of the scale word
-            tc_mma_mxf4_one(d, da + 2u * kk, db + 2u * kk, idesc | (id << 4) | (id << 29),
-                            sfa + 4u * (kk >> 1), sfb + uint32_t((kk >> 1) * 4 * sft) + shift,
-                            (kb | kk) != 0 ? 1u : 0u);
-          }
-          tc_commit_one(empty_bar(st));
-          if (++st == stages) {
-            st = 0;
-            ph ^= 1u;
-          }
+        if (leader) {
+          const uint32_t sfb = sfa + 8u;
+          const uint64_t dsb = dsa + (2 * kMxTileBytes >> 4);
+          constexpr uint64_t kTile = kMxTileBytes >> 4;
+          tc_copy_scales_one(sfa, dsa);
+          tc_copy_scales_one(sfa + 4u, dsa + kTile);
+          tc_copy_scales_one(sfb, dsb);
+          if (kSft == 2) tc_copy_scales_one(sfb + 4u, dsb + 2 * kTile);
+          tc_copy_scales_one(sfb + 4u * kSft, dsb + kTile);
+          if (kSft == 2) tc_copy_scales_one(sfb + 4u * kSft + 4u, dsb + 3 * kTile);
+          const uint64_t db = da + db_off;
+          const uint32_t sb = sfb + shift;
+          tc_mma_mxf4_one(d, da, db, idesc, sfa, sb, more);
+          if (left > 2) tc_mma_mxf4_one(d, da + 2, db + 2, idesc | kIdOdd, sfa, sb, 1u);
+          if (left > 4) tc_mma_mxf4_one(d, da + 4, db + 4, idesc, sfa + 4u, sb + 4u * kSft, 1u);
+          if (left > 6)
+            tc_mma_mxf4_one(d, da + 6, db + 6, idesc | kIdOdd, sfa + 4u, sb + 4u * kSft, 1u);
+          tc_commit_one(full + 8u * kMxgMaxStages);
         }
-        if (!ok) break;
-        tc_commit_one(tfull_bar(acc));
-        acc ^= 1;
-        if (acc == 0) acc_ph ^= 1u;
+        __syncwarp();
+        more = 1u;
+        left -= kMxgBlocks;
+        full += 8u;
+        sfa += kSfCols;
+        da += step;
+        dsa += step;
+        if (++st == stages) {
+          st = 0;
+          ph ^= 1u;
+          full = full_bar(0);
+          sfa = sf0;
+          da = da0;
+          dsa = dsa0;
+        }
       }
-      tc_commit_one(drain_bar);
-      drain_wait(drain_bar, 0, ok ? g.timeout_ns : 100000000ull);
+      if (!ok) break;
+      if (leader) tc_commit_one(tfull_bar(acc));
+      __syncwarp();
+      acc ^= 1;
+      if (acc == 0) acc_ph ^= 1u;
     }
+    if (leader) tc_commit_one(drain_bar);
+    __syncwarp();
+    drain_wait(drain_bar, 0, ok ? g.timeout_ns : 100000000ull);
   } else {
     // -------------------------------------------------- epilogue: lanes are head rows
     const int quarter = warp & 3;
@@ -314,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename TO>
+template <typename TO, int kSft>
 static int mx_launch_gemm(const MxGemmArgs& g, int grid, cudaStream_t cs) {
-  auto kern = mx_gemm_kernel<TO>;
+  auto kern = mx_gemm_kernel<TO, kSft>;
   const size_t smem = 1024 + size_t(g.stages) * mxg_stage_bytes(g.tile_n);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
       cudaSuccess)
@@ -394,6 +445,9 @@ extern "C" int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n, int64
   const double osz = out_dtype == FLCE_F32 ? 4.0 : 2.0;
   LaunchScope scope(KF_MX_GEMM, 2.0 * double(n) * double(h) * double(v),
                     double(n + v) * double(h) * 17.0 / 32.0 + osz * double(n) * double(v), cs);
-  return out_dtype == FLCE_BF16 ? mx_launch_gemm<__nv_bfloat16>(g, grid, cs)
-                                : mx_launch_gemm<float>(g, grid, cs);
+  if (mxg_scale_tiles(g.tile_n) == 1)
+    return out_dtype == FLCE_BF16 ? mx_launch_gemm<__nv_bfloat16, 1>(g, grid, cs)
+                                  : mx_launch_gemm<float, 1>(g, grid, cs);
+  return out_dtype == FLCE_BF16 ? mx_launch_gemm<__nv_bfloat16, 2>(g, grid, cs)
+                                : mx_launch_gemm<float, 2>(g, grid, cs);
 }
