@@ -5,11 +5,15 @@
 // itself (tcgen05.mma kind::mxf4, one E8M0 scale per 32 elements), with FP32
 // accumulation in tensor memory.
 //
-// The head's rows are the M side of the tile (128 rows) and the tokens the N
-// side (16 to 192 columns): a decoding step has few tokens, and then the head's
-// codes, which are all of the traffic, fill whole tiles, while N shrinks to the
-// tokens that exist.  With few tokens the kernel is bound by HBM (the head is
-// read once); with many by the tensor core.
+// Which operand is the M side (128 rows of a tile) and which the N side (16 to
+// 192 columns) depends on the tokens.  Few (up to 192): the head is the M side, so its
+// codes, which are nearly all of the traffic, fill whole tiles while N shrinks
+// to the tokens that exist; the kernel is bound by HBM, the head is read once.
+// Many: the tokens are the M side, so a thread of the epilogue holds consecutive
+// logits of one token and stores 32 bytes at a time; lanes that hold consecutive
+// logits store 2 bytes each, which took longer than the product (1205 us against
+// XX at 4096 x 4096 x 128256).  Rows of logits that do not start on 16 bytes need
+// the first form whatever the tokens.
 //
 // Warp 0 loads: per stage of 256 elements of K the head's tile of codes (16 KB),
 // the tokens' rows of theirs, and both operands' scale tiles, each a contiguous
@@ -27,24 +31,27 @@ namespace flce {
 
 constexpr int kMxgKBytes = 128;        // bytes of codes per row and stage
 constexpr int kMxgBlocks = 8;          // scale blocks (256 elements) per stage
-constexpr int kMxgM = 128;             // head rows per tile
-constexpr int kMxgMaxN = 192;          // tokens per tile: two accumulators and the scales fit
+constexpr int kMxgM = 128;             // rows on the M side of a tile
+constexpr int kMxgMaxN = 192;          // on the N side: two accumulators and the scales fit
 constexpr int kMxgMaxStages = 12;
 constexpr int kMxgSmem = 225 * 1024;   // shared memory for the stages
 
 struct MxGemmArgs {
-  int64_t n, v, h;
-  const uint8_t* w_codes;
-  const uint8_t* a_codes;
-  const uint8_t* w_scales;
-  const uint8_t* a_scales;
-  int tile_n;         // tokens per tile, a multiple of 16
-  int n_tiles;        // token tiles
-  int64_t tiles;      // token tiles x head tiles, token tiles fastest
+  int64_t rows_m, rows_n, h;  // rows of the operand on the M and on the N side
+  const uint8_t* m_codes;
+  const uint8_t* m_scales;
+  const uint8_t* n_codes;
+  const uint8_t* n_scales;
+  int tile_n;         // N rows per tile, a multiple of 16 (of 64 where there are several)
+  int64_t m_tiles, n_tiles;
+  int m_fast;         // M tiles of one N tile follow one another, else the reverse
+  int m_stream;       // the M side's codes are read once: they need not stay in L2
+  int64_t tiles;
   int stages;
   float softcap, inv_softcap;
   void* out;
   int64_t ldo;
+  int v8;             // kTokensM: rows of logits start on 32 bytes
   unsigned* err;
   uint64_t timeout_ns;
 };
@@ -123,8 +130,9 @@ __host__ __device__ __forceinline__ uint32_t mxg_stage_bytes(int tile_n) {
   return uint32_t((kMxgM + tile_n) * kMxgKBytes + (1 + mxg_scale_tiles(tile_n)) * 2 * kMxTileBytes);
 }
 
-// kSft: scale tiles of 128 tokens that a tile's columns touch (2 above 128 columns).
-template <typename TO, int kSft>
+// kSft: scale tiles of 128 rows that a tile's N side touches (2 above 128 rows).
+// kTokensM: the tokens are the M side.
+template <typename TO, int kSft, bool kTokensM>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const MxGemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
@@ -147,7 +155,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t off_sfb = off_sfa + 2 * kMxTileBytes;
   const int64_t blocks = mx_blocks(g.h);
   const int num_kb = int(mx_ctiles(g.h));
-  const int64_t a_tiles = (g.n + kMxTileRows - 1) / kMxTileRows;
+  const int64_t n_row_tiles = (g.rows_n + kMxTileRows - 1) / kMxTileRows;
+  auto coords = [&](int64_t t, int64_t& mt, int64_t& n0) {
+    const int64_t fast = g.m_fast ? g.m_tiles : g.n_tiles, q = t / fast, r = t - q * fast;
+    mt = g.m_fast ? r : q;
+    n0 = (g.m_fast ? q : r) * g.tile_n;
+  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -179,29 +192,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // -------------------------------------------------- loads
     const bool leader = elect_one();
-    const uint64_t pol_w = l2_policy_evict_normal();
-    const uint64_t pol_a = l2_policy_evict_last();
+    // A head read once is marked first to go, which spares the rest of L2 (64 ->
+    // 55 us at 8 tokens x 4096 x 128256).
+    const uint64_t pol_m = g.m_stream ? l2_policy_evict_first() : l2_policy_evict_normal();
+    const uint64_t pol_n = g.m_stream ? l2_policy_evict_last() : l2_policy_evict_normal();
     int st = 0;
     uint32_t ph = 0, base = smem_base, full = full_bar(0);
     bool ok = true;
     for (int64_t t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
-      const int64_t mt = t / g.n_tiles;
-      const int64_t n0 = (t - mt * g.n_tiles) * g.tile_n;
-      // The tokens' rows: from row n0 % 128 of row tile bt, up to two row tiles.
+      int64_t mt, n0;
+      coords(t, mt, n0);
+      // The N side's rows: from row n0 % 128 of row tile bt, up to two row tiles.
       const int64_t bt = n0 / kMxTileRows;
-      const bool two = kSft == 2 && bt + 1 < a_tiles;
+      const bool two = kSft == 2 && bt + 1 < n_row_tiles;
       const int r0 = int(n0 % kMxTileRows), first = min(g.tile_n, kMxTileRows - r0);
       const uint32_t bytes0 = uint32_t(first) * kMxgKBytes;
       const uint32_t bytes1 = uint32_t(g.tile_n - first) * kMxgKBytes;
       const uint32_t expect = kMxCodeBytes + 4 * kMxTileBytes + bytes0 +
                               (two ? bytes1 + 2 * kMxTileBytes : 0u);
-      const uint8_t* wc = g.w_codes + mt * num_kb * kMxCodeBytes;
-      const uint8_t* ws = g.w_scales + mt * num_kb * (2 * kMxTileBytes);
-      const uint8_t* ac = g.a_codes + bt * num_kb * kMxCodeBytes + r0 * kMxgKBytes;
-      const uint8_t* as = g.a_scales + bt * num_kb * (2 * kMxTileBytes);
+      const uint8_t* mc = g.m_codes + mt * num_kb * kMxCodeBytes;
+      const uint8_t* ms = g.m_scales + mt * num_kb * (2 * kMxTileBytes);
+      const uint8_t* nc = g.n_codes + bt * num_kb * kMxCodeBytes + r0 * kMxgKBytes;
+      const uint8_t* ns = g.n_scales + bt * num_kb * (2 * kMxTileBytes);
       // ... and of the second row tile, from its first row
-      const uint8_t* ac1 = g.a_codes + (bt + 1) * num_kb * kMxCodeBytes;
-      const uint8_t* as1 = as + num_kb * (2 * kMxTileBytes);
+      const uint8_t* nc1 = g.n_codes + (bt + 1) * num_kb * kMxCodeBytes;
+      const uint8_t* ns1 = ns + num_kb * (2 * kMxTileBytes);
       for (int kb = 0; kb < num_kb; ++kb) {
         if (!wait_phase(full + 8u * kMxgMaxStages, ph ^ 1u, ctl, g.err, g.timeout_ns)) {
           ok = false;
@@ -209,21 +224,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (leader) {
           mbar_arrive_expect_tx(full, expect);
-          bulk_load(base, wc, kMxCodeBytes, full, pol_w);
-          bulk_load(base + off_sfa, ws, 2 * kMxTileBytes, full, pol_w);
-          bulk_load(base + off_b, ac, bytes0, full, pol_a);
-          bulk_load(base + off_sfb, as, 2 * kMxTileBytes, full, pol_a);
+          bulk_load(base, mc, kMxCodeBytes, full, pol_m);
+          bulk_load(base + off_sfa, ms, 2 * kMxTileBytes, full, pol_m);
+          bulk_load(base + off_b, nc, bytes0, full, pol_n);
+          bulk_load(base + off_sfb, ns, 2 * kMxTileBytes, full, pol_n);
           if (two) {
-            bulk_load(base + off_b + bytes0, ac1, bytes1, full, pol_a);
-            bulk_load(base + off_sfb + 2 * kMxTileBytes, as1, 2 * kMxTileBytes, full, pol_a);
+            bulk_load(base + off_b + bytes0, nc1, bytes1, full, pol_n);
+            bulk_load(base + off_sfb + 2 * kMxTileBytes, ns1, 2 * kMxTileBytes, full, pol_n);
           }
         }
-        wc += kMxCodeBytes;
-        ws += 2 * kMxTileBytes;
-        ac += kMxCodeBytes;
-        as += 2 * kMxTileBytes;
-        ac1 += kMxCodeBytes;
-        as1 += 2 * kMxTileBytes;
+        mc += kMxCodeBytes;
+        ms += 2 * kMxTileBytes;
+        nc += kMxCodeBytes;
+        ns += 2 * kMxTileBytes;
+        nc1 += kMxCodeBytes;
+        ns1 += 2 * kMxTileBytes;
         base += stage_bytes;
         full += 8u;
         if (++st == stages) {
@@ -250,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t step = stage_bytes >> 4;
     const uint64_t db_off = off_b >> 4;
     const uint64_t dsa0 = mx_scale_desc(smem_base + off_sfa);
-    // Scale columns of a stage: the head's first and second half of K, 4 each;
-    // then the tokens' first half (4 per 128 tokens) and second half.
+    // Scale columns of a stage: the M side's first and second half of K, 4 each;
+    // then the N side's first half (4 per 128 rows) and second half.
     constexpr uint32_t kSfCols = 8 + 8 * kSft;
     const uint32_t sf0 = tmem + 2u * uint32_t(g.tile_n);
     int st = 0, acc = 0;
@@ -259,8 +274,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t da = da0, dsa = dsa0;
     bool ok = true;
     for (int64_t t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
-      const int64_t n0 = (t % g.n_tiles) * g.tile_n;
-      const uint32_t shift = uint32_t(n0 % kMxTileRows) / 32u;  // first token's scale column
+      int64_t mt, n0;
+      coords(t, mt, n0);
+      const uint32_t shift = uint32_t(n0 % kMxTileRows) / 32u;  // first N row's scale column
       if (!wait_phase(tempty_bar(acc), acc_ph ^ 1u, ctl, g.err, g.timeout_ns)) {
         ok = false;
         break;
@@ -320,32 +336,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     drain_wait(drain_bar, 0, ok ? g.timeout_ns : 100000000ull);
   } else {
-    // -------------------------------------------------- epilogue: lanes are head rows
+    // -------------------------------------------------- epilogue: lanes are M rows
     const int quarter = warp & 3;
     int acc = 0;
     uint32_t acc_ph = 0;
     const bool capped = g.softcap > 0.0f;
     for (int64_t t = blockIdx.x; t < g.tiles; t += gridDim.x) {
-      const int64_t mt = t / g.n_tiles;
-      const int64_t n0 = (t - mt * g.n_tiles) * g.tile_n;
+      int64_t mt, n0;
+      coords(t, mt, n0);
       if (!wait_phase(tfull_bar(acc), acc_ph, ctl, g.err, g.timeout_ns)) break;
       __syncwarp();
       tc_fence_after_sync();
-      const int64_t v = mt * kMxgM + quarter * 32 + lane;
-      const int cols = int(min(int64_t(g.tile_n), g.n - n0));
+      const int64_t row = mt * kMxgM + quarter * 32 + lane;
+      const bool live = row < g.rows_m;
+      const int cols = int(min(int64_t(g.tile_n), g.rows_n - n0));
       const uint32_t taddr =
           tmem + (static_cast<uint32_t>(quarter * 32) << 16) + uint32_t(acc) * uint32_t(g.tile_n);
       for (int c0 = 0; c0 < cols; c0 += 32) {
         float x[32];
         tmem_load_32cols(taddr + c0, x);
-        TO* out = static_cast<TO*>(g.out) + (n0 + c0) * g.ldo + v;
+        if (!live) continue;  // the load above is for the whole warp
+        if (capped) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (c0 + j < cols && v < g.v) {
-            float z = x[j];
-            if (capped) z = g.softcap * tanhf(z * g.inv_softcap);
-            const float one[1] = {z};
-            LnIo<TO, 1>::store(out + int64_t(j) * g.ldo, one);
+          for (int j = 0; j < 32; ++j) x[j] = g.softcap * tanhf(x[j] * g.inv_softcap);
+        }
+        if constexpr (kTokensM) {
+          // 32 consecutive logits of a token; rows start on 16 bytes, n0 + c0 is a
+          // multiple of 32.
+          TO* out = static_cast<TO*>(g.out) + row * g.ldo + n0 + c0;
+          if (c0 + 32 <= cols) {
+            if constexpr (sizeof(TO) == 2) {
+              store_bf16x32(reinterpret_cast<uint4*>(out), x, g.v8 != 0);
+            } else if (g.v8) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 8)
+                st_global_v8(out + q, __float_as_uint(x[q]), __float_as_uint(x[q + 1]),
+                             __float_as_uint(x[q + 2]), __float_as_uint(x[q + 3]),
+                             __float_as_uint(x[q + 4]), __float_as_uint(x[q + 5]),
+                             __float_as_uint(x[q + 6]), __float_as_uint(x[q + 7]));
+            } else {
+#pragma unroll
+              for (int q = 0; q < 32; q += 4)
+                *reinterpret_cast<float4*>(out + q) =
+                    make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float one[1] = {x[j]};
+              if (c0 + j < cols) LnIo<TO, 1>::store(out + j, one);
+            }
+          }
+        } else {
+          TO* out = static_cast<TO*>(g.out) + (n0 + c0) * g.ldo + row;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float one[1] = {x[j]};
+            if (c0 + j < cols) LnIo<TO, 1>::store(out + int64_t(j) * g.ldo, one);
           }
         }
       }
@@ -365,9 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename TO, int kSft>
+template <typename TO, int kSft, bool kTokensM>
 static int mx_launch_gemm(const MxGemmArgs& g, int grid, cudaStream_t cs) {
-  auto kern = mx_gemm_kernel<TO, kSft>;
+  auto kern = mx_gemm_kernel<TO, kSft, kTokensM>;
   const size_t smem = 1024 + size_t(g.stages) * mxg_stage_bytes(g.tile_n);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
       cudaSuccess)
@@ -422,32 +469,48 @@ extern "C" int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n, int64
   st = mx_quantize(*dev, hidden, dtype, n, h, ldh, a_codes, a_scales, cs);
   if (st != FLCE_OK) return st;
   MxGemmArgs g{};
-  g.n = n;
-  g.v = v;
+  const int esz = out_dtype == FLCE_F32 ? 4 : 2;
+  const int64_t ld = n > 1 ? ldo : v;
+  const bool tokens_m = n > kMxgMaxN && aligned(logits, 16) && (ld * esz) % 16 == 0;
+  const uint8_t* wc = static_cast<const uint8_t*>(w_codes);
+  const uint8_t* wsc = static_cast<const uint8_t*>(w_scales);
+  g.rows_m = tokens_m ? n : v;
+  g.rows_n = tokens_m ? v : n;
   g.h = h;
-  g.w_codes = static_cast<const uint8_t*>(w_codes);
-  g.a_codes = a_codes;
-  g.w_scales = static_cast<const uint8_t*>(w_scales);
-  g.a_scales = a_scales;
-  g.tile_n = int(std::min<int64_t>(cdiv(n, 16) * 16, kMxgMaxN));
-  if (g.tile_n > 128) g.tile_n = kMxgMaxN;  // tiles start on a multiple of 64 tokens
-  g.n_tiles = int(cdiv(n, g.tile_n));
-  g.tiles = int64_t(g.n_tiles) * cdiv(v, kMxgM);
+  g.m_codes = tokens_m ? a_codes : wc;
+  g.m_scales = tokens_m ? a_scales : wsc;
+  g.n_codes = tokens_m ? wc : a_codes;
+  g.n_scales = tokens_m ? wsc : a_scales;
+  g.tile_n = int(std::min<int64_t>(cdiv(g.rows_n, 16) * 16, kMxgMaxN));
+  if (g.tile_n > 128) g.tile_n = kMxgMaxN;  // tiles start on a multiple of 64 rows
+  g.m_tiles = cdiv(g.rows_m, kMxgM);
+  g.n_tiles = cdiv(g.rows_n, g.tile_n);
+  g.m_fast = tokens_m;  // blocks that run side by side share the head's tiles
+  g.m_stream = !tokens_m && g.n_tiles == 1;
+  g.tiles = g.m_tiles * g.n_tiles;
   const int sf_stages = (kTmemCols - 2 * g.tile_n) / (8 + 8 * mxg_scale_tiles(g.tile_n));
   g.stages = std::min({kMxgMaxStages, sf_stages, int(kMxgSmem / mxg_stage_bytes(g.tile_n))});
   g.softcap = softcap;
   g.inv_softcap = softcap > 0.0f ? 1.0f / softcap : 0.0f;
   g.out = logits;
-  g.ldo = n > 1 ? ldo : v;
+  g.ldo = ld;
+  g.v8 = aligned(logits, 32) && (ld * esz) % 32 == 0;
   g.err = dev->err;
   g.timeout_ns = kDefaultTimeoutNs;
   const int grid = int(std::min<int64_t>(g.tiles, dev->num_sms));
   const double osz = out_dtype == FLCE_F32 ? 4.0 : 2.0;
   LaunchScope scope(KF_MX_GEMM, 2.0 * double(n) * double(h) * double(v),
                     double(n + v) * double(h) * 17.0 / 32.0 + osz * double(n) * double(v), cs);
-  if (mxg_scale_tiles(g.tile_n) == 1)
-    return out_dtype == FLCE_BF16 ? mx_launch_gemm<__nv_bfloat16, 1>(g, grid, cs)
-                                  : mx_launch_gemm<float, 1>(g, grid, cs);
-  return out_dtype == FLCE_BF16 ? mx_launch_gemm<__nv_bfloat16, 2>(g, grid, cs)
-                                : mx_launch_gemm<float, 2>(g, grid, cs);
+  const bool bf = out_dtype == FLCE_BF16;
+  if (tokens_m && g.tile_n > 128)
+    return bf ? mx_launch_gemm<__nv_bfloat16, 2, true>(g, grid, cs)
+              : mx_launch_gemm<float, 2, true>(g, grid, cs);
+  if (tokens_m)  // a vocabulary of 128 entries at most
+    return bf ? mx_launch_gemm<__nv_bfloat16, 1, true>(g, grid, cs)
+              : mx_launch_gemm<float, 1, true>(g, grid, cs);
+  if (g.tile_n > 128)
+    return bf ? mx_launch_gemm<__nv_bfloat16, 2, false>(g, grid, cs)
+              : mx_launch_gemm<float, 2, false>(g, grid, cs);
+  return bf ? mx_launch_gemm<__nv_bfloat16, 1, false>(g, grid, cs)
+            : mx_launch_gemm<float, 1, false>(g, grid, cs);
 }

@@ -104,15 +104,18 @@ def test_logits_every_tail_of_k(dev, h):
     _check_logits(hidden, weight, got, 0.0)
 
 
-def test_logits_many_tiles_per_block(dev):
-    """More head tiles than SMs and several token tiles: the rings wrap many times."""
+@pytest.mark.parametrize("n", [150, 500, 1300])
+@pytest.mark.parametrize("v,out", [(20011, torch.float32), (20016, torch.float32), (20012, torch.bfloat16),
+                                   (20016, torch.bfloat16), (100, torch.bfloat16)])
+def test_logits_many_tiles_per_block(dev, n, v, out):
+    """More tiles than SMs: the rings wrap many times; rows of every alignment."""
     g = torch.Generator().manual_seed(3)
-    hidden = torch.randn(500, 320, generator=g).to(torch.bfloat16)
-    weight = torch.randn(20011, 320, generator=g).to(torch.bfloat16)
-    got = flce.mxfp4_logits(hidden.to(dev), flce.mxfp4_quantize(weight.to(dev)), dtype=torch.float32)
+    hidden = torch.randn(n, 320, generator=g).to(torch.bfloat16)
+    weight = torch.randn(v, 320, generator=g).to(torch.bfloat16)
+    got = flce.mxfp4_logits(hidden.to(dev), flce.mxfp4_quantize(weight.to(dev)), dtype=out)
     a = flce.mxfp4_dequantize(flce.mxfp4_quantize(hidden.to(dev)), torch.float32).double()
     w = flce.mxfp4_dequantize(flce.mxfp4_quantize(weight.to(dev)), torch.float32).double()
-    tol = (320 * 2.0 ** -23 + 2.0 ** -24) * (a.abs() @ w.abs().t())
+    tol = HALF[out] * (a @ w.t()).abs() + 320 * 2.0 ** -23 * (a.abs() @ w.abs().t())
     assert torch.all((got.double() - a @ w.t()).abs() <= tol)
 
 
