@@ -263,6 +263,7 @@ struct DeviceInfo {
   int status = FLCE_OK;
   int num_sms = 0;
   int max_pairs = 0;  // CTA pairs of the pair GEMM that fit at once (0 = not yet queried)
+  int mx_pairs = 0;   // ... of the MXFP4 pair product
   int ce_blocks[4] = {};  // resident CTAs per SM of the CE kernels (0 = not yet queried)
   unsigned* err = nullptr;
 };

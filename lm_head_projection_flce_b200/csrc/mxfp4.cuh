@@ -91,6 +91,7 @@ struct MxQuantArgs {
 // kVec: rows start on 16 bytes and hold whole vectors of 8.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const MxQuantArgs a) {
+  grid_launch_dependents();  // the product's set-up; it waits for this grid's end itself
   const int lane = threadIdx.x & 31;
   const int64_t warps = int64_t(gridDim.x) * (kMxThreads / 32);
   const int64_t blocks = mx_blocks(a.cols), ctiles = mx_ctiles(a.cols), ktiles = 2 * ctiles;

@@ -5,15 +5,17 @@
 // itself (tcgen05.mma kind::mxf4, one E8M0 scale per 32 elements), with FP32
 // accumulation in tensor memory.
 //
-// Which operand is the M side (128 rows of a tile) and which the N side (16 to
-// 192 columns) depends on the tokens.  Few (up to 192): the head is the M side, so its
-// codes, which are nearly all of the traffic, fill whole tiles while N shrinks
-// to the tokens that exist; the kernel is bound by HBM, the head is read once.
-// Many: the tokens are the M side, so a thread of the epilogue holds consecutive
-// logits of one token and stores 32 bytes at a time; lanes that hold consecutive
-// logits store 2 bytes each, which took longer than the product (1205 us against
-// XX at 4096 x 4096 x 128256).  Rows of logits that do not start on 16 bytes need
-// the first form whatever the tokens.
+// Two kernels.  Few tokens (up to 192): the head's rows are the M side of a tile
+// (128), so its codes, which are nearly all of the traffic, fill whole tiles,
+// and the tokens are the N side (16 to 192), which shrinks to those that exist;
+// the head is read once and the kernel is bound by HBM.  Many tokens: CTA pairs
+// and tiles of 256 tokens x 256 head rows (mx_gemm_pair_kernel, below), bound by
+// the tensor core.  There a thread of the epilogue holds consecutive logits of
+// one token and stores 32 bytes at a time; with the head on the M side its lanes
+// hold consecutive logits and store 2 bytes each, which at 4096 tokens took
+// longer than the product (1205 against 890 us, both on single CTAs).
+// Rows of logits that do not start on 16 bytes take the first kernel whatever
+// the tokens, as its stores join across lanes.
 //
 // Warp 0 loads: per stage of 256 elements of K the head's tile of codes (16 KB),
 // the tokens' rows of theirs, and both operands' scale tiles, each a contiguous
@@ -44,14 +46,13 @@ struct MxGemmArgs {
   const uint8_t* n_scales;
   int tile_n;         // N rows per tile, a multiple of 16 (of 64 where there are several)
   int64_t m_tiles, n_tiles;
-  int m_fast;         // M tiles of one N tile follow one another, else the reverse
   int m_stream;       // the M side's codes are read once: they need not stay in L2
   int64_t tiles;
   int stages;
   float softcap, inv_softcap;
   void* out;
   int64_t ldo;
-  int v8;             // kTokensM: rows of logits start on 32 bytes
+  int v8;             // rows of logits start on 32 bytes
   unsigned* err;
   uint64_t timeout_ns;
 };
@@ -67,6 +68,13 @@ __device__ __forceinline__ void tmem_relinquish_one() {
 __device__ __forceinline__ void tmem_dealloc_one(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
+}
+// wait_phase by a whole warp, with one answer for all its lanes: a wait that ran
+// out in one lane must not leave the others at a warp-wide instruction.
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, PipeCtl* ctl,
+                                          unsigned* err, uint64_t timeout_ns) {
+  return __all_sync(0xffffffffu, wait_phase<kCluster>(bar, parity, ctl, err, timeout_ns)) != 0;
 }
 // True in one lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
@@ -131,8 +139,7 @@ __host__ __device__ __forceinline__ uint32_t mxg_stage_bytes(int tile_n) {
 }
 
 // kSft: scale tiles of 128 rows that a tile's N side touches (2 above 128 rows).
-// kTokensM: the tokens are the M side.
-template <typename TO, int kSft, bool kTokensM>
+template <typename TO, int kSft>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const MxGemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
@@ -156,10 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t blocks = mx_blocks(g.h);
   const int num_kb = int(mx_ctiles(g.h));
   const int64_t n_row_tiles = (g.rows_n + kMxTileRows - 1) / kMxTileRows;
+  // The token tiles of a head tile follow one another, and share it in L2.
   auto coords = [&](int64_t t, int64_t& mt, int64_t& n0) {
-    const int64_t fast = g.m_fast ? g.m_tiles : g.n_tiles, q = t / fast, r = t - q * fast;
-    mt = g.m_fast ? r : q;
-    n0 = (g.m_fast ? q : r) * g.tile_n;
+    mt = t / g.n_tiles;
+    n0 = (t - mt * g.n_tiles) * g.tile_n;
   };
 
   if (threadIdx.x == 0) {
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint8_t* nc1 = g.n_codes + (bt + 1) * num_kb * kMxCodeBytes;
       const uint8_t* ns1 = ns + num_kb * (2 * kMxTileBytes);
       for (int kb = 0; kb < num_kb; ++kb) {
-        if (!wait_phase(full + 8u * kMxgMaxStages, ph ^ 1u, ctl, g.err, g.timeout_ns)) {
+        if (!wait_warp(full + 8u * kMxgMaxStages, ph ^ 1u, ctl, g.err, g.timeout_ns)) {
           ok = false;
           break;
         }
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t mt, n0;
       coords(t, mt, n0);
       const uint32_t shift = uint32_t(n0 % kMxTileRows) / 32u;  // first N row's scale column
-      if (!wait_phase(tempty_bar(acc), acc_ph ^ 1u, ctl, g.err, g.timeout_ns)) {
+      if (!wait_warp(tempty_bar(acc), acc_ph ^ 1u, ctl, g.err, g.timeout_ns)) {
         ok = false;
         break;
       }
@@ -286,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int left = int(blocks);  // scale blocks still to multiply
       uint32_t more = 0;
       for (int kb = 0; kb < num_kb; ++kb) {
-        if (!wait_phase(full, ph, ctl, g.err, g.timeout_ns)) {
+        if (!wait_warp(full, ph, ctl, g.err, g.timeout_ns)) {
           ok = false;
           break;
         }
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t t = blockIdx.x; t < g.tiles; t += gridDim.x) {
       int64_t mt, n0;
       coords(t, mt, n0);
-      if (!wait_phase(tfull_bar(acc), acc_ph, ctl, g.err, g.timeout_ns)) break;
+      if (!wait_warp(tfull_bar(acc), acc_ph, ctl, g.err, g.timeout_ns)) break;
       __syncwarp();
       tc_fence_after_sync();
       const int64_t row = mt * kMxgM + quarter * 32 + lane;
@@ -360,40 +367,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) x[j] = g.softcap * tanhf(x[j] * g.inv_softcap);
         }
-        if constexpr (kTokensM) {
-          // 32 consecutive logits of a token; rows start on 16 bytes, n0 + c0 is a
-          // multiple of 32.
-          TO* out = static_cast<TO*>(g.out) + row * g.ldo + n0 + c0;
-          if (c0 + 32 <= cols) {
-            if constexpr (sizeof(TO) == 2) {
-              store_bf16x32(reinterpret_cast<uint4*>(out), x, g.v8 != 0);
-            } else if (g.v8) {
+        TO* out = static_cast<TO*>(g.out) + (n0 + c0) * g.ldo + row;
 #pragma unroll
-              for (int q = 0; q < 32; q += 8)
-                st_global_v8(out + q, __float_as_uint(x[q]), __float_as_uint(x[q + 1]),
-                             __float_as_uint(x[q + 2]), __float_as_uint(x[q + 3]),
-                             __float_as_uint(x[q + 4]), __float_as_uint(x[q + 5]),
-                             __float_as_uint(x[q + 6]), __float_as_uint(x[q + 7]));
-            } else {
-#pragma unroll
-              for (int q = 0; q < 32; q += 4)
-                *reinterpret_cast<float4*>(out + q) =
-                    make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float one[1] = {x[j]};
-              if (c0 + j < cols) LnIo<TO, 1>::store(out + j, one);
-            }
-          }
-        } else {
-          TO* out = static_cast<TO*>(g.out) + (n0 + c0) * g.ldo + row;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float one[1] = {x[j]};
-            if (c0 + j < cols) LnIo<TO, 1>::store(out + int64_t(j) * g.ldo, one);
-          }
+        for (int j = 0; j < 32; ++j) {
+          const float one[1] = {x[j]};
+          if (c0 + j < cols) LnIo<TO, 1>::store(out + int64_t(j) * g.ldo, one);
         }
       }
       tc_fence_before_sync();
@@ -412,14 +390,344 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename TO, int kSft, bool kTokensM>
+template <typename TO, int kSft>
 static int mx_launch_gemm(const MxGemmArgs& g, int grid, cudaStream_t cs) {
-  auto kern = mx_gemm_kernel<TO, kSft, kTokensM>;
+  auto kern = mx_gemm_kernel<TO, kSft>;
   const size_t smem = 1024 + size_t(g.stages) * mxg_stage_bytes(g.tile_n);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
       cudaSuccess)
     return FLCE_ERR_CUDA;
-  kern<<<grid, kThreads, smem, cs>>>(g);
+  return launch_dependent(kern, dim3(unsigned(grid)), dim3(kThreads), smem, cs, g);
+}
+
+// ---------------------------------------------------------------- CTA pairs
+// A cluster of two CTAs on neighbouring SMs multiplies tiles of 256 tokens x 256
+// head rows (tcgen05.mma.cta_group::2): CTA r holds token rows [128 r, 128 r +
+// 128) and head rows [128 r, 128 r + 128) of a tile, one tile of codes each per
+// stage, and the scales of its own tokens and of all 256 head rows.  Per MMA a
+// single CTA's 128 x 192 tile moves 1.6 times the bytes through shared memory per
+// product, more than the tensor core leaves time for.  256 accumulator
+// columns and the scales (24 columns per stage, 6 stages) leave no room for a
+// second accumulator, so eight epilogue warps empty it into registers at once
+// (128 columns each) and store while the next tile is multiplied.
+constexpr int kMxpStages = 6;
+constexpr int kMxpN = 256;
+constexpr int kMxpEpiWarps = 8;
+constexpr int kMxpThreads = 64 + 32 * kMxpEpiWarps;
+constexpr uint32_t kMxpOffB = kMxCodeBytes;
+constexpr uint32_t kMxpOffSfa = 2 * kMxCodeBytes;
+constexpr uint32_t kMxpOffSfb = kMxpOffSfa + 2 * kMxTileBytes;
+constexpr uint32_t kMxpStageBytes = kMxpOffSfb + 4 * kMxTileBytes;  // 35 KB
+constexpr size_t kMxpSmem = 1024 + size_t(kMxpStages) * kMxpStageBytes;
+static_assert(kMxpN + kMxpStages * 24 <= kTmemCols, "accumulator and scales in tensor memory");
+
+__device__ __forceinline__ void tc_copy_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                                 uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
+      "p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+struct __align__(64) MxPairMaps {
+  // Codes as rows of 128 bytes, 128 rows per tile; scales as rows of 128 bytes,
+  // 8 rows per tile of codes.  No swizzle: the codes are stored swizzled.
+  CUtensorMap m_codes, m_scales, n_codes, n_scales;
+};
+
+template <typename TO>
+__global__ void __launch_bounds__(kMxpThreads, 1)
+    mx_gemm_pair_kernel(const __grid_constant__ MxPairMaps maps, const MxGemmArgs g) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kMxpStages + 3];
+  __shared__ uint32_t tmem_slot;
+  __shared__ PipeCtl ctl_s;
+  PipeCtl* ctl = &ctl_s;
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t bar_base = smem_u32(bars);
+  const uint32_t rank = cluster_cta_rank();
+  const uint32_t leader_bars = map_shared_to_rank(bar_base, 0);
+  constexpr uint32_t kEmpty = 8u * kMxpStages;
+  const uint32_t tfull = bar_base + 16u * kMxpStages, tempty = tfull + 8u, drain_bar = tfull + 16u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int num_kb = int(mx_ctiles(g.h));
+  const int64_t m_row_tiles = (g.rows_m + kMxTileRows - 1) / kMxTileRows;
+  const int64_t n_row_tiles = (g.rows_n + kMxTileRows - 1) / kMxTileRows;
+  const int64_t pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMxpStages; ++s) {
+      mbar_init(bar_base + 8u * s, 1);
+      mbar_init(bar_base + kEmpty + 8u * s, 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 2 * kMxpEpiWarps);
+    mbar_init(drain_bar, 1);
+    ctl->abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&maps.m_codes);
+    tma_prefetch_desc(&maps.m_scales);
+    tma_prefetch_desc(&maps.n_codes);
+    tma_prefetch_desc(&maps.n_scales);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync_all();  // the peer's barriers exist before anyone signals them
+  tc_fence_after_sync();
+  grid_dependency_wait();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    // -------------------------------------------------- loads (both CTAs)
+    const bool leader = elect_one();
+    const uint64_t pol = l2_policy_evict_normal();
+    int st = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int64_t t = first; ok && t < g.tiles; t += pairs) {
+      // The token tiles of a head tile follow one another, and share it in L2.
+      const int64_t nt = t / g.m_tiles, mt = t - nt * g.m_tiles;
+      // Row tiles that exist: token tile 2 mt + 1 and head tile 2 nt + 1 may not.
+      const int ma = 2 * mt + 1 < m_row_tiles ? 2 : 1, nb = 2 * nt + 1 < n_row_tiles ? 2 : 1;
+      const bool have_a = int(rank) < ma, have_b = int(rank) < nb;
+      const uint32_t expect = uint32_t(ma) * (kMxCodeBytes + 2 * kMxTileBytes) +
+                              uint32_t(nb) * (kMxCodeBytes + 4 * kMxTileBytes);
+      int am = int((2 * mt + rank) * num_kb), bn = int((2 * nt + rank) * num_kb);
+      int b0 = int(2 * nt * num_kb);
+      for (int kb = 0; kb < num_kb; ++kb, ++am, ++bn, ++b0) {
+        if (!wait_warp(bar_base + kEmpty + 8u * st, ph ^ 1u, ctl, g.err, g.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        const uint32_t base = smem_base + uint32_t(st) * kMxpStageBytes;
+        const uint32_t full = leader_bars + 8u * st;  // counts both CTAs' bytes
+        if (leader) {
+          if (rank == 0) mbar_arrive_expect_tx(bar_base + 8u * st, expect);
+          if (have_a) {
+            tma_load_2d_pair_hint(base, &maps.m_codes, full, 0, am * 128, pol);
+            tma_load_2d_pair_hint(base + kMxpOffSfa, &maps.m_scales, full, 0, am * 8, pol);
+          }
+          if (have_b) tma_load_2d_pair_hint(base + kMxpOffB, &maps.n_codes, full, 0, bn * 128, pol);
+          tma_load_2d_pair_hint(base + kMxpOffSfb, &maps.n_scales, full, 0, b0 * 8, pol);
+          if (nb == 2)
+            tma_load_2d_pair_hint(base + kMxpOffSfb + 2 * kMxTileBytes, &maps.n_scales, full, 0,
+                                  (b0 + num_kb) * 8, pol);
+        }
+        __syncwarp();
+        if (++st == kMxpStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      // Copies this warp started signal the leader's barriers; give them time to
+      // land before the CTA can exit.
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 200000ull) {
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ------------------------------------------------ scales and MMAs of both CTAs
+      const bool leader = elect_one();
+      constexpr uint32_t idesc = mma_idesc_mxf4(2 * kMxgM, kMxpN);
+      constexpr uint32_t kIdOdd = (2u << 4) | (2u << 29);  // bytes 2, 3 of the scale words
+      constexpr uint64_t hi = desc_hi_sw128(16u, 1024u);
+      constexpr uint64_t kTile = kMxTileBytes >> 4;
+      const uint64_t da0 = hi | static_cast<uint64_t>((smem_base & 0x3FFFFu) >> 4);
+      const uint64_t dsa0 = mx_scale_desc(smem_base + kMxpOffSfa);
+      const uint32_t sf0 = tmem + kMxpN;
+      int st = 0;
+      uint32_t ph = 0, acc_ph = 0, sfa = sf0;
+      uint64_t da = da0, dsa = dsa0;
+      bool ok = true;
+      const int blocks = int(mx_blocks(g.h));
+      for (int64_t t = first; ok && t < g.tiles; t += pairs) {
+        if (!wait_warp<true>(tempty, acc_ph ^ 1u, ctl, g.err, g.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        acc_ph ^= 1u;
+        tc_fence_after_sync();
+        int left = blocks;
+        uint32_t more = 0;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!wait_warp(bar_base + 8u * st, ph, ctl, g.err, g.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          if (leader) {
+            const uint32_t sfb = sfa + 8u;
+            const uint64_t dsb = dsa + ((kMxpOffSfb - kMxpOffSfa) >> 4);
+            tc_copy_scales_pair(sfa, dsa);
+            tc_copy_scales_pair(sfa + 4u, dsa + kTile);
+            tc_copy_scales_pair(sfb, dsb);
+            tc_copy_scales_pair(sfb + 4u, dsb + 2 * kTile);
+            tc_copy_scales_pair(sfb + 8u, dsb + kTile);
+            tc_copy_scales_pair(sfb + 12u, dsb + 3 * kTile);
+            const uint64_t db = da + (kMxpOffB >> 4);
+            tc_mma_mxf4_pair(tmem, da, db, idesc, sfa, sfb, more);
+            if (left > 2) tc_mma_mxf4_pair(tmem, da + 2, db + 2, idesc | kIdOdd, sfa, sfb, 1u);
+            if (left > 4) tc_mma_mxf4_pair(tmem, da + 4, db + 4, idesc, sfa + 4u, sfb + 8u, 1u);
+            if (left > 6)
+              tc_mma_mxf4_pair(tmem, da + 6, db + 6, idesc | kIdOdd, sfa + 4u, sfb + 8u, 1u);
+            tc_commit_pair_mc(bar_base + kEmpty + 8u * st, 0x3);
+          }
+          __syncwarp();
+          more = 1u;
+          left -= kMxgBlocks;
+          sfa += 24u;
+          da += kMxpStageBytes >> 4;
+          dsa += kMxpStageBytes >> 4;
+          if (++st == kMxpStages) {
+            st = 0;
+            ph ^= 1u;
+            sfa = sf0;
+            da = da0;
+            dsa = dsa0;
+          }
+        }
+        if (!ok) break;
+        if (leader) tc_commit_pair_mc(tfull, 0x3);
+        __syncwarp();
+      }
+      if (leader) tc_commit_pair_mc(drain_bar, 0x1);
+      __syncwarp();
+      drain_wait(drain_bar, 0, ok ? g.timeout_ns : 100000000ull);
+    }
+  } else {
+    // -------------------------------------------------- epilogue: lanes are tokens
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + uint32_t(half) * 128u;
+    const uint32_t leader_tempty = map_shared_to_rank(tempty, 0);
+    const bool capped = g.softcap > 0.0f;
+    uint32_t acc_ph = 0;
+    for (int64_t t = first; t < g.tiles; t += pairs) {
+      const int64_t nt = t / g.m_tiles, mt = t - nt * g.m_tiles;
+      if (!wait_warp(tfull, acc_ph, ctl, g.err, g.timeout_ns)) break;
+      acc_ph ^= 1u;
+      __syncwarp();
+      tc_fence_after_sync();
+      float x[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_load_32cols(taddr + 32u * q, x[q]);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(leader_tempty);
+      const int64_t row = (2 * mt + rank) * kMxgM + quarter * 32 + lane;
+      if (row >= g.rows_m) continue;
+      const int64_t c0 = nt * kMxpN + half * 128;
+      // 128 consecutive logits of a token; rows start on 16 bytes.
+      TO* out = static_cast<TO*>(g.out) + row * g.ldo + c0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t left = g.rows_n - (c0 + 32 * q);
+        if (left <= 0) break;
+        if (capped) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[q][j] = g.softcap * tanhf(x[q][j] * g.inv_softcap);
+        }
+        if (left >= 32) {
+          if constexpr (sizeof(TO) == 2) {
+            store_bf16x32(reinterpret_cast<uint4*>(out + 32 * q), x[q], g.v8 != 0);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              if (g.v8) {
+                st_global_v8(out + 32 * q + j, __float_as_uint(x[q][j]), __float_as_uint(x[q][j + 1]),
+                             __float_as_uint(x[q][j + 2]), __float_as_uint(x[q][j + 3]),
+                             __float_as_uint(x[q][j + 4]), __float_as_uint(x[q][j + 5]),
+                             __float_as_uint(x[q][j + 6]), __float_as_uint(x[q][j + 7]));
+              } else {
+                *reinterpret_cast<float4*>(out + 32 * q + j) =
+                    make_float4(x[q][j], x[q][j + 1], x[q][j + 2], x[q][j + 3]);
+                *reinterpret_cast<float4*>(out + 32 * q + j + 4) =
+                    make_float4(x[q][j + 4], x[q][j + 5], x[q][j + 6], x[q][j + 7]);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float one[1] = {x[q][j]};
+            if (j < left) LnIo<TO, 1>::store(out + 32 * q + j, one);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync_all();  // the leader's MMAs into this CTA's tensor memory are done
+  tc_fence_after_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// `tiles` tiles of box_rows rows of 128 bytes.
+static bool mx_tmap(CUtensorMap* tm, const void* base, int64_t tiles, int box_rows) {
+  cuuint64_t dims[2] = {128, cuuint64_t(tiles) * cuuint64_t(box_rows)};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t box[2] = {128, cuuint32_t(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename TO>
+static int mx_launch_pair(const MxGemmArgs& g, DeviceInfo& dev, cudaStream_t cs) {
+  auto kern = mx_gemm_pair_kernel<TO>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMxpSmem)) !=
+      cudaSuccess)
+    return FLCE_ERR_CUDA;
+  const int64_t kb = mx_ctiles(g.h);
+  const int64_t mt = cdiv(g.rows_m, kMxTileRows) * kb, nt = cdiv(g.rows_n, kMxTileRows) * kb;
+  MxPairMaps maps;
+  if (!mx_tmap(&maps.m_codes, g.m_codes, mt, 128) || !mx_tmap(&maps.m_scales, g.m_scales, mt, 8) ||
+      !mx_tmap(&maps.n_codes, g.n_codes, nt, 128) || !mx_tmap(&maps.n_scales, g.n_scales, nt, 8))
+    return FLCE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kMxpThreads, 1, 1);
+  cfg.dynamicSmemBytes = kMxpSmem;
+  cfg.stream = cs;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int pairs = dev.mx_pairs;
+  if (pairs == 0) {  // pairs that can be resident at once, queried once per device
+    cfg.gridDim = dim3(2 * (dev.num_sms / 2), 1, 1);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = dev.num_sms / 2;
+    pairs = std::min(n, dev.num_sms / 2);
+    std::lock_guard<std::mutex> lock(g_mutex);
+    dev.mx_pairs = pairs;
+  }
+  cfg.gridDim = dim3(unsigned(2 * std::min<int64_t>(pairs, g.tiles)), 1, 1);
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, maps, g) != cudaSuccess) return FLCE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 
@@ -483,9 +791,9 @@ extern "C" int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n, int64
   g.n_scales = tokens_m ? wsc : a_scales;
   g.tile_n = int(std::min<int64_t>(cdiv(g.rows_n, 16) * 16, kMxgMaxN));
   if (g.tile_n > 128) g.tile_n = kMxgMaxN;  // tiles start on a multiple of 64 rows
-  g.m_tiles = cdiv(g.rows_m, kMxgM);
+  if (tokens_m) g.tile_n = kMxpN;
+  g.m_tiles = cdiv(g.rows_m, tokens_m ? 2 * kMxgM : kMxgM);
   g.n_tiles = cdiv(g.rows_n, g.tile_n);
-  g.m_fast = tokens_m;  // blocks that run side by side share the head's tiles
   g.m_stream = !tokens_m && g.n_tiles == 1;
   g.tiles = g.m_tiles * g.n_tiles;
   const int sf_stages = (kTmemCols - 2 * g.tile_n) / (8 + 8 * mxg_scale_tiles(g.tile_n));
@@ -502,15 +810,15 @@ extern "C" int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n, int64
   LaunchScope scope(KF_MX_GEMM, 2.0 * double(n) * double(h) * double(v),
                     double(n + v) * double(h) * 17.0 / 32.0 + osz * double(n) * double(v), cs);
   const bool bf = out_dtype == FLCE_BF16;
-  if (tokens_m && g.tile_n > 128)
-    return bf ? mx_launch_gemm<__nv_bfloat16, 2, true>(g, grid, cs)
-              : mx_launch_gemm<float, 2, true>(g, grid, cs);
-  if (tokens_m)  // a vocabulary of 128 entries at most
-    return bf ? mx_launch_gemm<__nv_bfloat16, 1, true>(g, grid, cs)
-              : mx_launch_gemm<float, 1, true>(g, grid, cs);
+  if (tokens_m) {
+    // coordinates of the tensor maps are 32-bit
+    if ((cdiv(std::max(n, v), kMxTileRows) + 2) * mx_ctiles(h) * 128 > kMaxDim)
+      return FLCE_ERR_UNSUPPORTED;
+    return bf ? mx_launch_pair<__nv_bfloat16>(g, *dev, cs) : mx_launch_pair<float>(g, *dev, cs);
+  }
   if (g.tile_n > 128)
-    return bf ? mx_launch_gemm<__nv_bfloat16, 2, false>(g, grid, cs)
-              : mx_launch_gemm<float, 2, false>(g, grid, cs);
-  return bf ? mx_launch_gemm<__nv_bfloat16, 1, false>(g, grid, cs)
-            : mx_launch_gemm<float, 1, false>(g, grid, cs);
+    return bf ? mx_launch_gemm<__nv_bfloat16, 2>(g, grid, cs)
+              : mx_launch_gemm<float, 2>(g, grid, cs);
+  return bf ? mx_launch_gemm<__nv_bfloat16, 1>(g, grid, cs)
+            : mx_launch_gemm<float, 1>(g, grid, cs);
 }
