@@ -215,6 +215,180 @@ __global__ void __launch_bounds__(ln_block(VN * NV, kWarpRow))
   }
 }
 
+// ---------------------------------------------------------------- rows through a ring
+// With more rows than blocks a block that loads a row, reduces it and stores it
+// leaves HBM idle between its loads (195 + 280 us forward + backward of 16384
+// rows of 8192, 2.8 TB/s).  So one block (or 512 / tpr of them) per SM streams
+// its rows through a ring of shared-memory slots with bulk copies, several rows
+// ahead; a slot is refilled right after the first barrier of the row that used
+// it.  A thread's columns, weights and gradient sums stay in registers.
+//
+// Rows that do not start or end on 16 bytes are copied with the bytes around them,
+// up to the boundaries; these belong to neighbouring rows or the gaps between
+// rows.  The tensor's first and last row, whose surroundings belong to somebody
+// else, are loaded directly instead.
+constexpr int kLnSlots = 8;                  // rows in flight per block, at most
+constexpr int kLnRingBytes = 192 * 1024;     // per SM
+
+struct LnRing {
+  int slots;
+  uint32_t slot_bytes;   // per tensor
+  unsigned* err;
+  uint64_t timeout_ns;
+};
+
+struct LnRingRow {
+  const uint8_t* begin;  // 16-byte aligned start of the copy
+  uint32_t bytes;
+  uint32_t phase;        // offset of the row's first element in it
+  bool direct;
+};
+template <typename T>
+__device__ __forceinline__ LnRingRow ln_ring_row(const void* base, int64_t ld, int64_t n, int64_t h,
+                                                 int64_t r) {
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(static_cast<const T*>(base) + r * ld);
+  LnRingRow row;
+  row.phase = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15);
+  row.begin = p - row.phase;
+  const uint32_t len = row.phase + static_cast<uint32_t>(h * int64_t(sizeof(T)));
+  row.bytes = (len + 15u) & ~15u;
+  row.direct = (r == 0 && row.phase != 0) || (r == n - 1 && row.bytes != len);
+  return row;
+}
+// A thread's share of row r: from the ring's slot or, for a direct row, from global memory.
+template <typename T, int VN, int NV>
+__device__ __forceinline__ void ln_ring_read(const uint8_t* slot, const LnRingRow& row, int64_t h,
+                                             float (&v)[NV][VN]) {
+  auto from = [&](const T* src) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t(i) * blockDim.x + threadIdx.x) * VN;
+      if (c < h) {
+        LnIo<T, VN>::load(src + c, v[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VN; ++j) v[i][j] = 0.0f;
+      }
+    }
+  };
+  if constexpr (VN == 1) {  // wider vectors: whole rows of 16-byte pieces, never direct
+    if (row.direct) {
+      from(reinterpret_cast<const T*>(row.begin + row.phase));
+      return;
+    }
+    from(reinterpret_cast<const T*>(slot + row.phase));
+  } else {
+    from(reinterpret_cast<const T*>(slot));
+  }
+}
+
+// Two rows at a time: both sums of a reduction travel together.
+template <typename T, typename W, int VN, int NV>
+__global__ void __launch_bounds__(kLnMaxThreads, 1)
+    ln_forward_ring_kernel(const LnArgs a, const LnRing g) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(8) uint64_t full[kLnSlots];
+  __shared__ float2 red[2][32];
+  __shared__ PipeCtl ctl;
+  const int t = threadIdx.x, tpr = blockDim.x;
+  const int64_t count = (a.n - blockIdx.x + gridDim.x - 1) / gridDim.x;  // this block's rows
+  auto row_at = [&](int64_t i) {
+    return ln_ring_row<T>(a.x, a.ldx, a.n, a.h, int64_t(blockIdx.x) + i * gridDim.x);
+  };
+  auto issue = [&](int64_t i) {
+    if (i >= count) return;
+    const LnRingRow row = row_at(i);
+    const int s = int(i % g.slots);
+    const uint32_t bar = smem_u32(&full[s]);
+    if (row.direct) {
+      mbar_arrive(bar);  // keeps the slot's phases in step
+    } else {
+      mbar_arrive_expect_tx(bar, row.bytes);
+      bulk_load(smem_u32(ring) + uint32_t(s) * g.slot_bytes, row.begin, row.bytes, bar);
+    }
+  };
+  if (t == 0) {
+    for (int s = 0; s < g.slots; ++s) mbar_init(smem_u32(&full[s]), 1);
+    ctl.abort = 0;
+    fence_barrier_init();
+    for (int s = 0; s < g.slots; ++s) issue(s);
+  }
+  float w[NV][VN], b[NV][VN];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = (int64_t(i) * tpr + t) * VN;
+#pragma unroll
+    for (int j = 0; j < VN; ++j) {
+      w[i][j] = 1.0f;
+      b[i][j] = 0.0f;
+    }
+    if (a.w && c < a.h) LnIo<W, VN>::load(static_cast<const W*>(a.w) + c, w[i]);
+    if (a.b && c < a.h) LnIo<W, VN>::load(static_cast<const W*>(a.b) + c, b[i]);
+  }
+  __syncthreads();
+  const float inv_h = 1.0f / float(a.h);
+  int buf = 0;
+  auto fetch = [&](int64_t i, float (&v)[NV][VN]) {
+    const int s = int(i % g.slots);
+    // A wait that ran out is recorded and the row's result lost; the loop ends as usual.
+    wait_phase(smem_u32(&full[s]), uint32_t(i / g.slots) & 1u, &ctl, g.err, g.timeout_ns);
+    ln_ring_read<T, VN, NV>(ring + uint32_t(s) * g.slot_bytes, row_at(i), a.h, v);
+  };
+  auto finish = [&](int64_t i, float (&v)[NV][VN], float mean, float rstd) {
+    const int64_t r = int64_t(blockIdx.x) + i * gridDim.x;
+    if (t == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
+    T* y = static_cast<T*>(a.y) + r * a.ldy;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int64_t c = (int64_t(k) * tpr + t) * VN;
+      if (c < a.h) {
+#pragma unroll
+        for (int j = 0; j < VN; ++j) v[k][j] = v[k][j] * rstd * w[k][j] + b[k][j];
+        LnIo<T, VN>::store(y + c, v[k]);
+      }
+    }
+  };
+  for (int64_t i = 0; i < count; i += 2) {
+    const bool two = i + 1 < count;
+    float v0[NV][VN], v1[NV][VN];
+    fetch(i, v0);
+    if (two) fetch(i + 1, v1);
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int j = 0; j < VN; ++j) {
+        if (!two) v1[k][j] = 0.0f;
+        s.x += v0[k][j];
+        s.y += v1[k][j];
+      }
+    s = ln_row_sum<false>(s, red, buf);
+    if (t == 0) {
+      issue(i + g.slots);
+      if (two) issue(i + 1 + g.slots);
+    }
+    const float m0 = s.x * inv_h, m1 = s.y * inv_h;
+    s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const bool in = (int64_t(k) * tpr + t) * VN < a.h;
+#pragma unroll
+      for (int j = 0; j < VN; ++j) {
+        v0[k][j] = in ? v0[k][j] - m0 : 0.0f;
+        v1[k][j] = in ? v1[k][j] - m1 : 0.0f;
+        s.x += v0[k][j] * v0[k][j];
+        s.y += v1[k][j] * v1[k][j];
+      }
+    }
+    s = ln_row_sum<false>(s, red, buf);
+    finish(i, v0, m0, 1.0f / sqrtf(s.x * inv_h + a.eps));
+    if (two) finish(i + 1, v1, m1, 1.0f / sqrtf(s.y * inv_h + a.eps));
+  }
+}
+
 // Rows too long for the registers of one block: three looks at the row, the
 // later ones from L2.
 template <typename T, typename W>
@@ -352,6 +526,110 @@ __global__ void __launch_bounds__(ln_block(VN * NV, kWarpRow))
   }
 }
 
+// The backward through the ring: a slot holds the row of x and the row of dy.
+template <typename T, typename W, int VN, int NV>
+__global__ void __launch_bounds__(kLnMaxThreads, 1)
+    ln_backward_ring_kernel(const LnBwdArgs a, const LnRing g) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(8) uint64_t full[kLnSlots];
+  __shared__ float2 red[2][32];
+  __shared__ PipeCtl ctl;
+  const int t = threadIdx.x, tpr = blockDim.x;
+  const int64_t count = (a.n - blockIdx.x + gridDim.x - 1) / gridDim.x;
+  auto row_of = [&](int64_t i) { return int64_t(blockIdx.x) + i * gridDim.x; };
+  auto issue = [&](int64_t i) {
+    if (i >= count) return;
+    const LnRingRow rx = ln_ring_row<T>(a.x, a.ldx, a.n, a.h, row_of(i));
+    const LnRingRow rd = ln_ring_row<T>(a.dy, a.lddy, a.n, a.h, row_of(i));
+    const int s = int(i % g.slots);
+    const uint32_t bar = smem_u32(&full[s]), at = smem_u32(ring) + uint32_t(s) * 2u * g.slot_bytes;
+    const uint32_t bytes = (rx.direct ? 0u : rx.bytes) + (rd.direct ? 0u : rd.bytes);
+    if (bytes == 0) {
+      mbar_arrive(bar);  // keeps the slot's phases in step
+      return;
+    }
+    mbar_arrive_expect_tx(bar, bytes);
+    if (!rx.direct) bulk_load(at, rx.begin, rx.bytes, bar);
+    if (!rd.direct) bulk_load(at + g.slot_bytes, rd.begin, rd.bytes, bar);
+  };
+  if (t == 0) {
+    for (int s = 0; s < g.slots; ++s) mbar_init(smem_u32(&full[s]), 1);
+    ctl.abort = 0;
+    fence_barrier_init();
+    for (int s = 0; s < g.slots; ++s) issue(s);
+  }
+  float w[NV][VN], aw[NV][VN], ab[NV][VN];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = (int64_t(i) * tpr + t) * VN;
+#pragma unroll
+    for (int j = 0; j < VN; ++j) {
+      w[i][j] = 1.0f;
+      aw[i][j] = 0.0f;
+      ab[i][j] = 0.0f;
+    }
+    if (a.w && c < a.h) LnIo<W, VN>::load(static_cast<const W*>(a.w) + c, w[i]);
+  }
+  __syncthreads();
+  const float inv_h = 1.0f / float(a.h);
+  int buf = 0;
+  float mean = count > 0 ? a.mean[row_of(0)] : 0.0f, rstd = count > 0 ? a.rstd[row_of(0)] : 0.0f;
+  for (int64_t i = 0; i < count; ++i) {
+    const int64_t r = row_of(i), next = row_of(i + 1 < count ? i + 1 : i);
+    const float next_mean = a.mean[next], next_rstd = a.rstd[next];
+    const int slot = int(i % g.slots);
+    const uint8_t* at = ring + uint32_t(slot) * 2u * g.slot_bytes;
+    wait_phase(smem_u32(&full[slot]), uint32_t(i / g.slots) & 1u, &ctl, g.err, g.timeout_ns);
+    float xh[NV][VN], d[NV][VN];
+    ln_ring_read<T, VN, NV>(at, ln_ring_row<T>(a.x, a.ldx, a.n, a.h, r), a.h, xh);
+    ln_ring_read<T, VN, NV>(at + g.slot_bytes, ln_ring_row<T>(a.dy, a.lddy, a.n, a.h, r), a.h, d);
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (int j = 0; j < VN; ++j) {  // behind the row's end dy is 0
+        xh[k][j] = (xh[k][j] - mean) * rstd;
+        ab[k][j] += d[k][j];
+        aw[k][j] += d[k][j] * xh[k][j];
+        d[k][j] *= w[k][j];
+        s.x += d[k][j];
+        s.y += d[k][j] * xh[k][j];
+      }
+    }
+    if (a.dx == nullptr) {  // the same for every thread
+      __syncthreads();
+      if (t == 0) issue(i + g.slots);
+    } else {
+      s = ln_row_sum<false>(s, red, buf);
+      if (t == 0) issue(i + g.slots);
+      const float m1 = s.x * inv_h, m2 = s.y * inv_h;
+      T* dx = static_cast<T*>(a.dx) + r * a.lddx;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int64_t c = (int64_t(k) * tpr + t) * VN;
+        if (c < a.h) {
+#pragma unroll
+          for (int j = 0; j < VN; ++j) d[k][j] = rstd * (d[k][j] - m1 - xh[k][j] * m2);
+          LnIo<T, VN>::store(dx + c, d[k]);
+        }
+      }
+    }
+    mean = next_mean;
+    rstd = next_rstd;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = (int64_t(i) * tpr + t) * VN;
+    if (c >= a.h) continue;
+#pragma unroll
+    for (int j = 0; j < VN; ++j) {
+      const int64_t at = int64_t(blockIdx.x) * a.h + c + j;
+      if (a.part_w) a.part_w[at] = aw[i][j];
+      if (a.part_b) a.part_b[at] = ab[i][j];
+    }
+  }
+}
+
 // Long rows: dx row by row (two looks at x and dy) ...
 template <typename T, typename W>
 __global__ void __launch_bounds__(1024) ln_backward_long_dx_kernel(const LnBwdArgs a) {
@@ -456,6 +734,35 @@ static LnShape ln_shape(int dtype, int64_t h, int max_vec) {
   return s;
 }
 
+// How a ring kernel lays a row over threads: whole 16-byte vectors, or single
+// elements where the rows' alignment or length does not allow them; 16 columns a
+// thread (the backward keeps 80 values of them in registers), at least 64 threads.
+struct LnRingShape {
+  int vn, nv, threads, blocks_per_sm;
+  LnRing ring;
+  size_t smem;
+};
+static bool ln_ring_shape(int dtype, int64_t h, bool vec, int tensors, int64_t n, int sms,
+                          LnRingShape* out) {
+  const int esz = dtype == FLCE_F32 ? 4 : 2;
+  LnRingShape s{};
+  s.vn = vec ? 16 / esz : 1;
+  const int64_t vecs = cdiv(h, s.vn);
+  s.nv = 16 / s.vn;
+  s.threads = int(cdiv(cdiv(vecs, s.nv), 32) * 32);
+  if (cdiv(vecs, s.nv) > kLnMaxThreads || s.threads < 64) return false;
+  s.blocks_per_sm = std::max(1, kLnMaxThreads / s.threads);
+  // fewer rows than two per block: nothing to stream
+  if (n < 2 * int64_t(sms) * s.blocks_per_sm) return false;
+  s.ring.slot_bytes = uint32_t((h * esz + 15) / 16 * 16 + (vec ? 0 : 16));
+  const int64_t fit = int64_t(kLnRingBytes / s.blocks_per_sm) / (int64_t(s.ring.slot_bytes) * tensors);
+  s.ring.slots = int(std::min<int64_t>(kLnSlots, fit));
+  if (s.ring.slots < 2) return false;
+  s.smem = size_t(s.ring.slots) * tensors * s.ring.slot_bytes;
+  *out = s;
+  return true;
+}
+
 // Largest vector (elements, a power of two) that all rows of a tensor allow.
 static int ln_vec(const void* p, int64_t ld, int64_t h, int esz) {
   if (p == nullptr) return 8;
@@ -480,6 +787,12 @@ static int64_t ln_parts(int64_t n, const LnShape& s) {
 // Before the pointers' alignment is known: the most any layout takes.
 static int64_t ln_max_parts(int64_t n, int64_t h) {
   int64_t parts = std::min<int64_t>(std::max<int64_t>(n, 1), kLnSms);  // long rows
+  for (int dtype = 0; dtype < 2; ++dtype)
+    for (int vec = 0; vec < 2; ++vec) {
+      LnRingShape r;
+      if (ln_ring_shape(dtype, h, vec != 0, 2, n, 1, &r))
+        parts = std::max<int64_t>(parts, int64_t(kLnSms) * r.blocks_per_sm);
+    }
   for (int dtype = 0; dtype < 2; ++dtype)
     for (int v = 1; v <= 8; v *= 2) parts = std::max(parts, ln_parts(n, ln_shape(dtype, h, v)));
   return parts;
@@ -516,6 +829,26 @@ static void ln_dispatch_fwd(const LnArgs& a, const LnShape& s, int grid, cudaStr
     ln_launch_fwd<T, W, 2, 8>(a, s, grid, st);
   else
     ln_launch_fwd<T, W, 1, 8>(a, s, grid, st);
+}
+template <typename Kern, typename Args>
+static int ln_launch_ring(Kern kern, const Args& a, const LnRingShape& s, int grid, cudaStream_t st) {
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(s.smem)) !=
+      cudaSuccess)
+    return FLCE_ERR_CUDA;
+  kern<<<grid, s.threads, s.smem, st>>>(a, s.ring);
+  return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
+}
+template <typename T, typename W>
+static int ln_ring_fwd(const LnArgs& a, const LnRingShape& s, int grid, cudaStream_t st) {
+  constexpr int kFull = 16 / int(sizeof(T));
+  return s.vn == kFull ? ln_launch_ring(ln_forward_ring_kernel<T, W, kFull, 16 / kFull>, a, s, grid, st)
+                       : ln_launch_ring(ln_forward_ring_kernel<T, W, 1, 16>, a, s, grid, st);
+}
+template <typename T, typename W>
+static int ln_ring_bwd(const LnBwdArgs& a, const LnRingShape& s, int grid, cudaStream_t st) {
+  constexpr int kFull = 16 / int(sizeof(T));
+  return s.vn == kFull ? ln_launch_ring(ln_backward_ring_kernel<T, W, kFull, 16 / kFull>, a, s, grid, st)
+                       : ln_launch_ring(ln_backward_ring_kernel<T, W, 1, 16>, a, s, grid, st);
 }
 template <typename T, typename W, int VN, int NV>
 static void ln_launch_bwd(const LnBwdArgs& a, const LnShape& s, int grid, cudaStream_t st) {
@@ -568,6 +901,18 @@ extern "C" int flce_layer_norm_forward(const void* x, int dtype, int64_t n, int6
   const LnShape s = ln_shape(dtype, h, std::min({ln_vec(x, ldx, h, esz), ln_vec(y, ldy, h, esz),
                                                  ln_vec_w(weight, wsz), ln_vec_w(bias, wsz)}));
   const LnArgs a{x, ldx, weight, bias, n, h, eps, y, ldy, mean, rstd};
+  LnRingShape rs;
+  if (ln_ring_shape(dtype, h, s.vn == 16 / esz, 1, n, dev->num_sms, &rs)) {
+    rs.ring.err = dev->err;
+    rs.ring.timeout_ns = kDefaultTimeoutNs;
+    const int grid = dev->num_sms * rs.blocks_per_sm;
+    LaunchScope scope(KF_LN_FWD, 0.0, double(n) * double(h) * 2.0 * esz + 8.0 * double(n), cs);
+    if (dtype == FLCE_BF16)
+      return w_dtype == FLCE_BF16 ? ln_ring_fwd<__nv_bfloat16, __nv_bfloat16>(a, rs, grid, cs)
+                                  : ln_ring_fwd<__nv_bfloat16, float>(a, rs, grid, cs);
+    return w_dtype == FLCE_BF16 ? ln_ring_fwd<float, __nv_bfloat16>(a, rs, grid, cs)
+                                : ln_ring_fwd<float, float>(a, rs, grid, cs);
+  }
   const int64_t per_sm = s.vn == 0 ? 2 : std::max(1, 2048 / s.threads);
   const int grid = int(std::min<int64_t>(cdiv(n, s.vn == 0 ? 1 : s.rpb), dev->num_sms * per_sm));
   LaunchScope scope(KF_LN_FWD, 0.0, double(n) * double(h) * 2.0 * esz + 8.0 * double(n), cs);
@@ -616,7 +961,22 @@ extern "C" int flce_layer_norm_backward(const void* dy, int64_t lddy, const void
                                      ln_vec(dx, lddx, h, esz), ln_vec_w(weight, wsz)}));
     const LnBwdArgs a{dy, lddy, x, ldx, weight, mean, rstd, n, h, dx, lddx, part_w, part_b};
     const double bytes = double(n) * double(h) * 3.0 * esz + 8.0 * double(n);
-    if (s.vn == 0) {
+    LnRingShape rs;
+    if (ln_ring_shape(dtype, h, s.vn == 16 / esz, 2, n, dev->num_sms, &rs) &&
+        dev->num_sms <= kLnSms) {
+      rs.ring.err = dev->err;
+      rs.ring.timeout_ns = kDefaultTimeoutNs;
+      parts = dev->num_sms * rs.blocks_per_sm;
+      LaunchScope scope(KF_LN_BWD, 0.0, bytes, cs);
+      int rc;
+      if (dtype == FLCE_BF16)
+        rc = w_dtype == FLCE_BF16 ? ln_ring_bwd<__nv_bfloat16, __nv_bfloat16>(a, rs, parts, cs)
+                                  : ln_ring_bwd<__nv_bfloat16, float>(a, rs, parts, cs);
+      else
+        rc = w_dtype == FLCE_BF16 ? ln_ring_bwd<float, __nv_bfloat16>(a, rs, parts, cs)
+                                  : ln_ring_bwd<float, float>(a, rs, parts, cs);
+      if (rc != FLCE_OK) return rc;
+    } else if (s.vn == 0) {
       if (dx != nullptr) {
         const int grid = int(std::min<int64_t>(n, int64_t(dev->num_sms) * 2));
         LaunchScope scope(KF_LN_BWD, 0.0, bytes, cs);

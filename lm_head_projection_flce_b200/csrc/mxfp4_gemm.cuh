@@ -106,16 +106,6 @@ __device__ __forceinline__ void tc_mma_mxf4_one(uint32_t d, uint64_t a, uint64_t
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-// Untiled bulk copy to this CTA's shared memory (16-byte aligned, whole 16s).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
-      : "memory");
-}
-
 // Instruction descriptor of kind::mxf4: E2M1 A and B (K-major), E8M0 scales,
 // shape M x N; the scale words' first byte used (0 or 2) is added per MMA.
 __host__ __device__ constexpr uint32_t mma_idesc_mxf4(int m, int n) {
@@ -231,13 +221,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (leader) {
           mbar_arrive_expect_tx(full, expect);
-          bulk_load(base, mc, kMxCodeBytes, full, pol_m);
-          bulk_load(base + off_sfa, ms, 2 * kMxTileBytes, full, pol_m);
-          bulk_load(base + off_b, nc, bytes0, full, pol_n);
-          bulk_load(base + off_sfb, ns, 2 * kMxTileBytes, full, pol_n);
+          bulk_load_hint(base, mc, kMxCodeBytes, full, pol_m);
+          bulk_load_hint(base + off_sfa, ms, 2 * kMxTileBytes, full, pol_m);
+          bulk_load_hint(base + off_b, nc, bytes0, full, pol_n);
+          bulk_load_hint(base + off_sfb, ns, 2 * kMxTileBytes, full, pol_n);
           if (two) {
-            bulk_load(base + off_b + bytes0, nc1, bytes1, full, pol_n);
-            bulk_load(base + off_sfb + 2 * kMxTileBytes, ns1, 2 * kMxTileBytes, full, pol_n);
+            bulk_load_hint(base + off_b + bytes0, nc1, bytes1, full, pol_n);
+            bulk_load_hint(base + off_sfb + 2 * kMxTileBytes, ns1, 2 * kMxTileBytes, full, pol_n);
           }
         }
         mc += kMxCodeBytes;

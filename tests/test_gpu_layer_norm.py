@@ -95,6 +95,25 @@ def test_parity(dev, dtype, n, h):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,h,ld,off", [(700, 8192, 8192, 0), (5000, 1040, 1040, 0), (6003, 1003, 1003, 3),
+                                        (701, 5377, 5380, 1), (700, 4096, 4100, 0), (3001, 2050, 2050, 8)])
+def test_more_rows_than_blocks(dev, dtype, n, h, ld, off):
+    """Rows streamed through shared memory: aligned, odd, with gaps, starting and ending anywhere."""
+    g = torch.Generator(device=dev).manual_seed(n + h)
+    flat = torch.randn(2, n * ld + off, generator=g, device=dev) * 1.5 + 0.5
+    flat = flat.to(dtype)
+    x, dy = (flat[i, off:].view(n, ld)[:, :h] for i in (0, 1))
+    w = 1 + 0.2 * torch.randn(h, generator=g, device=dev)
+    b = 0.3 * torch.randn(h, generator=g, device=dev)
+    y, mean, rstd = flce.layer_norm_forward(x, w, b)
+    dx, dw, db = flce.layer_norm_backward(dy, x, mean, rstd, w)
+    _check(x, dy, w, b, 1e-5, y, mean, rstd, dx, dw, db)
+    only = flce.layer_norm_backward(dy, x, mean, rstd, w, want=("dweight", "dbias"))
+    assert torch.equal(only[1], dw) and torch.equal(only[2], db)
+    assert flce.get_error(dev) == flce.FLCE_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("h,ld,off", [(256, 264, 0), (256, 257, 0), (100, 128, 4), (511, 600, 1)])
 def test_row_strides_and_gaps(dev, dtype, h, ld, off):
     x, dy, w, b = _inputs(h + ld, 21, h, dtype, dtype, dev, ld=ld + off)
