@@ -125,16 +125,17 @@ __device__ __forceinline__ float2 ln_row_sum(float2 v, float2 (*red)[32], int& b
     v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
   if constexpr (kWarpRow) return v;
-  const int warps = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) red[buf][threadIdx.x >> 5] = v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[buf][threadIdx.x >> 5] = v;
   __syncthreads();
-  float2 s = make_float2(0.0f, 0.0f);
-  for (int w = 0; w < warps; ++w) {
-    s.x += red[buf][w].x;
-    s.y += red[buf][w].y;
+  v = lane < int(blockDim.x >> 5) ? red[buf][lane] : make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
   buf ^= 1;
-  return s;
+  return v;
 }
 
 struct LnArgs {
@@ -237,6 +238,18 @@ struct LnRing {
   uint64_t timeout_ns;
 };
 
+// Position in the ring of the next row to use or to load.
+struct LnRingPos {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void advance(int slots) {
+    if (++slot == slots) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
 struct LnRingRow {
   const uint8_t* begin;  // 16-byte aligned start of the copy
   uint32_t bytes;
@@ -295,23 +308,25 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
   auto row_at = [&](int64_t i) {
     return ln_ring_row<T>(a.x, a.ldx, a.n, a.h, int64_t(blockIdx.x) + i * gridDim.x);
   };
-  auto issue = [&](int64_t i) {
-    if (i >= count) return;
-    const LnRingRow row = row_at(i);
-    const int s = int(i % g.slots);
-    const uint32_t bar = smem_u32(&full[s]);
+  int64_t loaded = 0;  // thread 0: rows issued so far, and the slot of the next
+  LnRingPos put, get;
+  auto issue = [&]() {
+    if (loaded >= count) return;
+    const LnRingRow row = row_at(loaded++);
+    const uint32_t bar = smem_u32(&full[put.slot]);
     if (row.direct) {
       mbar_arrive(bar);  // keeps the slot's phases in step
     } else {
       mbar_arrive_expect_tx(bar, row.bytes);
-      bulk_load(smem_u32(ring) + uint32_t(s) * g.slot_bytes, row.begin, row.bytes, bar);
+      bulk_load(smem_u32(ring) + uint32_t(put.slot) * g.slot_bytes, row.begin, row.bytes, bar);
     }
+    put.advance(g.slots);
   };
   if (t == 0) {
     for (int s = 0; s < g.slots; ++s) mbar_init(smem_u32(&full[s]), 1);
     ctl.abort = 0;
     fence_barrier_init();
-    for (int s = 0; s < g.slots; ++s) issue(s);
+    for (int s = 0; s < g.slots; ++s) issue();
   }
   float w[NV][VN], b[NV][VN];
 #pragma unroll
@@ -329,10 +344,10 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
   const float inv_h = 1.0f / float(a.h);
   int buf = 0;
   auto fetch = [&](int64_t i, float (&v)[NV][VN]) {
-    const int s = int(i % g.slots);
     // A wait that ran out is recorded and the row's result lost; the loop ends as usual.
-    wait_phase(smem_u32(&full[s]), uint32_t(i / g.slots) & 1u, &ctl, g.err, g.timeout_ns);
-    ln_ring_read<T, VN, NV>(ring + uint32_t(s) * g.slot_bytes, row_at(i), a.h, v);
+    wait_phase(smem_u32(&full[get.slot]), get.parity, &ctl, g.err, g.timeout_ns);
+    ln_ring_read<T, VN, NV>(ring + uint32_t(get.slot) * g.slot_bytes, row_at(i), a.h, v);
+    get.advance(g.slots);
   };
   auto finish = [&](int64_t i, float (&v)[NV][VN], float mean, float rstd) {
     const int64_t r = int64_t(blockIdx.x) + i * gridDim.x;
@@ -367,8 +382,8 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
       }
     s = ln_row_sum<false>(s, red, buf);
     if (t == 0) {
-      issue(i + g.slots);
-      if (two) issue(i + 1 + g.slots);
+      issue();
+      if (two) issue();
     }
     const float m0 = s.x * inv_h, m1 = s.y * inv_h;
     s = make_float2(0.0f, 0.0f);
@@ -537,13 +552,17 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
   const int t = threadIdx.x, tpr = blockDim.x;
   const int64_t count = (a.n - blockIdx.x + gridDim.x - 1) / gridDim.x;
   auto row_of = [&](int64_t i) { return int64_t(blockIdx.x) + i * gridDim.x; };
-  auto issue = [&](int64_t i) {
-    if (i >= count) return;
-    const LnRingRow rx = ln_ring_row<T>(a.x, a.ldx, a.n, a.h, row_of(i));
-    const LnRingRow rd = ln_ring_row<T>(a.dy, a.lddy, a.n, a.h, row_of(i));
-    const int s = int(i % g.slots);
-    const uint32_t bar = smem_u32(&full[s]), at = smem_u32(ring) + uint32_t(s) * 2u * g.slot_bytes;
+  int64_t loaded = 0;  // thread 0: rows issued so far, and the slot of the next
+  LnRingPos put, get;
+  auto issue = [&]() {
+    if (loaded >= count) return;
+    const int64_t r = row_of(loaded++);
+    const LnRingRow rx = ln_ring_row<T>(a.x, a.ldx, a.n, a.h, r);
+    const LnRingRow rd = ln_ring_row<T>(a.dy, a.lddy, a.n, a.h, r);
+    const uint32_t bar = smem_u32(&full[put.slot]);
+    const uint32_t at = smem_u32(ring) + uint32_t(put.slot) * 2u * g.slot_bytes;
     const uint32_t bytes = (rx.direct ? 0u : rx.bytes) + (rd.direct ? 0u : rd.bytes);
+    put.advance(g.slots);
     if (bytes == 0) {
       mbar_arrive(bar);  // keeps the slot's phases in step
       return;
@@ -556,7 +575,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     for (int s = 0; s < g.slots; ++s) mbar_init(smem_u32(&full[s]), 1);
     ctl.abort = 0;
     fence_barrier_init();
-    for (int s = 0; s < g.slots; ++s) issue(s);
+    for (int s = 0; s < g.slots; ++s) issue();
   }
   float w[NV][VN], aw[NV][VN], ab[NV][VN];
 #pragma unroll
@@ -577,9 +596,9 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
   for (int64_t i = 0; i < count; ++i) {
     const int64_t r = row_of(i), next = row_of(i + 1 < count ? i + 1 : i);
     const float next_mean = a.mean[next], next_rstd = a.rstd[next];
-    const int slot = int(i % g.slots);
-    const uint8_t* at = ring + uint32_t(slot) * 2u * g.slot_bytes;
-    wait_phase(smem_u32(&full[slot]), uint32_t(i / g.slots) & 1u, &ctl, g.err, g.timeout_ns);
+    const uint8_t* at = ring + uint32_t(get.slot) * 2u * g.slot_bytes;
+    wait_phase(smem_u32(&full[get.slot]), get.parity, &ctl, g.err, g.timeout_ns);
+    get.advance(g.slots);
     float xh[NV][VN], d[NV][VN];
     ln_ring_read<T, VN, NV>(at, ln_ring_row<T>(a.x, a.ldx, a.n, a.h, r), a.h, xh);
     ln_ring_read<T, VN, NV>(at + g.slot_bytes, ln_ring_row<T>(a.dy, a.lddy, a.n, a.h, r), a.h, d);
@@ -598,10 +617,10 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     }
     if (a.dx == nullptr) {  // the same for every thread
       __syncthreads();
-      if (t == 0) issue(i + g.slots);
+      if (t == 0) issue();
     } else {
       s = ln_row_sum<false>(s, red, buf);
-      if (t == 0) issue(i + g.slots);
+      if (t == 0) issue();
       const float m1 = s.x * inv_h, m2 = s.y * inv_h;
       T* dx = static_cast<T*>(a.dx) + r * a.lddx;
 #pragma unroll
