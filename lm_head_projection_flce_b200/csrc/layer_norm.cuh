@@ -125,12 +125,18 @@ __device__ __forceinline__ float2 ln_row_sum(float2 v, float2 (*red)[32], int& b
     v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
   if constexpr (kWarpRow) return v;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warps = int(blockDim.x >> 5);
   if (lane == 0) red[buf][threadIdx.x >> 5] = v;
   __syncthreads();
-  v = lane < int(blockDim.x >> 5) ? red[buf][lane] : make_float2(0.0f, 0.0f);
+  // Up to 16 warps both halves of a warp add the same 16 values.
+  const int from = warps > 16 ? lane : lane & 15;
+  v = from < warps ? red[buf][from] : make_float2(0.0f, 0.0f);
+  if (warps > 16) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, 16);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = 8; o > 0; o >>= 1) {
     v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
     v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
@@ -268,51 +274,83 @@ __device__ __forceinline__ LnRingRow ln_ring_row(const void* base, int64_t ld, i
   row.direct = (r == 0 && row.phase != 0) || (r == n - 1 && row.bytes != len);
   return row;
 }
-// A thread's share of row r: from the ring's slot or, for a direct row, from global memory.
-template <typename T, int VN, int NV>
-__device__ __forceinline__ void ln_ring_read(const uint8_t* slot, const LnRingRow& row, int64_t h,
-                                             float (&v)[NV][VN]) {
-  auto from = [&](const T* src) {
+// A thread's 16 columns as 8 pairs (packed FP32 arithmetic works on two at a time):
+// vector i of VN columns starts at column (i * blockDim.x + threadIdx.x) * VN.
+// kExact: the block's shares cover the row exactly; else columns behind its end
+// read as `fill`.
+template <typename T, int VN, bool kExact>
+__device__ __forceinline__ void ln_share_load(const T* src, int h, float fill, float2 (&v)[8]) {
+  float x[16];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t(i) * blockDim.x + threadIdx.x) * VN;
-      if (c < h) {
-        LnIo<T, VN>::load(src + c, v[i]);
-      } else {
+  for (int i = 0; i < 16 / VN; ++i) {
+    const int c = (i * int(blockDim.x) + int(threadIdx.x)) * VN;
+    float one[VN];
 #pragma unroll
-        for (int j = 0; j < VN; ++j) v[i][j] = 0.0f;
-      }
-    }
-  };
-  if constexpr (VN == 1) {  // wider vectors: whole rows of 16-byte pieces, never direct
-    if (row.direct) {
-      from(reinterpret_cast<const T*>(row.begin + row.phase));
-      return;
-    }
-    from(reinterpret_cast<const T*>(slot + row.phase));
-  } else {
-    from(reinterpret_cast<const T*>(slot));
+    for (int j = 0; j < VN; ++j) one[j] = fill;
+    if (kExact || c < h) LnIo<T, VN>::load(src + c, one);
+#pragma unroll
+    for (int j = 0; j < VN; ++j) x[i * VN + j] = one[j];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
+}
+template <typename T, int VN, bool kExact>
+__device__ __forceinline__ void ln_share_store(T* dst, int h, const float2 (&v)[8]) {
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = v[i].x;
+    x[2 * i + 1] = v[i].y;
+  }
+#pragma unroll
+  for (int i = 0; i < 16 / VN; ++i) {
+    const int c = (i * int(blockDim.x) + int(threadIdx.x)) * VN;
+    float one[VN];
+#pragma unroll
+    for (int j = 0; j < VN; ++j) one[j] = x[i * VN + j];
+    if (kExact || c < h) LnIo<T, VN>::store(dst + c, one);
   }
 }
+// Zeroes the columns behind the row's end.
+template <int VN>
+__device__ __forceinline__ void ln_share_clip(int h, float2 (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int i = e / VN;
+    if ((i * int(blockDim.x) + int(threadIdx.x)) * VN >= h) (e % 2 ? v[e / 2].y : v[e / 2].x) = 0.0f;
+  }
+}
+template <typename T, int VN, bool kExact>
+__device__ __forceinline__ void ln_ring_read(const uint8_t* slot, const void* base, int64_t ld,
+                                             int64_t n, int h, int64_t r, float2 (&v)[8]) {
+  if constexpr (VN == 1) {
+    const LnRingRow row = ln_ring_row<T>(base, ld, n, h, r);
+    if (row.direct)
+      ln_share_load<T, VN, kExact>(reinterpret_cast<const T*>(row.begin + row.phase), h, 0.0f, v);
+    else
+      ln_share_load<T, VN, kExact>(reinterpret_cast<const T*>(slot + row.phase), h, 0.0f, v);
+  } else {  // whole rows of 16-byte pieces: never direct
+    ln_share_load<T, VN, kExact>(reinterpret_cast<const T*>(slot), h, 0.0f, v);
+  }
+}
+__device__ __forceinline__ float2 ln_both(float x) { return make_float2(x, x); }
 
 // Two rows at a time: both sums of a reduction travel together.
-template <typename T, typename W, int VN, int NV>
+template <typename T, typename W, int VN, bool kExact>
 __global__ void __launch_bounds__(kLnMaxThreads, 1)
     ln_forward_ring_kernel(const LnArgs a, const LnRing g) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(8) uint64_t full[kLnSlots];
   __shared__ float2 red[2][32];
   __shared__ PipeCtl ctl;
-  const int t = threadIdx.x, tpr = blockDim.x;
-  const int64_t count = (a.n - blockIdx.x + gridDim.x - 1) / gridDim.x;  // this block's rows
-  auto row_at = [&](int64_t i) {
-    return ln_ring_row<T>(a.x, a.ldx, a.n, a.h, int64_t(blockIdx.x) + i * gridDim.x);
-  };
-  int64_t loaded = 0;  // thread 0: rows issued so far, and the slot of the next
+  const int t = threadIdx.x, h = int(a.h);
+  const int count = int((a.n - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this block's rows
+  int loaded = 0;  // thread 0: rows issued so far, and the slot of the next
   LnRingPos put, get;
   auto issue = [&]() {
     if (loaded >= count) return;
-    const LnRingRow row = row_at(loaded++);
+    const LnRingRow row =
+        ln_ring_row<T>(a.x, a.ldx, a.n, a.h, int64_t(blockIdx.x) + int64_t(loaded++) * gridDim.x);
     const uint32_t bar = smem_u32(&full[put.slot]);
     if (row.direct) {
       mbar_arrive(bar);  // keeps the slot's phases in step
@@ -328,79 +366,65 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     fence_barrier_init();
     for (int s = 0; s < g.slots; ++s) issue();
   }
-  float w[NV][VN], b[NV][VN];
+  float2 w[8], b[8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t c = (int64_t(i) * tpr + t) * VN;
-#pragma unroll
-    for (int j = 0; j < VN; ++j) {
-      w[i][j] = 1.0f;
-      b[i][j] = 0.0f;
-    }
-    if (a.w && c < a.h) LnIo<W, VN>::load(static_cast<const W*>(a.w) + c, w[i]);
-    if (a.b && c < a.h) LnIo<W, VN>::load(static_cast<const W*>(a.b) + c, b[i]);
+  for (int i = 0; i < 8; ++i) {
+    w[i] = ln_both(1.0f);
+    b[i] = ln_both(0.0f);
   }
+  if (a.w) ln_share_load<W, VN, kExact>(static_cast<const W*>(a.w), h, 0.0f, w);
+  if (a.b) ln_share_load<W, VN, kExact>(static_cast<const W*>(a.b), h, 0.0f, b);
   __syncthreads();
-  const float inv_h = 1.0f / float(a.h);
+  const float inv_h = 1.0f / float(h);
   int buf = 0;
-  auto fetch = [&](int64_t i, float (&v)[NV][VN]) {
+  auto fetch = [&](int64_t r, float2 (&v)[8]) {
     // A wait that ran out is recorded and the row's result lost; the loop ends as usual.
     wait_phase(smem_u32(&full[get.slot]), get.parity, &ctl, g.err, g.timeout_ns);
-    ln_ring_read<T, VN, NV>(ring + uint32_t(get.slot) * g.slot_bytes, row_at(i), a.h, v);
+    ln_ring_read<T, VN, kExact>(ring + uint32_t(get.slot) * g.slot_bytes, a.x, a.ldx, a.n, h, r, v);
     get.advance(g.slots);
   };
-  auto finish = [&](int64_t i, float (&v)[NV][VN], float mean, float rstd) {
-    const int64_t r = int64_t(blockIdx.x) + i * gridDim.x;
+  auto sum = [&](const float2 (&v)[8]) {
+    float2 s = v[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s = __fadd2_rn(s, v[i]);
+    return s.x + s.y;
+  };
+  auto centre = [&](float mean, float2 (&v)[8]) {  // and the sum of squares
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __fadd2_rn(v[i], ln_both(-mean));
+    if constexpr (!kExact) ln_share_clip<VN>(h, v);
+    float2 s = __fmul2_rn(v[0], v[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s = __ffma2_rn(v[i], v[i], s);
+    return s.x + s.y;
+  };
+  auto finish = [&](int64_t r, float2 (&v)[8], float mean, float rstd) {
     if (t == 0) {
       if (a.mean) a.mean[r] = mean;
       if (a.rstd) a.rstd[r] = rstd;
     }
-    T* y = static_cast<T*>(a.y) + r * a.ldy;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int64_t c = (int64_t(k) * tpr + t) * VN;
-      if (c < a.h) {
-#pragma unroll
-        for (int j = 0; j < VN; ++j) v[k][j] = v[k][j] * rstd * w[k][j] + b[k][j];
-        LnIo<T, VN>::store(y + c, v[k]);
-      }
-    }
+    for (int i = 0; i < 8; ++i) v[i] = __ffma2_rn(__fmul2_rn(v[i], ln_both(rstd)), w[i], b[i]);
+    ln_share_store<T, VN, kExact>(static_cast<T*>(a.y) + r * a.ldy, h, v);
   };
-  for (int64_t i = 0; i < count; i += 2) {
+  int64_t r = blockIdx.x;
+  for (int i = 0; i < count; i += 2, r += 2 * int64_t(gridDim.x)) {
     const bool two = i + 1 < count;
-    float v0[NV][VN], v1[NV][VN];
-    fetch(i, v0);
-    if (two) fetch(i + 1, v1);
-    float2 s = make_float2(0.0f, 0.0f);
+    float2 v0[8], v1[8];
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int j = 0; j < VN; ++j) {
-        if (!two) v1[k][j] = 0.0f;
-        s.x += v0[k][j];
-        s.y += v1[k][j];
-      }
-    s = ln_row_sum<false>(s, red, buf);
+    for (int k = 0; k < 8; ++k) v1[k] = ln_both(0.0f);
+    fetch(r, v0);
+    if (two) fetch(r + gridDim.x, v1);
+    float2 s = ln_row_sum<false>(make_float2(sum(v0), sum(v1)), red, buf);
     if (t == 0) {
       issue();
       if (two) issue();
     }
     const float m0 = s.x * inv_h, m1 = s.y * inv_h;
-    s = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const bool in = (int64_t(k) * tpr + t) * VN < a.h;
-#pragma unroll
-      for (int j = 0; j < VN; ++j) {
-        v0[k][j] = in ? v0[k][j] - m0 : 0.0f;
-        v1[k][j] = in ? v1[k][j] - m1 : 0.0f;
-        s.x += v0[k][j] * v0[k][j];
-        s.y += v1[k][j] * v1[k][j];
-      }
-    }
+    s = make_float2(centre(m0, v0), centre(m1, v1));
     s = ln_row_sum<false>(s, red, buf);
-    finish(i, v0, m0, 1.0f / sqrtf(s.x * inv_h + a.eps));
-    if (two) finish(i + 1, v1, m1, 1.0f / sqrtf(s.y * inv_h + a.eps));
+    finish(r, v0, m0, 1.0f / sqrtf(s.x * inv_h + a.eps));
+    if (two) finish(r + gridDim.x, v1, m1, 1.0f / sqrtf(s.y * inv_h + a.eps));
   }
 }
 
@@ -542,21 +566,20 @@ __global__ void __launch_bounds__(ln_block(VN * NV, kWarpRow))
 }
 
 // The backward through the ring: a slot holds the row of x and the row of dy.
-template <typename T, typename W, int VN, int NV>
+template <typename T, typename W, int VN, bool kExact>
 __global__ void __launch_bounds__(kLnMaxThreads, 1)
     ln_backward_ring_kernel(const LnBwdArgs a, const LnRing g) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(8) uint64_t full[kLnSlots];
   __shared__ float2 red[2][32];
   __shared__ PipeCtl ctl;
-  const int t = threadIdx.x, tpr = blockDim.x;
-  const int64_t count = (a.n - blockIdx.x + gridDim.x - 1) / gridDim.x;
-  auto row_of = [&](int64_t i) { return int64_t(blockIdx.x) + i * gridDim.x; };
-  int64_t loaded = 0;  // thread 0: rows issued so far, and the slot of the next
+  const int t = threadIdx.x, h = int(a.h);
+  const int count = int((a.n - blockIdx.x + gridDim.x - 1) / gridDim.x);
+  int loaded = 0;  // thread 0: rows issued so far, and the slot of the next
   LnRingPos put, get;
   auto issue = [&]() {
     if (loaded >= count) return;
-    const int64_t r = row_of(loaded++);
+    const int64_t r = int64_t(blockIdx.x) + int64_t(loaded++) * gridDim.x;
     const LnRingRow rx = ln_ring_row<T>(a.x, a.ldx, a.n, a.h, r);
     const LnRingRow rd = ln_ring_row<T>(a.dy, a.lddy, a.n, a.h, r);
     const uint32_t bar = smem_u32(&full[put.slot]);
@@ -577,76 +600,54 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     fence_barrier_init();
     for (int s = 0; s < g.slots; ++s) issue();
   }
-  float w[NV][VN], aw[NV][VN], ab[NV][VN];
+  float2 w[8], aw[8], ab[8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t c = (int64_t(i) * tpr + t) * VN;
-#pragma unroll
-    for (int j = 0; j < VN; ++j) {
-      w[i][j] = 1.0f;
-      aw[i][j] = 0.0f;
-      ab[i][j] = 0.0f;
-    }
-    if (a.w && c < a.h) LnIo<W, VN>::load(static_cast<const W*>(a.w) + c, w[i]);
+  for (int i = 0; i < 8; ++i) {
+    w[i] = ln_both(1.0f);
+    aw[i] = ab[i] = ln_both(0.0f);
   }
+  if (a.w) ln_share_load<W, VN, kExact>(static_cast<const W*>(a.w), h, 0.0f, w);
   __syncthreads();
-  const float inv_h = 1.0f / float(a.h);
+  const float inv_h = 1.0f / float(h);
   int buf = 0;
-  float mean = count > 0 ? a.mean[row_of(0)] : 0.0f, rstd = count > 0 ? a.rstd[row_of(0)] : 0.0f;
-  for (int64_t i = 0; i < count; ++i) {
-    const int64_t r = row_of(i), next = row_of(i + 1 < count ? i + 1 : i);
+  int64_t r = blockIdx.x;
+  float mean = a.mean[r], rstd = a.rstd[r];  // a block has two rows at least
+  for (int i = 0; i < count; ++i, r += gridDim.x) {
+    const int64_t next = i + 1 < count ? r + gridDim.x : r;
     const float next_mean = a.mean[next], next_rstd = a.rstd[next];
     const uint8_t* at = ring + uint32_t(get.slot) * 2u * g.slot_bytes;
     wait_phase(smem_u32(&full[get.slot]), get.parity, &ctl, g.err, g.timeout_ns);
     get.advance(g.slots);
-    float xh[NV][VN], d[NV][VN];
-    ln_ring_read<T, VN, NV>(at, ln_ring_row<T>(a.x, a.ldx, a.n, a.h, r), a.h, xh);
-    ln_ring_read<T, VN, NV>(at + g.slot_bytes, ln_ring_row<T>(a.dy, a.lddy, a.n, a.h, r), a.h, d);
-    float2 s = make_float2(0.0f, 0.0f);
+    float2 xh[8], d[8];
+    ln_ring_read<T, VN, kExact>(at, a.x, a.ldx, a.n, h, r, xh);
+    ln_ring_read<T, VN, kExact>(at + g.slot_bytes, a.dy, a.lddy, a.n, h, r, d);
+    float2 s1 = ln_both(0.0f), s2 = ln_both(0.0f);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-#pragma unroll
-      for (int j = 0; j < VN; ++j) {  // behind the row's end dy is 0
-        xh[k][j] = (xh[k][j] - mean) * rstd;
-        ab[k][j] += d[k][j];
-        aw[k][j] += d[k][j] * xh[k][j];
-        d[k][j] *= w[k][j];
-        s.x += d[k][j];
-        s.y += d[k][j] * xh[k][j];
-      }
+    for (int k = 0; k < 8; ++k) {  // behind the row's end dy and w are 0
+      xh[k] = __fmul2_rn(__fadd2_rn(xh[k], ln_both(-mean)), ln_both(rstd));
+      ab[k] = __fadd2_rn(ab[k], d[k]);
+      aw[k] = __ffma2_rn(d[k], xh[k], aw[k]);
+      d[k] = __fmul2_rn(d[k], w[k]);
+      s1 = __fadd2_rn(s1, d[k]);
+      s2 = __ffma2_rn(d[k], xh[k], s2);
     }
     if (a.dx == nullptr) {  // the same for every thread
       __syncthreads();
       if (t == 0) issue();
     } else {
-      s = ln_row_sum<false>(s, red, buf);
+      const float2 s = ln_row_sum<false>(make_float2(s1.x + s1.y, s2.x + s2.y), red, buf);
       if (t == 0) issue();
-      const float m1 = s.x * inv_h, m2 = s.y * inv_h;
-      T* dx = static_cast<T*>(a.dx) + r * a.lddx;
+      const float2 m1 = ln_both(-s.x * inv_h), m2 = ln_both(-s.y * inv_h);
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int64_t c = (int64_t(k) * tpr + t) * VN;
-        if (c < a.h) {
-#pragma unroll
-          for (int j = 0; j < VN; ++j) d[k][j] = rstd * (d[k][j] - m1 - xh[k][j] * m2);
-          LnIo<T, VN>::store(dx + c, d[k]);
-        }
-      }
+      for (int k = 0; k < 8; ++k)
+        d[k] = __fmul2_rn(__ffma2_rn(xh[k], m2, __fadd2_rn(d[k], m1)), ln_both(rstd));
+      ln_share_store<T, VN, kExact>(static_cast<T*>(a.dx) + r * a.lddx, h, d);
     }
     mean = next_mean;
     rstd = next_rstd;
   }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t c = (int64_t(i) * tpr + t) * VN;
-    if (c >= a.h) continue;
-#pragma unroll
-    for (int j = 0; j < VN; ++j) {
-      const int64_t at = int64_t(blockIdx.x) * a.h + c + j;
-      if (a.part_w) a.part_w[at] = aw[i][j];
-      if (a.part_b) a.part_b[at] = ab[i][j];
-    }
-  }
+  if (a.part_w) ln_share_store<float, VN, kExact>(a.part_w + int64_t(blockIdx.x) * h, h, aw);
+  if (a.part_b) ln_share_store<float, VN, kExact>(a.part_b + int64_t(blockIdx.x) * h, h, ab);
 }
 
 // Long rows: dx row by row (two looks at x and dy) ...
@@ -757,7 +758,7 @@ static LnShape ln_shape(int dtype, int64_t h, int max_vec) {
 // elements where the rows' alignment or length does not allow them; 16 columns a
 // thread (the backward keeps 80 values of them in registers), at least 64 threads.
 struct LnRingShape {
-  int vn, nv, threads, blocks_per_sm;
+  int vn, threads, blocks_per_sm;
   LnRing ring;
   size_t smem;
 };
@@ -767,9 +768,10 @@ static bool ln_ring_shape(int dtype, int64_t h, bool vec, int tensors, int64_t n
   LnRingShape s{};
   s.vn = vec ? 16 / esz : 1;
   const int64_t vecs = cdiv(h, s.vn);
-  s.nv = 16 / s.vn;
-  s.threads = int(cdiv(cdiv(vecs, s.nv), 32) * 32);
-  if (cdiv(vecs, s.nv) > kLnMaxThreads || s.threads < 64) return false;
+  const int64_t want = cdiv(vecs, 16 / s.vn);
+  if (want > kLnMaxThreads) return false;
+  s.threads = int(cdiv(want, 32) * 32);
+  if (s.threads < 64) return false;
   s.blocks_per_sm = std::max(1, kLnMaxThreads / s.threads);
   // fewer rows than two per block: nothing to stream
   if (n < 2 * int64_t(sms) * s.blocks_per_sm) return false;
@@ -860,14 +862,18 @@ static int ln_launch_ring(Kern kern, const Args& a, const LnRingShape& s, int gr
 template <typename T, typename W>
 static int ln_ring_fwd(const LnArgs& a, const LnRingShape& s, int grid, cudaStream_t st) {
   constexpr int kFull = 16 / int(sizeof(T));
-  return s.vn == kFull ? ln_launch_ring(ln_forward_ring_kernel<T, W, kFull, 16 / kFull>, a, s, grid, st)
-                       : ln_launch_ring(ln_forward_ring_kernel<T, W, 1, 16>, a, s, grid, st);
+  if (s.vn == 1) return ln_launch_ring(ln_forward_ring_kernel<T, W, 1, false>, a, s, grid, st);
+  return a.h == int64_t(s.threads) * 16
+             ? ln_launch_ring(ln_forward_ring_kernel<T, W, kFull, true>, a, s, grid, st)
+             : ln_launch_ring(ln_forward_ring_kernel<T, W, kFull, false>, a, s, grid, st);
 }
 template <typename T, typename W>
 static int ln_ring_bwd(const LnBwdArgs& a, const LnRingShape& s, int grid, cudaStream_t st) {
   constexpr int kFull = 16 / int(sizeof(T));
-  return s.vn == kFull ? ln_launch_ring(ln_backward_ring_kernel<T, W, kFull, 16 / kFull>, a, s, grid, st)
-                       : ln_launch_ring(ln_backward_ring_kernel<T, W, 1, 16>, a, s, grid, st);
+  if (s.vn == 1) return ln_launch_ring(ln_backward_ring_kernel<T, W, 1, false>, a, s, grid, st);
+  return a.h == int64_t(s.threads) * 16
+             ? ln_launch_ring(ln_backward_ring_kernel<T, W, kFull, true>, a, s, grid, st)
+             : ln_launch_ring(ln_backward_ring_kernel<T, W, kFull, false>, a, s, grid, st);
 }
 template <typename T, typename W, int VN, int NV>
 static void ln_launch_bwd(const LnBwdArgs& a, const LnShape& s, int grid, cudaStream_t st) {
