@@ -25,18 +25,13 @@
 
 namespace flce {
 
-constexpr int kLnMaxThreads = 512;      // threads per row with the short per-thread share
+constexpr int kLnShare = 16;            // columns per thread
+constexpr int kLnMaxThreads = 512;      // threads per row: rows up to 8192 columns in registers
 constexpr int kLnWarpRows = 4;          // rows (warps) per block when a warp holds a row
-constexpr int kLnRowThreads = 1024;     // resident threads per SM the grid aims at
-constexpr int kLnSms = 148;             // blocks per "one block per SM" of the partials' layout
+constexpr int kLnWarpCols = 32 * kLnShare;
+constexpr int kLnSms = 148;             // SMs the partials' layout is sized for
 constexpr int kLnReduceCols = 32;       // columns per block of the partials' sum
 constexpr int kLnReduceWarps = 16;
-
-// Threads of a block whose threads hold `share` columns each, at most: the
-// backward keeps five values per column in registers.
-__host__ __device__ constexpr int ln_block(int share, bool warp_row) {
-  return warp_row ? 32 * kLnWarpRows : (share > 8 ? kLnMaxThreads : 2 * kLnMaxThreads);
-}
 
 // N consecutive elements at a time, as floats.  The address is aligned to the
 // vector's size (16 bytes at most per access).
@@ -157,68 +152,145 @@ struct LnArgs {
   float* rstd;
 };
 
-// kWarpRow: a warp holds a row (no barrier); else the block does.  A thread's
-// share is NV vectors of VN elements, `tpr` vectors apart.
-template <typename T, typename W, int VN, int NV, bool kWarpRow>
-__global__ void __launch_bounds__(ln_block(VN * NV, kWarpRow))
+// A thread's 16 columns as 8 pairs (packed FP32 arithmetic works on two at a time):
+// vector i of VN columns starts at column (i * tpr + t) * VN for thread t of the
+// tpr that share the row.
+// kExact: the block's shares cover the row exactly; else columns behind its end
+// read as `fill`.
+template <typename T, int VN, bool kExact>
+__device__ __forceinline__ void ln_share_load(const T* src, int t, int tpr, int h, float fill,
+                                              float2 (&v)[8]) {
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16 / VN; ++i) {
+    const int c = (i * tpr + t) * VN;
+    float one[VN];
+#pragma unroll
+    for (int j = 0; j < VN; ++j) one[j] = fill;
+    if (kExact || c < h) LnIo<T, VN>::load(src + c, one);
+#pragma unroll
+    for (int j = 0; j < VN; ++j) x[i * VN + j] = one[j];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
+}
+template <typename T, int VN, bool kExact>
+__device__ __forceinline__ void ln_share_store(T* dst, int t, int tpr, int h,
+                                               const float2 (&v)[8]) {
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = v[i].x;
+    x[2 * i + 1] = v[i].y;
+  }
+#pragma unroll
+  for (int i = 0; i < 16 / VN; ++i) {
+    const int c = (i * tpr + t) * VN;
+    float one[VN];
+#pragma unroll
+    for (int j = 0; j < VN; ++j) one[j] = x[i * VN + j];
+    if (kExact || c < h) LnIo<T, VN>::store(dst + c, one);
+  }
+}
+// Zeroes the columns behind the row's end.
+template <int VN>
+__device__ __forceinline__ void ln_share_clip(int t, int tpr, int h, float2 (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int i = e / VN;
+    if ((i * tpr + t) * VN >= h) (e % 2 ? v[e / 2].y : v[e / 2].x) = 0.0f;
+  }
+}
+__device__ __forceinline__ float2 ln_both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float ln_share_sum(const float2 (&v)[8]) {
+  float2 s = v[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s = __fadd2_rn(s, v[i]);
+  return s.x + s.y;
+}
+// Subtracts the mean; returns the share's sum of squares.
+template <int VN, bool kExact>
+__device__ __forceinline__ float ln_share_centre(float mean, int t, int tpr, int h, float2 (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __fadd2_rn(v[i], ln_both(-mean));
+  if constexpr (!kExact) ln_share_clip<VN>(t, tpr, h, v);
+  float2 s = __fmul2_rn(v[0], v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s = __ffma2_rn(v[i], v[i], s);
+  return s.x + s.y;
+}
+// xhat in place of x, the row's shares of dw and db, g = dy w in place of dy;
+// returns the shares of sum g and sum g xhat.  Behind the row's end dy is 0.
+__device__ __forceinline__ float2 ln_share_grads(float mean, float rstd, const float2 (&w)[8],
+                                                 float2 (&xh)[8], float2 (&d)[8], float2 (&aw)[8],
+                                                 float2 (&ab)[8]) {
+  float2 s1 = ln_both(0.0f), s2 = ln_both(0.0f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    xh[k] = __fmul2_rn(__fadd2_rn(xh[k], ln_both(-mean)), ln_both(rstd));
+    ab[k] = __fadd2_rn(ab[k], d[k]);
+    aw[k] = __ffma2_rn(d[k], xh[k], aw[k]);
+    d[k] = __fmul2_rn(d[k], w[k]);
+    s1 = __fadd2_rn(s1, d[k]);
+    s2 = __ffma2_rn(d[k], xh[k], s2);
+  }
+  return make_float2(s1.x + s1.y, s2.x + s2.y);
+}
+// dx in place of g, from the row's sums of g and g xhat over H.
+__device__ __forceinline__ void ln_share_dx(float2 means, float rstd, const float2 (&xh)[8],
+                                            float2 (&d)[8]) {
+  const float2 m1 = ln_both(-means.x), m2 = ln_both(-means.y);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    d[k] = __fmul2_rn(__ffma2_rn(xh[k], m2, __fadd2_rn(d[k], m1)), ln_both(rstd));
+}
+
+// Rows straight from global memory: few rows, or rows that a warp holds (kWarpRow;
+// no barriers).  Two rows at a time: both sums of a reduction travel together.
+template <typename T, typename W, int VN, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarpRows : kLnMaxThreads)
     ln_forward_kernel(const LnArgs a) {
   __shared__ float2 red[2][32];
-  const int tpr = kWarpRow ? 32 : int(blockDim.x);
+  const int tpr = kWarpRow ? 32 : int(blockDim.x), h = int(a.h);
   const int t = kWarpRow ? int(threadIdx.x & 31) : int(threadIdx.x);
   const int rpb = kWarpRow ? int(blockDim.x >> 5) : 1;
-  const int64_t r0 = int64_t(blockIdx.x) * rpb + (kWarpRow ? int(threadIdx.x >> 5) : 0);
   const int64_t step = int64_t(gridDim.x) * rpb;
-  const float inv_h = 1.0f / float(a.h);
+  const float inv_h = 1.0f / float(h);
   int buf = 0;
-  for (int64_t r = r0; r < a.n; r += step) {  // uniform over the threads that share a row
-    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
-    float v[NV][VN];
-    float2 s = make_float2(0.0f, 0.0f);
+  float2 w[8], b[8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t(i) * tpr + t) * VN;
-      if (c < a.h) {
-        LnIo<T, VN>::load(x + c, v[i]);
-#pragma unroll
-        for (int j = 0; j < VN; ++j) s.x += v[i][j];
-      }
-    }
-    const float mean = ln_row_sum<kWarpRow>(s, red, buf).x * inv_h;
-    s = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t(i) * tpr + t) * VN;
-      if (c < a.h) {
-#pragma unroll
-        for (int j = 0; j < VN; ++j) {
-          v[i][j] -= mean;
-          s.x += v[i][j] * v[i][j];
-        }
-      }
-    }
-    const float rstd = 1.0f / sqrtf(ln_row_sum<kWarpRow>(s, red, buf).x * inv_h + a.eps);
+  for (int i = 0; i < 8; ++i) {
+    w[i] = ln_both(1.0f);
+    b[i] = ln_both(0.0f);
+  }
+  if (a.w) ln_share_load<W, VN, false>(static_cast<const W*>(a.w), t, tpr, h, 0.0f, w);
+  if (a.b) ln_share_load<W, VN, false>(static_cast<const W*>(a.b), t, tpr, h, 0.0f, b);
+  auto finish = [&](int64_t r, float2 (&v)[8], float mean, float rstd) {
     if (t == 0) {
       if (a.mean) a.mean[r] = mean;
       if (a.rstd) a.rstd[r] = rstd;
     }
-    T* y = static_cast<T*>(a.y) + r * a.ldy;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t(i) * tpr + t) * VN;
-      if (c < a.h) {
-        float w[VN], b[VN];
-        if (a.w) LnIo<W, VN>::load(static_cast<const W*>(a.w) + c, w);
-        if (a.b) LnIo<W, VN>::load(static_cast<const W*>(a.b) + c, b);
+    for (int i = 0; i < 8; ++i) v[i] = __ffma2_rn(__fmul2_rn(v[i], ln_both(rstd)), w[i], b[i]);
+    ln_share_store<T, VN, false>(static_cast<T*>(a.y) + r * a.ldy, t, tpr, h, v);
+  };
+  // The loop is uniform over the threads that share a row.
+  for (int64_t r = int64_t(blockIdx.x) * rpb + (kWarpRow ? int(threadIdx.x >> 5) : 0); r < a.n;
+       r += 2 * step) {
+    const bool two = r + step < a.n;
+    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+    float2 v0[8], v1[8];
 #pragma unroll
-        for (int j = 0; j < VN; ++j) {
-          float o = v[i][j] * rstd;
-          if (a.w) o *= w[j];
-          if (a.b) o += b[j];
-          v[i][j] = o;
-        }
-        LnIo<T, VN>::store(y + c, v[i]);
-      }
-    }
+    for (int k = 0; k < 8; ++k) v1[k] = ln_both(0.0f);
+    ln_share_load<T, VN, false>(x, t, tpr, h, 0.0f, v0);
+    if (two) ln_share_load<T, VN, false>(x + step * a.ldx, t, tpr, h, 0.0f, v1);
+    float2 s = ln_row_sum<kWarpRow>(make_float2(ln_share_sum(v0), ln_share_sum(v1)), red, buf);
+    const float m0 = s.x * inv_h, m1 = s.y * inv_h;
+    s = make_float2(ln_share_centre<VN, false>(m0, t, tpr, h, v0),
+                    ln_share_centre<VN, false>(m1, t, tpr, h, v1));
+    s = ln_row_sum<kWarpRow>(s, red, buf);
+    finish(r, v0, m0, 1.0f / sqrtf(s.x * inv_h + a.eps));
+    if (two) finish(r + step, v1, m1, 1.0f / sqrtf(s.y * inv_h + a.eps));
   }
 }
 
@@ -274,67 +346,22 @@ __device__ __forceinline__ LnRingRow ln_ring_row(const void* base, int64_t ld, i
   row.direct = (r == 0 && row.phase != 0) || (r == n - 1 && row.bytes != len);
   return row;
 }
-// A thread's 16 columns as 8 pairs (packed FP32 arithmetic works on two at a time):
-// vector i of VN columns starts at column (i * blockDim.x + threadIdx.x) * VN.
-// kExact: the block's shares cover the row exactly; else columns behind its end
-// read as `fill`.
-template <typename T, int VN, bool kExact>
-__device__ __forceinline__ void ln_share_load(const T* src, int h, float fill, float2 (&v)[8]) {
-  float x[16];
-#pragma unroll
-  for (int i = 0; i < 16 / VN; ++i) {
-    const int c = (i * int(blockDim.x) + int(threadIdx.x)) * VN;
-    float one[VN];
-#pragma unroll
-    for (int j = 0; j < VN; ++j) one[j] = fill;
-    if (kExact || c < h) LnIo<T, VN>::load(src + c, one);
-#pragma unroll
-    for (int j = 0; j < VN; ++j) x[i * VN + j] = one[j];
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
-}
-template <typename T, int VN, bool kExact>
-__device__ __forceinline__ void ln_share_store(T* dst, int h, const float2 (&v)[8]) {
-  float x[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = v[i].x;
-    x[2 * i + 1] = v[i].y;
-  }
-#pragma unroll
-  for (int i = 0; i < 16 / VN; ++i) {
-    const int c = (i * int(blockDim.x) + int(threadIdx.x)) * VN;
-    float one[VN];
-#pragma unroll
-    for (int j = 0; j < VN; ++j) one[j] = x[i * VN + j];
-    if (kExact || c < h) LnIo<T, VN>::store(dst + c, one);
-  }
-}
-// Zeroes the columns behind the row's end.
-template <int VN>
-__device__ __forceinline__ void ln_share_clip(int h, float2 (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int i = e / VN;
-    if ((i * int(blockDim.x) + int(threadIdx.x)) * VN >= h) (e % 2 ? v[e / 2].y : v[e / 2].x) = 0.0f;
-  }
-}
 template <typename T, int VN, bool kExact>
 __device__ __forceinline__ void ln_ring_read(const uint8_t* slot, const void* base, int64_t ld,
                                              int64_t n, int h, int64_t r, float2 (&v)[8]) {
   if constexpr (VN == 1) {
     const LnRingRow row = ln_ring_row<T>(base, ld, n, h, r);
     if (row.direct)
-      ln_share_load<T, VN, kExact>(reinterpret_cast<const T*>(row.begin + row.phase), h, 0.0f, v);
+      ln_share_load<T, VN, kExact>(reinterpret_cast<const T*>(row.begin + row.phase), threadIdx.x,
+                                   blockDim.x, h, 0.0f, v);
     else
-      ln_share_load<T, VN, kExact>(reinterpret_cast<const T*>(slot + row.phase), h, 0.0f, v);
+      ln_share_load<T, VN, kExact>(reinterpret_cast<const T*>(slot + row.phase), threadIdx.x,
+                                   blockDim.x, h, 0.0f, v);
   } else {  // whole rows of 16-byte pieces: never direct
-    ln_share_load<T, VN, kExact>(reinterpret_cast<const T*>(slot), h, 0.0f, v);
+    ln_share_load<T, VN, kExact>(reinterpret_cast<const T*>(slot), threadIdx.x, blockDim.x, h, 0.0f,
+                                 v);
   }
 }
-__device__ __forceinline__ float2 ln_both(float x) { return make_float2(x, x); }
-
 // Two rows at a time: both sums of a reduction travel together.
 template <typename T, typename W, int VN, bool kExact>
 __global__ void __launch_bounds__(kLnMaxThreads, 1)
@@ -343,7 +370,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
   __shared__ __align__(8) uint64_t full[kLnSlots];
   __shared__ float2 red[2][32];
   __shared__ PipeCtl ctl;
-  const int t = threadIdx.x, h = int(a.h);
+  const int t = threadIdx.x, tpr = blockDim.x, h = int(a.h);
   const int count = int((a.n - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this block's rows
   int loaded = 0;  // thread 0: rows issued so far, and the slot of the next
   LnRingPos put, get;
@@ -372,8 +399,8 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     w[i] = ln_both(1.0f);
     b[i] = ln_both(0.0f);
   }
-  if (a.w) ln_share_load<W, VN, kExact>(static_cast<const W*>(a.w), h, 0.0f, w);
-  if (a.b) ln_share_load<W, VN, kExact>(static_cast<const W*>(a.b), h, 0.0f, b);
+  if (a.w) ln_share_load<W, VN, kExact>(static_cast<const W*>(a.w), t, tpr, h, 0.0f, w);
+  if (a.b) ln_share_load<W, VN, kExact>(static_cast<const W*>(a.b), t, tpr, h, 0.0f, b);
   __syncthreads();
   const float inv_h = 1.0f / float(h);
   int buf = 0;
@@ -383,21 +410,6 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     ln_ring_read<T, VN, kExact>(ring + uint32_t(get.slot) * g.slot_bytes, a.x, a.ldx, a.n, h, r, v);
     get.advance(g.slots);
   };
-  auto sum = [&](const float2 (&v)[8]) {
-    float2 s = v[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s = __fadd2_rn(s, v[i]);
-    return s.x + s.y;
-  };
-  auto centre = [&](float mean, float2 (&v)[8]) {  // and the sum of squares
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fadd2_rn(v[i], ln_both(-mean));
-    if constexpr (!kExact) ln_share_clip<VN>(h, v);
-    float2 s = __fmul2_rn(v[0], v[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) s = __ffma2_rn(v[i], v[i], s);
-    return s.x + s.y;
-  };
   auto finish = [&](int64_t r, float2 (&v)[8], float mean, float rstd) {
     if (t == 0) {
       if (a.mean) a.mean[r] = mean;
@@ -405,7 +417,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __ffma2_rn(__fmul2_rn(v[i], ln_both(rstd)), w[i], b[i]);
-    ln_share_store<T, VN, kExact>(static_cast<T*>(a.y) + r * a.ldy, h, v);
+    ln_share_store<T, VN, kExact>(static_cast<T*>(a.y) + r * a.ldy, t, tpr, h, v);
   };
   int64_t r = blockIdx.x;
   for (int i = 0; i < count; i += 2, r += 2 * int64_t(gridDim.x)) {
@@ -415,13 +427,14 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     for (int k = 0; k < 8; ++k) v1[k] = ln_both(0.0f);
     fetch(r, v0);
     if (two) fetch(r + gridDim.x, v1);
-    float2 s = ln_row_sum<false>(make_float2(sum(v0), sum(v1)), red, buf);
+    float2 s = ln_row_sum<false>(make_float2(ln_share_sum(v0), ln_share_sum(v1)), red, buf);
     if (t == 0) {
       issue();
       if (two) issue();
     }
     const float m0 = s.x * inv_h, m1 = s.y * inv_h;
-    s = make_float2(centre(m0, v0), centre(m1, v1));
+    s = make_float2(ln_share_centre<VN, kExact>(m0, t, tpr, h, v0),
+                    ln_share_centre<VN, kExact>(m1, t, tpr, h, v1));
     s = ln_row_sum<false>(s, red, buf);
     finish(r, v0, m0, 1.0f / sqrtf(s.x * inv_h + a.eps));
     if (two) finish(r + gridDim.x, v1, m1, 1.0f / sqrtf(s.y * inv_h + a.eps));
@@ -485,82 +498,57 @@ struct LnBwdArgs {
   float* part_b;
 };
 
-template <typename T, typename W, int VN, int NV, bool kWarpRow>
-__global__ void __launch_bounds__(ln_block(VN * NV, kWarpRow))
+template <typename T, typename W, int VN, bool kWarpRow>
+__global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarpRows : kLnMaxThreads)
     ln_backward_kernel(const LnBwdArgs a) {
   __shared__ float2 red[2][32];
-  const int tpr = kWarpRow ? 32 : int(blockDim.x);
+  __shared__ __align__(16) float part[kWarpRow ? kLnWarpRows : 1][kWarpRow ? kLnWarpCols : 4];
+  grid_launch_dependents();
+  const int tpr = kWarpRow ? 32 : int(blockDim.x), h = int(a.h);
   const int t = kWarpRow ? int(threadIdx.x & 31) : int(threadIdx.x);
-  const int rpb = kWarpRow ? int(blockDim.x >> 5) : 1;
-  const int64_t r0 = int64_t(blockIdx.x) * rpb + (kWarpRow ? int(threadIdx.x >> 5) : 0);
+  const int warp = threadIdx.x >> 5;
+  const int rpb = kWarpRow ? kLnWarpRows : 1;
   const int64_t step = int64_t(gridDim.x) * rpb;
-  const float inv_h = 1.0f / float(a.h);
+  const float inv_h = 1.0f / float(h);
   int buf = 0;
-  float w[NV][VN], aw[NV][VN], ab[NV][VN];
+  float2 w[8], aw[8], ab[8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int64_t c = (int64_t(i) * tpr + t) * VN;
-#pragma unroll
-    for (int j = 0; j < VN; ++j) {
-      w[i][j] = 1.0f;
-      aw[i][j] = 0.0f;
-      ab[i][j] = 0.0f;
-    }
-    if (a.w && c < a.h) LnIo<W, VN>::load(static_cast<const W*>(a.w) + c, w[i]);
+  for (int i = 0; i < 8; ++i) {
+    w[i] = ln_both(1.0f);
+    aw[i] = ab[i] = ln_both(0.0f);
   }
-  for (int64_t r = r0; r < a.n; r += step) {
-    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
-    const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
+  if (a.w) ln_share_load<W, VN, false>(static_cast<const W*>(a.w), t, tpr, h, 0.0f, w);
+  for (int64_t r = int64_t(blockIdx.x) * rpb + (kWarpRow ? warp : 0); r < a.n; r += step) {
     const float mean = a.mean[r], rstd = a.rstd[r];
-    float xh[NV][VN], g[NV][VN];
-    float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t(i) * tpr + t) * VN;
-      if (c < a.h) {
-        LnIo<T, VN>::load(x + c, xh[i]);
-        LnIo<T, VN>::load(dy + c, g[i]);
-#pragma unroll
-        for (int j = 0; j < VN; ++j) {
-          xh[i][j] = (xh[i][j] - mean) * rstd;
-          ab[i][j] += g[i][j];
-          aw[i][j] += g[i][j] * xh[i][j];
-          g[i][j] *= w[i][j];
-          s.x += g[i][j];
-          s.y += g[i][j] * xh[i][j];
-        }
-      }
-    }
+    float2 xh[8], d[8];
+    ln_share_load<T, VN, false>(static_cast<const T*>(a.x) + r * a.ldx, t, tpr, h, 0.0f, xh);
+    ln_share_load<T, VN, false>(static_cast<const T*>(a.dy) + r * a.lddy, t, tpr, h, 0.0f, d);
+    float2 s = ln_share_grads(mean, rstd, w, xh, d, aw, ab);
     if (a.dx == nullptr) continue;  // the same for every thread
     s = ln_row_sum<kWarpRow>(s, red, buf);
-    const float m1 = s.x * inv_h, m2 = s.y * inv_h;
-    T* dx = static_cast<T*>(a.dx) + r * a.lddx;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t(i) * tpr + t) * VN;
-      if (c < a.h) {
-#pragma unroll
-        for (int j = 0; j < VN; ++j) g[i][j] = rstd * (g[i][j] - m1 - xh[i][j] * m2);
-        LnIo<T, VN>::store(dx + c, g[i]);
-      }
-    }
+    ln_share_dx(make_float2(s.x * inv_h, s.y * inv_h), rstd, xh, d);
+    ln_share_store<T, VN, false>(static_cast<T*>(a.dx) + r * a.lddx, t, tpr, h, d);
   }
-  if (a.part_w == nullptr && a.part_b == nullptr) return;
-  // The block's partial row: the block's only row group, or the sum over its
-  // warps, one warp after the other (each column stays with one lane).
-  for (int turn = 0; turn < rpb; ++turn) {
-    if (kWarpRow) __syncthreads();
-    if (kWarpRow && int(threadIdx.x >> 5) != turn) continue;
+  // The block's row of partials: its threads' sums, or the sum over its warps.
+  float* out[2] = {a.part_w, a.part_b};
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t(i) * tpr + t) * VN;
-      if (c >= a.h) continue;
+  for (int p = 0; p < 2; ++p) {
+    if (out[p] == nullptr) continue;
+    float* to = out[p] + int64_t(blockIdx.x) * h;
+    if constexpr (kWarpRow) {
+      ln_share_store<float, VN, false>(part[warp], t, tpr, h, p == 0 ? aw : ab);
+    } else {
+      ln_share_store<float, VN, false>(to, t, tpr, h, p == 0 ? aw : ab);
+    }
+    if constexpr (kWarpRow) {
+      __syncthreads();
+      for (int c = threadIdx.x; c < h; c += 32 * kLnWarpRows) {
+        float v = part[0][c];
 #pragma unroll
-      for (int j = 0; j < VN; ++j) {
-        const int64_t at = int64_t(blockIdx.x) * a.h + c + j;
-        if (a.part_w) a.part_w[at] = turn == 0 ? aw[i][j] : a.part_w[at] + aw[i][j];
-        if (a.part_b) a.part_b[at] = turn == 0 ? ab[i][j] : a.part_b[at] + ab[i][j];
+        for (int k = 1; k < kLnWarpRows; ++k) v += part[k][c];
+        to[c] = v;
       }
+      __syncthreads();
     }
   }
 }
@@ -573,7 +561,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
   __shared__ __align__(8) uint64_t full[kLnSlots];
   __shared__ float2 red[2][32];
   __shared__ PipeCtl ctl;
-  const int t = threadIdx.x, h = int(a.h);
+  const int t = threadIdx.x, tpr = blockDim.x, h = int(a.h);
   const int count = int((a.n - blockIdx.x + gridDim.x - 1) / gridDim.x);
   int loaded = 0;  // thread 0: rows issued so far, and the slot of the next
   LnRingPos put, get;
@@ -606,7 +594,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     w[i] = ln_both(1.0f);
     aw[i] = ab[i] = ln_both(0.0f);
   }
-  if (a.w) ln_share_load<W, VN, kExact>(static_cast<const W*>(a.w), h, 0.0f, w);
+  if (a.w) ln_share_load<W, VN, kExact>(static_cast<const W*>(a.w), t, tpr, h, 0.0f, w);
   __syncthreads();
   const float inv_h = 1.0f / float(h);
   int buf = 0;
@@ -621,33 +609,21 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     float2 xh[8], d[8];
     ln_ring_read<T, VN, kExact>(at, a.x, a.ldx, a.n, h, r, xh);
     ln_ring_read<T, VN, kExact>(at + g.slot_bytes, a.dy, a.lddy, a.n, h, r, d);
-    float2 s1 = ln_both(0.0f), s2 = ln_both(0.0f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {  // behind the row's end dy and w are 0
-      xh[k] = __fmul2_rn(__fadd2_rn(xh[k], ln_both(-mean)), ln_both(rstd));
-      ab[k] = __fadd2_rn(ab[k], d[k]);
-      aw[k] = __ffma2_rn(d[k], xh[k], aw[k]);
-      d[k] = __fmul2_rn(d[k], w[k]);
-      s1 = __fadd2_rn(s1, d[k]);
-      s2 = __ffma2_rn(d[k], xh[k], s2);
-    }
+    float2 s = ln_share_grads(mean, rstd, w, xh, d, aw, ab);
     if (a.dx == nullptr) {  // the same for every thread
       __syncthreads();
       if (t == 0) issue();
     } else {
-      const float2 s = ln_row_sum<false>(make_float2(s1.x + s1.y, s2.x + s2.y), red, buf);
+      s = ln_row_sum<false>(s, red, buf);
       if (t == 0) issue();
-      const float2 m1 = ln_both(-s.x * inv_h), m2 = ln_both(-s.y * inv_h);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        d[k] = __fmul2_rn(__ffma2_rn(xh[k], m2, __fadd2_rn(d[k], m1)), ln_both(rstd));
-      ln_share_store<T, VN, kExact>(static_cast<T*>(a.dx) + r * a.lddx, h, d);
+      ln_share_dx(make_float2(s.x * inv_h, s.y * inv_h), rstd, xh, d);
+      ln_share_store<T, VN, kExact>(static_cast<T*>(a.dx) + r * a.lddx, t, tpr, h, d);
     }
     mean = next_mean;
     rstd = next_rstd;
   }
-  if (a.part_w) ln_share_store<float, VN, kExact>(a.part_w + int64_t(blockIdx.x) * h, h, aw);
-  if (a.part_b) ln_share_store<float, VN, kExact>(a.part_b + int64_t(blockIdx.x) * h, h, ab);
+  if (a.part_w) ln_share_store<float, VN, kExact>(a.part_w + int64_t(blockIdx.x) * h, t, tpr, h, aw);
+  if (a.part_b) ln_share_store<float, VN, kExact>(a.part_b + int64_t(blockIdx.x) * h, t, tpr, h, ab);
 }
 
 // Long rows: dx row by row (two looks at x and dy) ...
@@ -707,6 +683,7 @@ __global__ void __launch_bounds__(32 * kLnReduceWarps)
   const float* part = blockIdx.y == 0 ? part_w : part_b;
   W* out = blockIdx.y == 0 ? dw : db;
   if (out == nullptr) return;
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = int64_t(blockIdx.x) * kLnReduceCols + lane;
   float s = 0.0f;
@@ -722,41 +699,27 @@ __global__ void __launch_bounds__(32 * kLnReduceWarps)
   LnIo<W, 1>::store(out + c, o);
 }
 
-// How a row is laid over threads: the widest vector that every pointer and row
-// stride allows, then a warp per row while a lane's share is at most NV = 2
-// vectors (8 narrow ones), then one block per row.
+// How a row is laid over threads, 16 columns each: whole 16-byte vectors where every
+// pointer, row stride and the row's length allow them, else single elements; a
+// warp per row while that suffices, then one block per row.
 struct LnShape {
   int vn;        // elements per vector (0: the row is too long for registers)
-  int nv;        // vectors per thread
   int threads;   // per block
   bool warp_row;
   int rpb;       // rows per block
 };
 
-static LnShape ln_shape(int dtype, int64_t h, int max_vec) {
-  const int full = dtype == FLCE_BF16 ? 8 : 4;
+static LnShape ln_shape(int dtype, int64_t h, bool vec) {
   LnShape s{};
-  s.vn = max_vec >= full ? full : (dtype == FLCE_BF16 && max_vec >= 2 ? 2 : 1);
-  const int64_t vecs = (h + s.vn - 1) / s.vn;
-  const bool wide = s.vn == full;
-  s.nv = wide ? 2 : 8;
-  if (vecs <= 32 * s.nv) {
-    s.warp_row = true;
-    s.threads = 32 * kLnWarpRows;
-    s.rpb = kLnWarpRows;
-    return s;
-  }
-  if (wide && vecs > int64_t(kLnMaxThreads) * s.nv) s.nv = 4;
-  const int64_t t = (vecs + s.nv - 1) / s.nv;
-  s.rpb = 1;
-  s.threads = int((t + 31) / 32 * 32);
-  if (t > ln_block(s.nv * s.vn, false)) s.vn = 0;
+  s.vn = vec ? (dtype == FLCE_BF16 ? 8 : 4) : 1;
+  s.warp_row = h <= kLnWarpCols;
+  s.rpb = s.warp_row ? kLnWarpRows : 1;
+  s.threads = s.warp_row ? 32 * kLnWarpRows : int(std::min<int64_t>(cdiv(h, 32 * kLnShare) * 32, 1024));
+  if (h > kLnMaxThreads * kLnShare) s.vn = 0;
   return s;
 }
 
-// How a ring kernel lays a row over threads: whole 16-byte vectors, or single
-// elements where the rows' alignment or length does not allow them; 16 columns a
-// thread (the backward keeps 80 values of them in registers), at least 64 threads.
+// The ring's plan for rows that a block holds.
 struct LnRingShape {
   int vn, threads, blocks_per_sm;
   LnRing ring;
@@ -767,11 +730,8 @@ static bool ln_ring_shape(int dtype, int64_t h, bool vec, int tensors, int64_t n
   const int esz = dtype == FLCE_F32 ? 4 : 2;
   LnRingShape s{};
   s.vn = vec ? 16 / esz : 1;
-  const int64_t vecs = cdiv(h, s.vn);
-  const int64_t want = cdiv(vecs, 16 / s.vn);
-  if (want > kLnMaxThreads) return false;
-  s.threads = int(cdiv(want, 32) * 32);
-  if (s.threads < 64) return false;
+  if (h <= kLnWarpCols || h > kLnMaxThreads * kLnShare) return false;
+  s.threads = int(cdiv(h, 32 * kLnShare) * 32);
   s.blocks_per_sm = std::max(1, kLnMaxThreads / s.threads);
   // fewer rows than two per block: nothing to stream
   if (n < 2 * int64_t(sms) * s.blocks_per_sm) return false;
@@ -784,38 +744,26 @@ static bool ln_ring_shape(int dtype, int64_t h, bool vec, int tensors, int64_t n
   return true;
 }
 
-// Largest vector (elements, a power of two) that all rows of a tensor allow.
-static int ln_vec(const void* p, int64_t ld, int64_t h, int esz) {
-  if (p == nullptr) return 8;
-  int v = 16 / esz;
-  while (v > 1 && ((reinterpret_cast<uintptr_t>(p) % (size_t(v) * esz)) != 0 || ld % v != 0 || h % v != 0))
-    v >>= 1;
-  return v;
-}
-static int ln_vec_w(const void* p, int esz) {  // the weights: one row, up to 8 elements as 16-byte loads
-  if (p == nullptr) return 8;
-  int v = 8;
-  while (v > 1 && (reinterpret_cast<uintptr_t>(p) % size_t(std::min(16, v * esz))) != 0) v >>= 1;
-  return v;
+// True when all rows of a tensor are whole, aligned 16-byte vectors.
+static bool ln_vec(const void* p, int64_t ld, int64_t h, int esz) {
+  return p == nullptr || (aligned(p, 16) && (ld * esz) % 16 == 0 && (h * esz) % 16 == 0);
 }
 
 // Rows of partials of the weight gradients: one per block of the backward.
 static int64_t ln_parts(int64_t n, const LnShape& s) {
-  const int64_t per_sm = std::max<int64_t>(1, kLnRowThreads / std::max(s.threads, 1));
-  return std::max<int64_t>(1, std::min<int64_t>(cdiv(std::max<int64_t>(n, 1), std::max(s.rpb, 1)),
-                                                kLnSms * per_sm));
+  const int64_t per_sm = std::max(1, kLnMaxThreads / s.threads);
+  return std::min<int64_t>(cdiv(std::max<int64_t>(n, 1), s.rpb), kLnSms * per_sm);
 }
 // Before the pointers' alignment is known: the most any layout takes.
 static int64_t ln_max_parts(int64_t n, int64_t h) {
   int64_t parts = std::min<int64_t>(std::max<int64_t>(n, 1), kLnSms);  // long rows
   for (int dtype = 0; dtype < 2; ++dtype)
     for (int vec = 0; vec < 2; ++vec) {
+      parts = std::max(parts, ln_parts(n, ln_shape(dtype, h, vec != 0)));
       LnRingShape r;
       if (ln_ring_shape(dtype, h, vec != 0, 2, n, 1, &r))
         parts = std::max<int64_t>(parts, int64_t(kLnSms) * r.blocks_per_sm);
     }
-  for (int dtype = 0; dtype < 2; ++dtype)
-    for (int v = 1; v <= 8; v *= 2) parts = std::max(parts, ln_parts(n, ln_shape(dtype, h, v)));
   return parts;
 }
 
@@ -827,29 +775,19 @@ static bool ln_ld_ok(int64_t n, int64_t h, int64_t ld) {
 }
 static bool ln_dtype_ok(int d) { return d == FLCE_BF16 || d == FLCE_F32; }
 
-template <typename T, typename W, int VN, int NV>
-static void ln_launch_fwd(const LnArgs& a, const LnShape& s, int grid, cudaStream_t st) {
-  if constexpr (NV != 4) {  // the warp-per-row layouts
-    if (s.warp_row) {
-      ln_forward_kernel<T, W, VN, NV, true><<<grid, s.threads, 0, st>>>(a);
-      return;
-    }
-  }
-  ln_forward_kernel<T, W, VN, NV, false><<<grid, s.threads, 0, st>>>(a);
-}
 template <typename T, typename W>
 static void ln_dispatch_fwd(const LnArgs& a, const LnShape& s, int grid, cudaStream_t st) {
   constexpr int kFull = 16 / int(sizeof(T));
   if (s.vn == 0)
     ln_forward_long_kernel<T, W><<<grid, 1024, 0, st>>>(a);
-  else if (s.vn == kFull && s.nv == 2)
-    ln_launch_fwd<T, W, kFull, 2>(a, s, grid, st);
-  else if (s.vn == kFull)
-    ln_launch_fwd<T, W, kFull, 4>(a, s, grid, st);
-  else if (sizeof(T) == 2 && s.vn == 2)
-    ln_launch_fwd<T, W, 2, 8>(a, s, grid, st);
+  else if (s.vn == 1 && s.warp_row)
+    ln_forward_kernel<T, W, 1, true><<<grid, s.threads, 0, st>>>(a);
+  else if (s.vn == 1)
+    ln_forward_kernel<T, W, 1, false><<<grid, s.threads, 0, st>>>(a);
+  else if (s.warp_row)
+    ln_forward_kernel<T, W, kFull, true><<<grid, s.threads, 0, st>>>(a);
   else
-    ln_launch_fwd<T, W, 1, 8>(a, s, grid, st);
+    ln_forward_kernel<T, W, kFull, false><<<grid, s.threads, 0, st>>>(a);
 }
 template <typename Kern, typename Args>
 static int ln_launch_ring(Kern kern, const Args& a, const LnRingShape& s, int grid, cudaStream_t st) {
@@ -863,7 +801,7 @@ template <typename T, typename W>
 static int ln_ring_fwd(const LnArgs& a, const LnRingShape& s, int grid, cudaStream_t st) {
   constexpr int kFull = 16 / int(sizeof(T));
   if (s.vn == 1) return ln_launch_ring(ln_forward_ring_kernel<T, W, 1, false>, a, s, grid, st);
-  return a.h == int64_t(s.threads) * 16
+  return a.h == int64_t(s.threads) * kLnShare
              ? ln_launch_ring(ln_forward_ring_kernel<T, W, kFull, true>, a, s, grid, st)
              : ln_launch_ring(ln_forward_ring_kernel<T, W, kFull, false>, a, s, grid, st);
 }
@@ -871,31 +809,21 @@ template <typename T, typename W>
 static int ln_ring_bwd(const LnBwdArgs& a, const LnRingShape& s, int grid, cudaStream_t st) {
   constexpr int kFull = 16 / int(sizeof(T));
   if (s.vn == 1) return ln_launch_ring(ln_backward_ring_kernel<T, W, 1, false>, a, s, grid, st);
-  return a.h == int64_t(s.threads) * 16
+  return a.h == int64_t(s.threads) * kLnShare
              ? ln_launch_ring(ln_backward_ring_kernel<T, W, kFull, true>, a, s, grid, st)
              : ln_launch_ring(ln_backward_ring_kernel<T, W, kFull, false>, a, s, grid, st);
-}
-template <typename T, typename W, int VN, int NV>
-static void ln_launch_bwd(const LnBwdArgs& a, const LnShape& s, int grid, cudaStream_t st) {
-  if constexpr (NV != 4) {  // the warp-per-row layouts
-    if (s.warp_row) {
-      ln_backward_kernel<T, W, VN, NV, true><<<grid, s.threads, 0, st>>>(a);
-      return;
-    }
-  }
-  ln_backward_kernel<T, W, VN, NV, false><<<grid, s.threads, 0, st>>>(a);
 }
 template <typename T, typename W>
 static void ln_dispatch_bwd(const LnBwdArgs& a, const LnShape& s, int grid, cudaStream_t st) {
   constexpr int kFull = 16 / int(sizeof(T));
-  if (s.vn == kFull && s.nv == 2)
-    ln_launch_bwd<T, W, kFull, 2>(a, s, grid, st);
-  else if (s.vn == kFull)
-    ln_launch_bwd<T, W, kFull, 4>(a, s, grid, st);
-  else if (sizeof(T) == 2 && s.vn == 2)
-    ln_launch_bwd<T, W, 2, 8>(a, s, grid, st);
+  if (s.vn == 1 && s.warp_row)
+    ln_backward_kernel<T, W, 1, true><<<grid, s.threads, 0, st>>>(a);
+  else if (s.vn == 1)
+    ln_backward_kernel<T, W, 1, false><<<grid, s.threads, 0, st>>>(a);
+  else if (s.warp_row)
+    ln_backward_kernel<T, W, kFull, true><<<grid, s.threads, 0, st>>>(a);
   else
-    ln_launch_bwd<T, W, 1, 8>(a, s, grid, st);
+    ln_backward_kernel<T, W, kFull, false><<<grid, s.threads, 0, st>>>(a);
 }
 
 }  // namespace flce
@@ -923,11 +851,11 @@ extern "C" int flce_layer_norm_forward(const void* x, int dtype, int64_t n, int6
   const int st = device_info(&dev);
   if (st != FLCE_OK) return st;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const LnShape s = ln_shape(dtype, h, std::min({ln_vec(x, ldx, h, esz), ln_vec(y, ldy, h, esz),
-                                                 ln_vec_w(weight, wsz), ln_vec_w(bias, wsz)}));
+  const LnShape s = ln_shape(dtype, h, ln_vec(x, ldx, h, esz) && ln_vec(y, ldy, h, esz) &&
+                                           aligned(weight, 16) && aligned(bias, 16));
   const LnArgs a{x, ldx, weight, bias, n, h, eps, y, ldy, mean, rstd};
   LnRingShape rs;
-  if (ln_ring_shape(dtype, h, s.vn == 16 / esz, 1, n, dev->num_sms, &rs)) {
+  if (ln_ring_shape(dtype, h, s.vn > 1, 1, n, dev->num_sms, &rs)) {
     rs.ring.err = dev->err;
     rs.ring.timeout_ns = kDefaultTimeoutNs;
     const int grid = dev->num_sms * rs.blocks_per_sm;
@@ -982,12 +910,12 @@ extern "C" int flce_layer_norm_backward(const void* dy, int64_t lddy, const void
   int parts = 0;
   if (n > 0) {
     const LnShape s =
-        ln_shape(dtype, h, std::min({ln_vec(x, ldx, h, esz), ln_vec(dy, lddy, h, esz),
-                                     ln_vec(dx, lddx, h, esz), ln_vec_w(weight, wsz)}));
+        ln_shape(dtype, h, ln_vec(x, ldx, h, esz) && ln_vec(dy, lddy, h, esz) &&
+                               ln_vec(dx, lddx, h, esz) && aligned(weight, 16));
     const LnBwdArgs a{dy, lddy, x, ldx, weight, mean, rstd, n, h, dx, lddx, part_w, part_b};
     const double bytes = double(n) * double(h) * 3.0 * esz + 8.0 * double(n);
     LnRingShape rs;
-    if (ln_ring_shape(dtype, h, s.vn == 16 / esz, 2, n, dev->num_sms, &rs) &&
+    if (ln_ring_shape(dtype, h, s.vn > 1, 2, n, dev->num_sms, &rs) &&
         dev->num_sms <= kLnSms) {
       rs.ring.err = dev->err;
       rs.ring.timeout_ns = kDefaultTimeoutNs;
@@ -1041,14 +969,13 @@ extern "C" int flce_layer_norm_backward(const void* dy, int64_t lddy, const void
   if (params) {
     const dim3 grid(unsigned(cdiv(h, kLnReduceCols)), 2);
     LaunchScope scope(KF_LN_REDUCE, 0.0, 8.0 * double(parts) * double(h), cs);
-    if (w_dtype == FLCE_BF16)
-      ln_reduce_kernel<__nv_bfloat16><<<grid, 32 * kLnReduceWarps, 0, cs>>>(
-          part_w, part_b, parts, h, static_cast<__nv_bfloat16*>(dweight),
-          static_cast<__nv_bfloat16*>(dbias));
-    else
-      ln_reduce_kernel<float><<<grid, 32 * kLnReduceWarps, 0, cs>>>(
-          part_w, part_b, parts, h, static_cast<float*>(dweight), static_cast<float*>(dbias));
-    if (cudaGetLastError() != cudaSuccess) return FLCE_ERR_CUDA;
+    const dim3 block(32 * kLnReduceWarps);
+    return w_dtype == FLCE_BF16
+               ? launch_dependent(ln_reduce_kernel<__nv_bfloat16>, grid, block, 0, cs, part_w, part_b,
+                                  parts, h, static_cast<__nv_bfloat16*>(dweight),
+                                  static_cast<__nv_bfloat16*>(dbias))
+               : launch_dependent(ln_reduce_kernel<float>, grid, block, 0, cs, part_w, part_b, parts, h,
+                                  static_cast<float*>(dweight), static_cast<float*>(dbias));
   }
   return FLCE_OK;
 }
