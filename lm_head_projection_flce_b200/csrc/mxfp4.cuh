@@ -55,30 +55,6 @@ __host__ __device__ __forceinline__ int64_t mx_ctiles(int64_t cols) {
 }
 __host__ __device__ __forceinline__ int64_t mx_ktiles(int64_t cols) { return 2 * mx_ctiles(cols); }
 
-// Byte offset of the 4 bytes of codes of row r, columns [8 vec, 8 vec + 8).
-__device__ __forceinline__ int64_t mx_code_word(int64_t r, int64_t vec, int64_t ctiles) {
-  const int64_t tile = (r / kMxTileRows) * ctiles + (vec >> 5);
-  const int row = int(r % kMxTileRows), v = int(vec & 31);
-  return tile * kMxCodeBytes + row * 128 + (((v >> 2) ^ (row & 7)) << 4) + (v & 3) * 4;
-}
-
-// Byte offset of the 4-byte word that holds row r's scales of column tile kt.
-__device__ __forceinline__ int64_t mx_scale_word(int64_t r, int64_t kt, int64_t ktiles) {
-  return ((r / kMxTileRows) * ktiles + kt) * kMxTileBytes + (r % 32) * 16 +
-         ((r % kMxTileRows) / 32) * 4;
-}
-
-// Four E2M1 pairs of 8 scaled values, the first value in the lowest bits.
-__device__ __forceinline__ uint32_t mx_pack8(const float (&x)[8]) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(x[2 * i], x[2 * i + 1]),
-                                                        __NV_E2M1, cudaRoundNearest))
-         << (8 * i);
-  return w;
-}
-
 struct MxQuantArgs {
   const void* x;
   int64_t rows, cols, ld;
@@ -87,60 +63,121 @@ struct MxQuantArgs {
   int64_t segs;  // pieces a row is cut into, a warp each (whole tiles of 256 columns)
 };
 
-// A warp takes a piece of a row: 8 blocks (32 vectors of 8 elements) per step.
+// 8 elements as they were loaded, and what the conversion needs of them: the
+// largest magnitude as bits (NaN and Inf order above every number), and the
+// scaled values.
+template <typename T>
+struct MxVec;
+template <>
+struct MxVec<__nv_bfloat16> {
+  uint32_t u[4];
+  __device__ __forceinline__ void zero() { u[0] = u[1] = u[2] = u[3] = 0; }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    u[0] = w.x;
+    u[1] = w.y;
+    u[2] = w.z;
+    u[3] = w.w;
+  }
+  __device__ __forceinline__ void set(int j, const __nv_bfloat16* p) {
+    u[j >> 1] |= uint32_t(*reinterpret_cast<const uint16_t*>(p)) << (16 * (j & 1));
+  }
+  // Over the four lanes of the block: two 16-bit magnitudes at a time.
+  __device__ __forceinline__ int exponent() const {
+    uint32_t m = u[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __vmaxu2(m, u[i] & 0x7fff7fffu);
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return int(max(m >> 16, m & 0xffffu) >> 7);
+  }
+  __device__ __forceinline__ float2 pair(int i) const {
+    return make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+  }
+};
+template <>
+struct MxVec<float> {
+  float x[8];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+  }
+  __device__ __forceinline__ void load(const float* p) { LnIo<float, 8>::load(p, x); }
+  __device__ __forceinline__ void set(int j, const float* p) { x[j] = *p; }
+  __device__ __forceinline__ int exponent() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return int(m >> 23);
+  }
+  __device__ __forceinline__ float2 pair(int i) const { return make_float2(x[2 * i], x[2 * i + 1]); }
+};
+
+// A warp takes a piece of a row, a tile's 256 columns (32 vectors of 8) per step:
+// lane l holds columns 8 l.. of the tile, so its places in the tiles of codes
+// and scales only move on by whole tiles.
 // kVec: rows start on 16 bytes and hold whole vectors of 8.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const MxQuantArgs a) {
   grid_launch_dependents();  // the product's set-up; it waits for this grid's end itself
   const int lane = threadIdx.x & 31;
   const int64_t warps = int64_t(gridDim.x) * (kMxThreads / 32);
-  const int64_t blocks = mx_blocks(a.cols), ctiles = mx_ctiles(a.cols), ktiles = 2 * ctiles;
-  const int64_t steps = ctiles;  // of 8 blocks each
-  const int64_t per = (steps + a.segs - 1) / a.segs;
-  for (int64_t u = int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5);
-       u < a.rows * a.segs; u += warps) {
-    const int64_t r = u / a.segs, s0 = (u - r * a.segs) * per, s1 = min(steps, s0 + per);
-    const T* row = static_cast<const T*>(a.x) + r * a.ld;
+  const int64_t ctiles = mx_ctiles(a.cols);
+  const int64_t per = (ctiles + a.segs - 1) / a.segs;
+  for (int64_t unit = int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5);
+       unit < a.rows * a.segs; unit += warps) {
+    const int64_t r = a.segs == 1 ? unit : unit / a.segs;
+    const int64_t s0 = (unit - r * a.segs) * per, s1 = min(ctiles, s0 + per);
+    const int tr = int(r % kMxTileRows);
+    const T* src = static_cast<const T*>(a.x) + r * a.ld + s0 * kMxTileCols + lane * 8;
+    const int64_t tile = (r / kMxTileRows) * ctiles + s0;
+    uint8_t* code = a.codes + tile * kMxCodeBytes + tr * 128 + (((lane >> 2) ^ (tr & 7)) << 4) +
+                    (lane & 3) * 4;
+    uint8_t* scale = a.scales + tile * (2 * kMxTileBytes) + (lane >> 4) * kMxTileBytes +
+                     (tr % 32) * 16 + (tr / 32) * 4;
+    int64_t left = a.cols - s0 * kMxTileCols - lane * 8;  // columns from this lane's first on
     for (int64_t s = s0; s < s1; s += kMxUnroll) {
-      float v[kMxUnroll][8];
+      MxVec<T> v[kMxUnroll];
 #pragma unroll
       for (int i = 0; i < kMxUnroll; ++i) {
-        const int64_t c = ((s + i) * 32 + lane) * 8;
-        if (kVec && s + i < s1 && c < a.cols) {
-          LnIo<T, 8>::load(row + c, v[i]);
-        } else {
+        v[i].zero();
+        if (s + i < s1 && left > i * kMxTileCols) {
+          if constexpr (kVec) {
+            v[i].load(src + i * kMxTileCols);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float one[1] = {0.0f};
-            if (!kVec && s + i < s1 && c + j < a.cols) LnIo<T, 1>::load(row + c + j, one);
-            v[i][j] = one[0];
+            for (int j = 0; j < 8; ++j)
+              if (left > i * kMxTileCols + j) v[i].set(j, src + i * kMxTileCols + j);
           }
         }
       }
 #pragma unroll
       for (int i = 0; i < kMxUnroll; ++i) {
         if (s + i >= s1) break;  // the same for the whole warp
-        // The largest magnitude as bits: NaN and Inf order above every number.
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7fffffffu);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int ex = static_cast<int>(m >> 23);
+        const int ex = v[i].exponent();
         const int sc = ex == 255 ? 255 : max(ex - 2, 0);
         const float inv = __uint_as_float(static_cast<uint32_t>(ex == 255 ? 127 : 254 - sc) << 23);
+        uint32_t w = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= inv;
-        const uint32_t w = mx_pack8(v[i]);
-        const int64_t vec = (s + i) * 32 + lane, b = vec >> 2;
-        *reinterpret_cast<uint32_t*>(a.codes + mx_code_word(r, vec, ctiles)) = w;
-        // Four blocks' scales as one word, written by the first of 16 lanes.
-        uint32_t word = (b < blocks ? static_cast<uint32_t>(sc) : 127u) << (8 * ((lane >> 2) & 3));
+        for (int j = 0; j < 4; ++j)
+          w |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(
+                   __fmul2_rn(v[i].pair(j), make_float2(inv, inv)), __NV_E2M1, cudaRoundNearest))
+               << (8 * j);
+        *reinterpret_cast<uint32_t*>(code + i * kMxCodeBytes) = w;
+        // Four blocks' scales as one word, written by the first of 16 lanes.  A
+        // block starts at the first of its four lanes.
+        const bool in = left + (lane & 3) * 8 > i * kMxTileCols;
+        uint32_t word = (in ? static_cast<uint32_t>(sc) : 127u) << (8 * ((lane >> 2) & 3));
         word |= __shfl_xor_sync(0xffffffffu, word, 4);
         word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        if ((lane & 15) == 0)
-          *reinterpret_cast<uint32_t*>(a.scales + mx_scale_word(r, b >> 2, ktiles)) = word;
+        if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scale + i * (2 * kMxTileBytes)) = word;
       }
+      src += kMxUnroll * kMxTileCols;
+      code += kMxUnroll * kMxCodeBytes;
+      scale += kMxUnroll * 2 * kMxTileBytes;
+      left -= kMxUnroll * kMxTileCols;
     }
   }
 }
@@ -163,27 +200,33 @@ template <typename T, bool kVec>
 __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const MxDequantArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = int64_t(gridDim.x) * (kMxThreads / 32);
-  const int64_t ctiles = mx_ctiles(a.cols), ktiles = 2 * ctiles, steps = ctiles;
-  const int64_t per = (steps + a.segs - 1) / a.segs;
-  for (int64_t u = int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5);
-       u < a.rows * a.segs; u += warps) {
-    const int64_t r = u / a.segs, s0 = (u - r * a.segs) * per, s1 = min(steps, s0 + per);
-    T* row = static_cast<T*>(a.out) + r * a.ld;
+  const int64_t ctiles = mx_ctiles(a.cols);
+  const int64_t per = (ctiles + a.segs - 1) / a.segs;
+  for (int64_t unit = int64_t(blockIdx.x) * (kMxThreads / 32) + (threadIdx.x >> 5);
+       unit < a.rows * a.segs; unit += warps) {
+    const int64_t r = a.segs == 1 ? unit : unit / a.segs;
+    const int64_t s0 = (unit - r * a.segs) * per, s1 = min(ctiles, s0 + per);
+    const int tr = int(r % kMxTileRows);
+    T* dst = static_cast<T*>(a.out) + r * a.ld + s0 * kMxTileCols + lane * 8;
+    const int64_t tile = (r / kMxTileRows) * ctiles + s0;
+    const uint8_t* code = a.codes + tile * kMxCodeBytes + tr * 128 +
+                          (((lane >> 2) ^ (tr & 7)) << 4) + (lane & 3) * 4;
+    const uint8_t* scale = a.scales + tile * (2 * kMxTileBytes) + (lane >> 4) * kMxTileBytes +
+                           (tr % 32) * 16 + (tr / 32) * 4 + ((lane >> 2) & 3);
+    int64_t left = a.cols - s0 * kMxTileCols - lane * 8;
     for (int64_t s = s0; s < s1; s += kMxUnroll) {
       uint32_t w[kMxUnroll], sc[kMxUnroll];
 #pragma unroll
       for (int i = 0; i < kMxUnroll; ++i) {
-        const int64_t vec = (s + i) * 32 + lane;
         w[i] = sc[i] = 0;
-        if (s + i < s1 && vec * 8 < a.cols) {
-          w[i] = *reinterpret_cast<const uint32_t*>(a.codes + mx_code_word(r, vec, ctiles));
-          sc[i] = a.scales[mx_scale_word(r, vec >> 4, ktiles) + ((vec >> 2) & 3)];
+        if (s + i < s1 && left > i * kMxTileCols) {
+          w[i] = *reinterpret_cast<const uint32_t*>(code + i * kMxCodeBytes);
+          sc[i] = scale[i * (2 * kMxTileBytes)];
         }
       }
 #pragma unroll
       for (int i = 0; i < kMxUnroll; ++i) {
-        const int64_t c = ((s + i) * 32 + lane) * 8;
-        if (s + i >= s1 || c >= a.cols) continue;
+        if (s + i >= s1 || left <= i * kMxTileCols) continue;
         const float k = mx_scale(sc[i]);
         float v[8];
 #pragma unroll
@@ -194,16 +237,20 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const MxDequa
           v[2 * j] = f.x * k;
           v[2 * j + 1] = f.y * k;
         }
-        if (kVec) {
-          LnIo<T, 8>::store(row + c, v);
+        if constexpr (kVec) {
+          LnIo<T, 8>::store(dst + i * kMxTileCols, v);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float one[1] = {v[j]};
-            if (c + j < a.cols) LnIo<T, 1>::store(row + c + j, one);
+            if (left > i * kMxTileCols + j) LnIo<T, 1>::store(dst + i * kMxTileCols + j, one);
           }
         }
       }
+      dst += kMxUnroll * kMxTileCols;
+      code += kMxUnroll * kMxCodeBytes;
+      scale += kMxUnroll * 2 * kMxTileBytes;
+      left -= kMxUnroll * kMxTileCols;
     }
   }
 }
