@@ -36,6 +36,8 @@ constexpr int kBeamThreads = 256;
 constexpr int kBeamMaxBeams = 64;
 constexpr int kBeamMaxSelect = 64;
 constexpr int kBeamUnroll = 4;            // vectors in flight per thread
+constexpr int kBeamResident = 4;          // blocks per SM the registers are limited for
+constexpr int kBeamUnits = 4;             // blocks per SM aimed at when rows are few
 constexpr int kBeamList = 1024;           // elements above the bound that are sorted in one go
 constexpr int64_t kBeamMinSegment = 4096; // elements
 constexpr int kBeamMaxItems = 4096;       // candidates merged per batch item: K x segments x M
@@ -53,19 +55,58 @@ __device__ __forceinline__ uint64_t beam_key(float x, uint32_t index) {
   return (static_cast<uint64_t>(beam_order(x)) << 32) | (0xffffffffu - index);
 }
 
-// VN elements at row + c, c + j < end only.
-template <typename T, int VN>
-__device__ __forceinline__ void beam_load(const T* row, int64_t c, int64_t end, bool vec,
-                                          float (&x)[VN]) {
-  if (vec && c + VN <= end) {
-    LnIo<T, VN>::load(row + c, x);
+// 16 bytes of elements [c, c + N) of a row, -inf behind `end`.  In a row that does
+// not start on 16 bytes the vector is cut out of the two aligned ones around it
+// (the second is the neighbouring thread's first: an L1 hit); the row's first and
+// last vectors, where these would reach out of the row, are read by elements.
+template <typename T>
+__device__ __forceinline__ uint4 beam_load(const T* row, int64_t c, int64_t end) {
+  constexpr int N = 16 / int(sizeof(T));
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+  const uint32_t off = static_cast<uint32_t>(at) & 15u;  // the same for the whole row
+  if (off == 0 && c + N <= end) return *reinterpret_cast<const uint4*>(at);
+  if (off != 0 && c >= N && c + 2 * N <= end) {
+    const uint4 lo = *reinterpret_cast<const uint4*>(at - off);
+    const uint4 hi = *reinterpret_cast<const uint4*>(at - off + 16);
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (off & 8u) {
+#pragma unroll
+      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4u) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t sh = (off & 3u) * 8u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], sh);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = c + i < end ? reinterpret_cast<const uint32_t*>(row)[c + i] : 0xff800000u;
+    } else {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+      w[i] = (c + 2 * i < end ? p[c + 2 * i] : 0xff80u) |
+             uint32_t(c + 2 * i + 1 < end ? p[c + 2 * i + 1] : 0xff80u) << 16;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The elements of a vector, as pairs.
+template <typename T>
+__device__ __forceinline__ void beam_unpack(const uint4& v, float2 (&x)[8 / int(sizeof(T))]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      x[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
   } else {
 #pragma unroll
-    for (int j = 0; j < VN; ++j) {
-      float one[1] = {-INFINITY};
-      if (c + j < end) LnIo<T, 1>::load(row + c + j, one);
-      x[j] = one[0];
-    }
+    for (int i = 0; i < 4; ++i)
+      x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
 }
 
@@ -138,8 +179,9 @@ __device__ __forceinline__ bool beam_is_live(float score) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kBeamThreads) beam_partials_kernel(const BeamPartArgs a) {
+__global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_kernel(const BeamPartArgs a) {
   constexpr int VN = 16 / int(sizeof(T));
+  constexpr uint32_t kNegInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
   __shared__ BeamBound bs;
   __shared__ uint64_t list[kBeamList];
   __shared__ int owners[kBeamMaxSelect];
@@ -152,49 +194,58 @@ __global__ void __launch_bounds__(kBeamThreads) beam_partials_kernel(const BeamP
   if (!beam_is_live(a.scores[row]) || (a.finished && a.finished[row])) return;
   grid_launch_dependents();
   const T* z = static_cast<const T*>(a.logits) + row * a.ld;
-  const bool vec = (reinterpret_cast<uintptr_t>(z) & 15) == 0;
   const int64_t begin = int64_t(part) * a.segment, end = min(a.vocab, begin + a.segment);
-  const int64_t count = max(int64_t(0), (end - begin + VN - 1) / VN);  // vectors
+  const int count = int(max(int64_t(0), (end - begin + VN - 1) / VN));  // vectors
 
-  float m = -INFINITY, s = 0.0f, best = -INFINITY;
+  float m = -INFINITY, best = -INFINITY;
+  float2 s2 = make_float2(0.0f, 0.0f);
   uint32_t best_at = 0;  // first element of the vector that holds `best`
-  for (int64_t j0 = tid; j0 < count; j0 += int64_t(kBeamUnroll) * kBeamThreads) {
-    float x[kBeamUnroll][VN];
+  // The next batch is loaded before the current one is used: a block alone, or
+  // with few neighbours, would otherwise leave HBM idle between its loads.
+  uint4 raw[kBeamUnroll];
+  auto fetch = [&](int j0) {
 #pragma unroll
     for (int u = 0; u < kBeamUnroll; ++u) {
-      const int64_t c = begin + (j0 + int64_t(u) * kBeamThreads) * VN;
-      beam_load<T, VN>(z, min(c, end), end, vec, x[u]);
+      const int j = j0 + u * kBeamThreads;
+      // vectors end at the row's end, not the segment's: a segment is whole vectors
+      if (j < count) raw[u] = beam_load<T>(z, begin + int64_t(j) * VN, a.vocab);
+      else raw[u] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
     }
+  };
+  fetch(tid);
+  for (int j0 = tid; j0 < count; j0 += kBeamUnroll * kBeamThreads) {
+    float2 x[kBeamUnroll][VN / 2];
+#pragma unroll
+    for (int u = 0; u < kBeamUnroll; ++u) beam_unpack<T>(raw[u], x[u]);
+    fetch(j0 + kBeamUnroll * kBeamThreads);
     float bm = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kBeamUnroll; ++u) {
-      float vm = x[u][0];
+      float vm = fmaxf(x[u][0].x, x[u][0].y);
 #pragma unroll
-      for (int j = 1; j < VN; ++j) vm = fmaxf(vm, x[u][j]);
+      for (int j = 1; j < VN / 2; ++j) vm = fmaxf(vm, fmaxf(x[u][j].x, x[u][j].y));
       if (vm > best) {
         best = vm;
-        best_at = uint32_t(begin + (j0 + int64_t(u) * kBeamThreads) * VN);
+        best_at = uint32_t(begin) + uint32_t(j0 + u * kBeamThreads) * VN;
       }
       bm = fmaxf(bm, vm);
     }
     if (bm > m) {
-      s *= fast_exp2((m - bm) * kLog2e);
+      s2 = __fmul2_rn(s2, ln_both(fast_exp2((m - bm) * kLog2e)));
       m = bm;
     }
-    if (m == -INFINITY) {
-      // nothing but -inf so far; a NaN must still reach the sum
-#pragma unroll
-      for (int u = 0; u < kBeamUnroll; ++u)
-#pragma unroll
-        for (int j = 0; j < VN; ++j)
-          if (x[u][j] != x[u][j]) s = x[u][j];
-      continue;
-    }
+    // Before the first element above -inf the terms are taken against 0: -inf
+    // adds nothing, and a NaN still reaches the sum.
+    const float2 base = ln_both(m == -INFINITY ? 0.0f : -m);
 #pragma unroll
     for (int u = 0; u < kBeamUnroll; ++u)
 #pragma unroll
-      for (int j = 0; j < VN; ++j) s += fast_exp2((x[u][j] - m) * kLog2e);
+      for (int j = 0; j < VN / 2; ++j) {
+        const float2 t = __fmul2_rn(__fadd2_rn(x[u][j], base), ln_both(kLog2e));
+        s2 = __fadd2_rn(s2, make_float2(fast_exp2(t.x), fast_exp2(t.y)));
+      }
   }
+  const float s = s2.x + s2.y;
 
   // The segment's maximum and sum, added in a fixed order.
   float bm = m;
@@ -225,18 +276,22 @@ __global__ void __launch_bounds__(kBeamThreads) beam_partials_kernel(const BeamP
   __syncthreads();
 
   // Elements of the owners' vectors whose (value, vector) is not below the bound.
-  const int64_t per = (count + kBeamThreads - 1) / kBeamThreads;  // vectors per thread
-  const int64_t work = int64_t(n_owners) * per;
+  const int per = (count + kBeamThreads - 1) / kBeamThreads;  // vectors per thread
+  const int work = n_owners * per;
   auto scan = [&](auto&& take) {
-    for (int64_t w = tid; w < work; w += kBeamThreads) {
-      const int64_t j = owners[w / per] + (w % per) * kBeamThreads;
+    for (int w = tid; w < work; w += kBeamThreads) {
+      const int q = w / per, j = owners[q] + (w - q * per) * kBeamThreads;
       if (j >= count) continue;
-      float x[VN];
-      beam_load<T, VN>(z, begin + j * VN, end, vec, x);
+      float2 x[VN / 2];
+      beam_unpack<T>(beam_load<T>(z, begin + int64_t(j) * VN, a.vocab), x);
+      const uint32_t at = uint32_t(begin) + uint32_t(j) * VN;
+      auto one = [&](float v, uint32_t i) {
+        if (v > -INFINITY && beam_key(v, at) >= bound) take(beam_key(v, at + i));
+      };
 #pragma unroll
-      for (int i = 0; i < VN; ++i) {
-        const uint32_t at = uint32_t(begin + j * VN);
-        if (x[i] > -INFINITY && beam_key(x[i], at) >= bound) take(beam_key(x[i], at + i));
+      for (int i = 0; i < VN / 2; ++i) {
+        one(x[i].x, 2 * i);
+        one(x[i].y, 2 * i + 1);
       }
     }
   };
@@ -316,8 +371,10 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
   __shared__ uint32_t chosen[kBeamMaxSelect];
   constexpr int kAhead = 4;  // items per thread loaded before the sums are known
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per_beam = a.splits * a.select;
-  const int items = a.beams * per_beam;
+  // Item i is candidate i / lists of list i % lists: the lists are sorted, and dealt
+  // this way their best entries lie with different threads, which keeps the
+  // bound tight (list by list, 64 candidates of 64 lists took 129 us to merge).
+  const int lists = a.beams * a.splits, items = lists * a.select;
   const uint32_t vocab = uint32_t(a.vocab);
   uint64_t* tot = dyn;                                       // [items]
   uint32_t* idx = reinterpret_cast<uint32_t*>(tot + items);  // [items]
@@ -326,6 +383,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
   const float* scores = a.scores + b * a.beams;
   const uint8_t* finished = a.finished ? a.finished + b * a.beams : nullptr;
   const int64_t at0 = b * items;
+  auto place = [&](int i) { return (i % lists) * a.select + i / lists; };
   grid_dependency_wait();
   float az[kAhead];
   int av[kAhead];
@@ -333,8 +391,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
   for (int u = 0; u < kAhead; ++u) {
     const int i = tid + u * kBeamThreads;
     // dead and finished beams' entries were never written: loaded, not used
-    az[u] = i < items ? a.cand_z[at0 + i] : 0.0f;
-    av[u] = i < items ? a.cand_v[at0 + i] : -1;
+    az[u] = i < items ? a.cand_z[at0 + place(i)] : 0.0f;
+    av[u] = i < items ? a.cand_v[at0 + place(i)] : -1;
   }
   if (tid == 0) n_list = 0;
   const double ninf = -static_cast<double>(INFINITY);
@@ -364,13 +422,13 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
 
   uint64_t top = 0;
   auto item = [&](int i, float z, int v) {
-    const int k = i / per_beam;
+    const int k = (i % lists) / a.splits;
     double t = ninf;
     const float s = scores[k];
     if (beam_is_live(s)) {
       if (finished && finished[k]) {
         v = int(a.eos);
-        if (i == k * per_beam) t = double(s);
+        if (i == k * a.splits) t = double(s);
       } else if (v >= 0) {
         t = double(s) + double(z) - lse[k];
       }
@@ -384,7 +442,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
   for (int u = 0; u < kAhead; ++u)
     if (tid + u * kBeamThreads < items) item(tid + u * kBeamThreads, az[u], av[u]);
   for (int i = tid + kAhead * kBeamThreads; i < items; i += kBeamThreads)
-    item(i, a.cand_z[at0 + i], a.cand_v[at0 + i]);
+    item(i, a.cand_z[at0 + place(i)], a.cand_v[at0 + place(i)]);
   const uint64_t bound = beam_bound(top, a.select, bs);
   for (int i = tid; i < items; i += kBeamThreads)
     if (tot[i] != 0 && tot[i] >= bound) list[atomicAdd(&n_list, 1)] = i;
@@ -434,7 +492,7 @@ struct BeamPlan {
 static BeamPlan plan_beam(int64_t batch, int64_t beams, int64_t vocab, int64_t select) {
   BeamPlan p{};
   const int64_t rows = std::max<int64_t>(1, batch * beams);
-  int64_t s = cdiv(4 * kLnSms, rows);
+  int64_t s = cdiv(kBeamUnits * kLnSms, rows);
   s = std::min({s, std::max<int64_t>(1, vocab / kBeamMinSegment),
                 std::max<int64_t>(1, kBeamMaxItems / (beams * select))});
   p.segment = cdiv(cdiv(vocab, s), 8) * 8;
