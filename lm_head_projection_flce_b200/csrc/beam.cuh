@@ -95,6 +95,19 @@ __device__ __forceinline__ uint4 beam_load(const T* row, int64_t c, int64_t end)
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// The largest element of a vector (NaN does not count).
+template <typename T>
+__device__ __forceinline__ float beam_max(const uint4& v) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                 fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else {
+    auto pair = [](const uint32_t& u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+    const float2 f = __bfloat1622float2(
+        __hmax2(__hmax2(pair(v.x), pair(v.y)), __hmax2(pair(v.z), pair(v.w))));
+    return fmaxf(f.x, f.y);
+  }
+}
 // The elements of a vector, as pairs.
 template <typename T>
 __device__ __forceinline__ void beam_unpack(const uint4& v, float2 (&x)[8 / int(sizeof(T))]) {
@@ -203,7 +216,16 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
   // The next batch is loaded before the current one is used: a block alone, or
   // with few neighbours, would otherwise leave HBM idle between its loads.
   uint4 raw[kBeamUnroll];
+  const uint4* body = reinterpret_cast<const uint4*>(z + begin);
+  // whole vectors on 16 bytes: none of them needs a look at its ends
+  const int whole =
+      (reinterpret_cast<uintptr_t>(z) & 15) == 0 ? int(min(int64_t(count), (a.vocab - begin) / VN)) : 0;
   auto fetch = [&](int j0) {
+    if (j0 + (kBeamUnroll - 1) * kBeamThreads < whole) {
+#pragma unroll
+      for (int u = 0; u < kBeamUnroll; ++u) raw[u] = body[j0 + u * kBeamThreads];
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < kBeamUnroll; ++u) {
       const int j = j0 + u * kBeamThreads;
@@ -214,16 +236,14 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
   };
   fetch(tid);
   for (int j0 = tid; j0 < count; j0 += kBeamUnroll * kBeamThreads) {
-    float2 x[kBeamUnroll][VN / 2];
+    uint4 cur[kBeamUnroll];
 #pragma unroll
-    for (int u = 0; u < kBeamUnroll; ++u) beam_unpack<T>(raw[u], x[u]);
+    for (int u = 0; u < kBeamUnroll; ++u) cur[u] = raw[u];
     fetch(j0 + kBeamUnroll * kBeamThreads);
     float bm = -INFINITY;
 #pragma unroll
     for (int u = 0; u < kBeamUnroll; ++u) {
-      float vm = fmaxf(x[u][0].x, x[u][0].y);
-#pragma unroll
-      for (int j = 1; j < VN / 2; ++j) vm = fmaxf(vm, fmaxf(x[u][j].x, x[u][j].y));
+      const float vm = beam_max<T>(cur[u]);
       if (vm > best) {
         best = vm;
         best_at = uint32_t(begin) + uint32_t(j0 + u * kBeamThreads) * VN;
@@ -238,12 +258,15 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
     // adds nothing, and a NaN still reaches the sum.
     const float2 base = ln_both(m == -INFINITY ? 0.0f : -m);
 #pragma unroll
-    for (int u = 0; u < kBeamUnroll; ++u)
+    for (int u = 0; u < kBeamUnroll; ++u) {
+      float2 x[VN / 2];
+      beam_unpack<T>(cur[u], x);
 #pragma unroll
       for (int j = 0; j < VN / 2; ++j) {
-        const float2 t = __fmul2_rn(__fadd2_rn(x[u][j], base), ln_both(kLog2e));
+        const float2 t = __fmul2_rn(__fadd2_rn(x[j], base), ln_both(kLog2e));
         s2 = __fadd2_rn(s2, make_float2(fast_exp2(t.x), fast_exp2(t.y)));
       }
+    }
   }
   const float s = s2.x + s2.y;
 
