@@ -37,7 +37,7 @@ constexpr int kBeamMaxBeams = 64;
 constexpr int kBeamMaxSelect = 64;
 constexpr int kBeamUnroll = 4;            // vectors in flight per thread
 constexpr int kBeamResident = 4;          // blocks per SM the registers are limited for
-constexpr int kBeamUnits = 4;             // blocks per SM aimed at when rows are few
+constexpr int kBeamUnits = 3;             // blocks per SM aimed at when rows are few
 constexpr int kBeamList = 1024;           // elements above the bound that are sorted in one go
 constexpr int64_t kBeamMinSegment = 4096; // elements
 constexpr int kBeamMaxItems = 4096;       // candidates merged per batch item: K x segments x M
