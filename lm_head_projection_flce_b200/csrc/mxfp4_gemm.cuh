@@ -179,7 +179,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  grid_dependency_wait();
   const uint32_t tmem = tmem_slot;
 
   // Warps 0 and 1 run their loops with all lanes, so that addresses and
@@ -214,15 +213,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ... and of the second row tile, from its first row
       const uint8_t* nc1 = g.n_codes + (bt + 1) * num_kb * kMxCodeBytes;
       const uint8_t* ns1 = ns + num_kb * (2 * kMxTileBytes);
+      int ahead = 0;
+      if (t == blockIdx.x) {
+        // The head does not depend on the kernel before this one, which puts the
+        // tokens into 4 bits: its first stages are on their way before that ends.
+        ahead = min(stages, num_kb);
+        if (leader) {
+          for (int s = 0; s < ahead; ++s) {
+            const uint32_t to = smem_base + uint32_t(s) * stage_bytes;
+            mbar_arrive_expect_tx(full_bar(s), expect);
+            bulk_load_hint(to, mc + int64_t(s) * kMxCodeBytes, kMxCodeBytes, full_bar(s), pol_m);
+            bulk_load_hint(to + off_sfa, ms + int64_t(s) * (2 * kMxTileBytes), 2 * kMxTileBytes,
+                           full_bar(s), pol_m);
+          }
+        }
+        __syncwarp();
+        grid_dependency_wait();
+      }
       for (int kb = 0; kb < num_kb; ++kb) {
         if (!wait_warp(full + 8u * kMxgMaxStages, ph ^ 1u, ctl, g.err, g.timeout_ns)) {
           ok = false;
           break;
         }
         if (leader) {
-          mbar_arrive_expect_tx(full, expect);
-          bulk_load_hint(base, mc, kMxCodeBytes, full, pol_m);
-          bulk_load_hint(base + off_sfa, ms, 2 * kMxTileBytes, full, pol_m);
+          if (kb >= ahead) {
+            mbar_arrive_expect_tx(full, expect);
+            bulk_load_hint(base, mc, kMxCodeBytes, full, pol_m);
+            bulk_load_hint(base + off_sfa, ms, 2 * kMxTileBytes, full, pol_m);
+          }
           bulk_load_hint(base + off_b, nc, bytes0, full, pol_n);
           bulk_load_hint(base + off_sfb, ns, 2 * kMxTileBytes, full, pol_n);
           if (two) {
@@ -334,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     drain_wait(drain_bar, 0, ok ? g.timeout_ns : 100000000ull);
   } else {
     // -------------------------------------------------- epilogue: lanes are M rows
+    grid_dependency_wait();  // before anything is stored
     const int quarter = warp & 3;
     int acc = 0;
     uint32_t acc_ph = 0;
