@@ -12,6 +12,7 @@ Entry points mirror include/flce.h:
   layer_norm(...)                                  the final norm, autograd-aware
   mxfp4_quantize(...), mxfp4_logits(...)           the head in 4 bits and its product
   beam_select(...), beam_reorder(...)              beam search behind the head
+  CapturedStep, CapturedBeamStep                   a training / decoding step as one graph
 with the options of the NeMo-AutoModel loss pages
 ("nemo_automodel.components.loss.linear_ce", FusedLinearCrossEntropy:
 ignore_index=-100, logit_softcapping=0, reduction='sum', num_label_tokens;
@@ -1044,3 +1045,71 @@ def beam_reorder(states, parents, *, length: int | None = None, length_dim: int 
                                    max(k, 1), _stream_handle(dev, stream))
     _check("flce_beam_reorder", st)
     return dsts[0] if single else dsts
+
+
+class CapturedBeamStep:
+    """One decoding step behind the model, captured once into a CUDA graph: layer norm
+    (when ``norm_weight`` or ``norm_bias`` is given), the head's product in MXFP4,
+    beam selection and, with ``states``, their reordering in place.
+
+    The inputs are static tensors owned here -- ``hidden`` [B, K, H], ``scores``
+    [B, K] and ``finished`` [B, K] when given -- and a step copies new values into
+    them (``set_inputs``) and calls ``replay()``, one graph launch instead of a
+    handful of small ones.  The head, the norm's parameters and the states are the
+    caller's and must keep their storage.  ``replay()`` returns ``(scores, parents,
+    tokens)``, [B, num_select], static too and overwritten by each replay; ``logits``
+    holds the step's logits.  Results equal the separate calls bit for bit.  The
+    options are host values baked into the graph; with ``states``, num_select must be
+    K, and every position of a state is reordered.  Replays of one step, or of
+    two that share states, must be ordered on one stream.
+    """
+
+    def __init__(self, hidden, head: Mxfp4, scores, *, norm_weight=None, norm_bias=None,
+                 norm_eps: float = 1e-5, softcap: float = 0.0, unpadded_vocab: int | None = None,
+                 num_select: int | None = None, finished=None, eos_token: int | None = None,
+                 states=None, dtype: torch.dtype = torch.bfloat16):
+        _cuda_tensor(hidden, W_DTYPES, None, "hidden")
+        if hidden.dim() != 3:
+            raise ValueError("hidden must be [batch, beams, hidden]")
+        if states is not None and num_select not in (None, hidden.shape[1]):
+            raise ValueError("states follow as many beams as there are: num_select must be beams")
+        dev = hidden.device
+        self.hidden = hidden.detach().clone(memory_format=torch.contiguous_format)
+        self.scores = scores.clone()
+        self.finished = None if finished is None else finished.clone()
+        self.head, self.norm, self.states = head, (norm_weight, norm_bias, norm_eps), states
+        self.kw = dict(softcap=softcap, unpadded_vocab=unpadded_vocab, dtype=dtype)
+        self.select = dict(num_select=num_select, finished=self.finished, eos_token=eos_token)
+        stream = torch.cuda.Stream(dev)
+        stream.wait_stream(torch.cuda.current_stream(dev))
+        with torch.cuda.stream(stream):
+            self._step(reorder=False)  # eager: per-device set-up and argument checks, outside capture
+        torch.cuda.current_stream(dev).wait_stream(stream)
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph, stream=stream):
+            self.logits, self.out = self._step(reorder=True)
+
+    def _step(self, reorder: bool):
+        x, (weight, bias, eps) = self.hidden, self.norm
+        if weight is not None or bias is not None:
+            x = layer_norm_forward(x, weight, bias, eps=eps, stats=False)[0]
+        logits = mxfp4_logits(x, self.head, **self.kw)
+        out = beam_select(logits, self.scores, **self.select)
+        if reorder and self.states is not None:
+            beam_reorder(self.states, out[1])
+        return logits, out
+
+    def set_inputs(self, hidden=None, scores=None, finished=None) -> None:
+        """Copy a step's values into the captured input buffers (same shapes)."""
+        for buf, new in ((self.hidden, hidden), (self.scores, scores), (self.finished, finished)):
+            if new is not None:
+                if buf is None:
+                    raise ValueError("the step was captured without finished beams")
+                if new.shape != buf.shape:
+                    raise ValueError("inputs must have the captured shapes")
+                buf.copy_(new, non_blocking=True)
+
+    def replay(self):
+        """Run the step; returns (scores, parents, tokens), static buffers."""
+        self.graph.replay()
+        return self.out
