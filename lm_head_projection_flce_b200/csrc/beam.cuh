@@ -55,46 +55,6 @@ __device__ __forceinline__ uint64_t beam_key(float x, uint32_t index) {
   return (static_cast<uint64_t>(beam_order(x)) << 32) | (0xffffffffu - index);
 }
 
-// 16 bytes of elements [c, c + N) of a row, -inf behind `end`.  In a row that does
-// not start on 16 bytes the vector is cut out of the two aligned ones around it
-// (the second is the neighbouring thread's first: an L1 hit); the row's first and
-// last vectors, where these would reach out of the row, are read by elements.
-template <typename T>
-__device__ __forceinline__ uint4 beam_load(const T* row, int64_t c, int64_t end) {
-  constexpr int N = 16 / int(sizeof(T));
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
-  const uint32_t off = static_cast<uint32_t>(at) & 15u;  // the same for the whole row
-  if (off == 0 && c + N <= end) return *reinterpret_cast<const uint4*>(at);
-  if (off != 0 && c >= N && c + 2 * N <= end) {
-    const uint4 lo = *reinterpret_cast<const uint4*>(at - off);
-    const uint4 hi = *reinterpret_cast<const uint4*>(at - off + 16);
-    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    if (off & 8u) {
-#pragma unroll
-      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    }
-    if (off & 4u) {
-#pragma unroll
-      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    }
-    const uint32_t sh = (off & 3u) * 8u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], sh);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      w[i] = c + i < end ? reinterpret_cast<const uint32_t*>(row)[c + i] : 0xff800000u;
-    } else {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
-      w[i] = (c + 2 * i < end ? p[c + 2 * i] : 0xff80u) |
-             uint32_t(c + 2 * i + 1 < end ? p[c + 2 * i + 1] : 0xff80u) << 16;
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 // The largest element of a vector (NaN does not count).
 template <typename T>
 __device__ __forceinline__ float beam_max(const uint4& v) {
@@ -230,7 +190,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
     for (int u = 0; u < kBeamUnroll; ++u) {
       const int j = j0 + u * kBeamThreads;
       // vectors end at the row's end, not the segment's: a segment is whole vectors
-      if (j < count) raw[u] = beam_load<T>(z, begin + int64_t(j) * VN, a.vocab);
+      if (j < count) raw[u] = load16_any<T>(z, begin + int64_t(j) * VN, a.vocab, kNegInf);
       else raw[u] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
     }
   };
@@ -306,7 +266,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
       const int q = w / per, j = owners[q] + (w - q * per) * kBeamThreads;
       if (j >= count) continue;
       float2 x[VN / 2];
-      beam_unpack<T>(beam_load<T>(z, begin + int64_t(j) * VN, a.vocab), x);
+      beam_unpack<T>(load16_any<T>(z, begin + int64_t(j) * VN, a.vocab, kNegInf), x);
       const uint32_t at = uint32_t(begin) + uint32_t(j) * VN;
       auto one = [&](float v, uint32_t i) {
         if (v > -INFINITY && beam_key(v, at) >= bound) take(beam_key(v, at + i));

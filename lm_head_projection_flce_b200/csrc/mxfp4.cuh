@@ -79,8 +79,12 @@ struct MxVec<__nv_bfloat16> {
     u[2] = w.z;
     u[3] = w.w;
   }
-  __device__ __forceinline__ void set(int j, const __nv_bfloat16* p) {
-    u[j >> 1] |= uint32_t(*reinterpret_cast<const uint16_t*>(p)) << (16 * (j & 1));
+  __device__ __forceinline__ void load_any(const __nv_bfloat16* row, int64_t c, int64_t end) {
+    const uint4 w = load16_any(row, c, end, 0);
+    u[0] = w.x;
+    u[1] = w.y;
+    u[2] = w.z;
+    u[3] = w.w;
   }
   // Over the four lanes of the block: two 16-bit magnitudes at a time.
   __device__ __forceinline__ int exponent() const {
@@ -103,7 +107,16 @@ struct MxVec<float> {
     for (int j = 0; j < 8; ++j) x[j] = 0.0f;
   }
   __device__ __forceinline__ void load(const float* p) { LnIo<float, 8>::load(p, x); }
-  __device__ __forceinline__ void set(int j, const float* p) { x[j] = *p; }
+  __device__ __forceinline__ void load_any(const float* row, int64_t c, int64_t end) {
+#pragma unroll
+    for (int h = 0; h < 8; h += 4) {
+      const uint4 w = load16_any(row, c + h, end, 0);
+      x[h] = __uint_as_float(w.x);
+      x[h + 1] = __uint_as_float(w.y);
+      x[h + 2] = __uint_as_float(w.z);
+      x[h + 3] = __uint_as_float(w.w);
+    }
+  }
   __device__ __forceinline__ int exponent() const {
     uint32_t m = 0;
 #pragma unroll
@@ -131,7 +144,8 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const MxQuantAr
     const int64_t r = a.segs == 1 ? unit : unit / a.segs;
     const int64_t s0 = (unit - r * a.segs) * per, s1 = min(ctiles, s0 + per);
     const int tr = int(r % kMxTileRows);
-    const T* src = static_cast<const T*>(a.x) + r * a.ld + s0 * kMxTileCols + lane * 8;
+    const T* row = static_cast<const T*>(a.x) + r * a.ld;
+    const T* src = row + s0 * kMxTileCols + lane * 8;
     const int64_t tile = (r / kMxTileRows) * ctiles + s0;
     uint8_t* code = a.codes + tile * kMxCodeBytes + tr * 128 + (((lane >> 2) ^ (tr & 7)) << 4) +
                     (lane & 3) * 4;
@@ -147,9 +161,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const MxQuantAr
           if constexpr (kVec) {
             v[i].load(src + i * kMxTileCols);
           } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (left > i * kMxTileCols + j) v[i].set(j, src + i * kMxTileCols + j);
+            v[i].load_any(row, a.cols - left + i * kMxTileCols, a.cols);
           }
         }
       }
@@ -198,6 +210,9 @@ __device__ __forceinline__ float mx_scale(uint32_t sc) {
 
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const MxDequantArgs a) {
+  // Rows of any alignment: a tile's 256 values change hands through shared memory,
+  // so that a warp stores 32 neighbours at a time.
+  __shared__ __align__(16) T stage_s[kVec ? 1 : kMxThreads / 32][kVec ? 8 : kMxTileCols];
   const int lane = threadIdx.x & 31;
   const int64_t warps = int64_t(gridDim.x) * (kMxThreads / 32);
   const int64_t ctiles = mx_ctiles(a.cols);
@@ -226,7 +241,8 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const MxDequa
       }
 #pragma unroll
       for (int i = 0; i < kMxUnroll; ++i) {
-        if (s + i >= s1 || left <= i * kMxTileCols) continue;
+        if (s + i >= s1) break;  // the same for the whole warp
+        if (kVec && left <= i * kMxTileCols) continue;
         const float k = mx_scale(sc[i]);
         float v[8];
 #pragma unroll
@@ -240,11 +256,16 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const MxDequa
         if constexpr (kVec) {
           LnIo<T, 8>::store(dst + i * kMxTileCols, v);
         } else {
+          T* stage = stage_s[threadIdx.x >> 5];
+          LnIo<T, 8>::store(stage + lane * 8, v);
+          __syncwarp();
+          // first column of the tile, and how many there are from it on
+          T* to = dst - lane * 8 + i * kMxTileCols;
+          const int64_t n = left + lane * 8 - i * kMxTileCols;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float one[1] = {v[j]};
-            if (left > i * kMxTileCols + j) LnIo<T, 1>::store(dst + i * kMxTileCols + j, one);
-          }
+          for (int j = 0; j < 8; ++j)
+            if (j * 32 + lane < n) to[j * 32 + lane] = stage[j * 32 + lane];
+          __syncwarp();
         }
       }
       dst += kMxUnroll * kMxTileCols;

@@ -14,8 +14,6 @@
 // one token and stores 32 bytes at a time; with the head on the M side its lanes
 // hold consecutive logits and store 2 bytes each, which at 4096 tokens took
 // longer than the product (1205 against 890 us, both on single CTAs).
-// Rows of logits that do not start on 16 bytes take the first kernel whatever
-// the tokens, as its stores join across lanes.
 //
 // Warp 0 loads: per stage of 256 elements of K the head's tile of codes (16 KB),
 // the tokens' rows of theirs, and both operands' scale tiles, each a contiguous
@@ -52,7 +50,7 @@ struct MxGemmArgs {
   float softcap, inv_softcap;
   void* out;
   int64_t ldo;
-  int v8;             // rows of logits start on 32 bytes
+  int v4, v8;         // rows of logits start on 16, on 32 bytes
   unsigned* err;
   uint64_t timeout_ns;
 };
@@ -445,6 +443,24 @@ __device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d, uint64_t a, uint64_
       : "memory");
 }
 
+// Exchanges rows and columns of a 32 x 32 block that a warp holds a row per lane.
+__device__ __forceinline__ void warp_transpose(float (&x)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const bool upper = (lane & s) != 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i & s) continue;
+      const float got = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[i + s], s);
+      if (upper)
+        x[i] = got;
+      else
+        x[i + s] = got;
+    }
+  }
+}
+
 struct __align__(64) MxPairMaps {
   // Codes as rows of 128 bytes, 128 rows per tile; scales as rows of 128 bytes,
   // 8 rows per tile of codes.  No swizzle: the codes are stored swizzled.
@@ -637,9 +653,31 @@ __global__ void __launch_bounds__(kMxpThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(leader_tempty);
       const int64_t row = (2 * mt + rank) * kMxgM + quarter * 32 + lane;
-      if (row >= g.rows_m) continue;
       const int64_t c0 = nt * kMxpN + half * 128;
-      // 128 consecutive logits of a token; rows start on 16 bytes.
+      if (!g.v4) {
+        // Rows of logits at any alignment: lanes take turns with the tokens, so that a
+        // store covers 32 consecutive logits of one token.
+        const int rows = int(min(int64_t(32), g.rows_m - (row - lane)));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t c = c0 + 32 * q + lane;
+          if (c - lane >= g.rows_n) break;  // the same for the whole warp
+          if (capped) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[q][j] = g.softcap * tanhf(x[q][j] * g.inv_softcap);
+          }
+          warp_transpose(x[q]);
+          TO* out = static_cast<TO*>(g.out) + (row - lane) * g.ldo + c;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float one[1] = {x[q][j]};
+            if (j < rows && c < g.rows_n) LnIo<TO, 1>::store(out + int64_t(j) * g.ldo, one);
+          }
+        }
+        continue;
+      }
+      if (row >= g.rows_m) continue;
+      // 128 consecutive logits of a token
       TO* out = static_cast<TO*>(g.out) + row * g.ldo + c0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -788,7 +826,7 @@ extern "C" int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n, int64
   MxGemmArgs g{};
   const int esz = out_dtype == FLCE_F32 ? 4 : 2;
   const int64_t ld = n > 1 ? ldo : v;
-  const bool tokens_m = n > kMxgMaxN && aligned(logits, 16) && (ld * esz) % 16 == 0;
+  const bool tokens_m = n > kMxgMaxN;
   const uint8_t* wc = static_cast<const uint8_t*>(w_codes);
   const uint8_t* wsc = static_cast<const uint8_t*>(w_scales);
   g.rows_m = tokens_m ? n : v;
@@ -811,6 +849,7 @@ extern "C" int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n, int64
   g.inv_softcap = softcap > 0.0f ? 1.0f / softcap : 0.0f;
   g.out = logits;
   g.ldo = ld;
+  g.v4 = aligned(logits, 16) && (ld * esz) % 16 == 0;
   g.v8 = aligned(logits, 32) && (ld * esz) % 32 == 0;
   g.err = dev->err;
   g.timeout_ns = kDefaultTimeoutNs;

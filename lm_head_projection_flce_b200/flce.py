@@ -658,16 +658,21 @@ def _result_rows(t, h: int, name: str) -> tuple[int, int]:
 
 
 def _norm_params(weight, bias, h: int, dev, param_dtype=None) -> torch.dtype:
-    given = [p for p in (weight, bias) if p is not None]
-    for p in given:
-        _cuda_tensor(p, W_DTYPES, dev, "weight and bias")
-        if p.shape != (h,) or not p.is_contiguous():
+    """The parameters' common dtype, after checking them."""
+    dtype = param_dtype
+    for p in (weight, bias):
+        if p is None:
+            continue
+        if dtype is None:
+            dtype = p.dtype
+        elif p.dtype != dtype:
+            raise TypeError("weight, bias and param_dtype must be one dtype")
+        if p.dim() != 1 or p.shape[0] != h or not p.is_contiguous():
             raise ValueError("weight and bias must be contiguous [hidden] tensors")
-        if p.dtype != given[0].dtype:
-            raise TypeError("weight and bias must have one dtype")
-    dtype = given[0].dtype if given else (param_dtype or torch.float32)
-    if param_dtype is not None and param_dtype != dtype:
-        raise TypeError("param_dtype differs from the weight's dtype")
+        if p.device != dev:
+            raise ValueError("tensors must be on one CUDA device")
+    if dtype is None:
+        return torch.float32
     if dtype not in W_DTYPES:
         raise TypeError("weight and bias must be bf16 or fp32")
     return dtype
@@ -697,8 +702,12 @@ def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5,
     dev = x.device
     w_dtype = _norm_params(weight, bias, h, dev)
     with _on(dev, stream):
-        y = _result(y, x, x.shape, x.dtype, "y")
-        out, ldy = _result_rows(y, h, "y")
+        if y is None:
+            y = x.new_empty(x.shape)
+            out, ldy = _ptr(y), h
+        else:
+            _result(y, x, x.shape, x.dtype, "y")
+            out, ldy = _result_rows(y, h, "y")
         if mean is not None:
             _buffer(mean, n, torch.float32, dev, "mean")
         elif stats:
@@ -822,6 +831,14 @@ class Mxfp4:
     rows: int
     cols: int
 
+    def __post_init__(self):
+        lib = _LIB or load_library()
+        if self.codes.device.type != "cuda":
+            raise ValueError("tensors must be on one CUDA device")
+        for t, size, name in ((self.codes, lib.flce_mxfp4_codes_size, "codes"),
+                              (self.scales, lib.flce_mxfp4_scales_size, "scales")):
+            _buffer(t, size(self.rows, self.cols), torch.uint8, self.codes.device, name)
+
     @property
     def shape(self) -> tuple[int, int]:
         return self.rows, self.cols
@@ -846,15 +863,8 @@ class Mxfp4:
 
 
 def _mxfp4_operand(q: Mxfp4, name: str) -> None:
-    lib = _LIB or load_library()
     if not isinstance(q, Mxfp4):
         raise TypeError(f"{name} must be an Mxfp4 (from mxfp4_quantize)")
-    _buffer(q.codes, int(lib.flce_mxfp4_codes_size(q.rows, q.cols)), torch.uint8, q.device,
-            f"{name}.codes")
-    _buffer(q.scales, int(lib.flce_mxfp4_scales_size(q.rows, q.cols)), torch.uint8, q.device,
-            f"{name}.scales")
-    if q.device.type != "cuda":
-        raise ValueError("tensors must be on one CUDA device")
 
 
 def mxfp4_quantize(x, *, out: Mxfp4 | None = None, stream=None) -> Mxfp4:
@@ -921,8 +931,12 @@ def mxfp4_logits(hidden, head: Mxfp4, *, softcap: float = 0.0, unpadded_vocab: i
     n = rows.shape[0]
     shape = (*hidden.shape[:-1], v)
     with _on(dev, stream):
-        logits = _result(logits, hidden, shape, dtype, "logits")
-        out, ldo = _result_rows(logits, v, "logits")
+        if logits is None:
+            logits = hidden.new_empty(shape, dtype=dtype)
+            out, ldo = _ptr(logits), v
+        else:
+            _result(logits, hidden, shape, dtype, "logits")
+            out, ldo = _result_rows(logits, v, "logits")
         ws, ws_bytes = _workspace(workspace, lib.flce_mxfp4_logits_workspace_size(n, h), dev)
         st = lib.flce_mxfp4_logits(_ptr(rows), W_DTYPES[hidden.dtype], n, h, ldh, _ptr(head.codes),
                                    _ptr(head.scales), vp, v, softcap, out,
@@ -983,6 +997,36 @@ def beam_select(logits, scores, *, num_select: int | None = None, finished=None,
     return out, parents, tokens
 
 
+def _reorder_plan(dtype, shape, stride, device, to_dtype, to_shape, into, to_device, b: int, k: int,
+                  dev, length: int | None, length_dim: int):
+    """Strides and pieces of one state's layout in bytes; None where there is nothing to move."""
+    if device != dev or to_device != dev:
+        raise ValueError("tensors must be on one CUDA device")
+    if len(shape) < 2 or shape[0] != b or shape[1] != k:
+        raise ValueError("states must be [batch, beams, ...]")
+    if to_shape != shape or to_dtype != dtype:
+        raise ValueError("out must have the states' shapes and dtypes")
+    e = dtype.itemsize
+    inner, outer, outer_stride = e, 1, 0
+    for i in range(len(shape) - 1, 1, -1):
+        n = shape[i]
+        if n > 1 and (stride[i] * e != inner or into[i] * e != inner):
+            raise ValueError("states must be contiguous behind [batch, beams]")
+        inner *= n
+    if (b > 1 and into[0] == 0) or (k > 1 and into[1] == 0):
+        raise ValueError("a state's beams must not share memory")
+    if length is not None:
+        if not 2 <= length_dim < len(shape) or not 0 <= length <= shape[length_dim]:
+            raise ValueError("length must lie within the states' length_dim")
+        for n in shape[2:length_dim]:
+            outer *= n
+        outer_stride = inner // outer if outer else 0
+        inner = outer_stride // max(shape[length_dim], 1) * length
+    if outer * inner * b * k == 0:
+        return None
+    return (stride[0] * e, stride[1] * e, into[0] * e, into[1] * e, outer, outer_stride, inner)
+
+
 def beam_reorder(states, parents, *, length: int | None = None, length_dim: int = 2, out=None,
                  stream=None):
     """``state[b, k] <- state[b, parents[b, k]]`` for one state or a list of them.
@@ -1007,39 +1051,17 @@ def beam_reorder(states, parents, *, length: int | None = None, length_dim: int 
     b, k = parents.shape
     dev = parents.device
     live = []
+    last = plan = None  # states of one layout (a model's layers) share its checks
     for src, dst in zip(srcs, dsts):
-        shape, stride = src.shape, src.stride()
-        _cuda_tensor(src, (src.dtype,), dev, "states")
-        if len(shape) < 2 or shape[0] != b or shape[1] != k:
-            raise ValueError("states must be [batch, beams, ...]")
-        if dst is not src:
-            _cuda_tensor(dst, (src.dtype,), dev, "out")
-            if dst.shape != shape:
-                raise ValueError("out must have the states' shapes")
-        e = src.element_size()
-        inner, outer, outer_stride = e, 1, 0
-        into = dst.stride()
-        for i in range(len(shape) - 1, 1, -1):
-            n = shape[i]
-            if n > 1 and (stride[i] * e != inner or into[i] * e != inner):
-                raise ValueError("states must be contiguous behind [batch, beams]")
-            inner *= n
-        if (b > 1 and into[0] == 0) or (k > 1 and into[1] == 0):
-            raise ValueError("a state's beams must not share memory")
-        if length is not None:
-            if not 2 <= length_dim < len(shape) or not 0 <= length <= shape[length_dim]:
-                raise ValueError("length must lie within the states' length_dim")
-            for n in shape[2:length_dim]:
-                outer *= n
-            outer_stride = inner // outer if outer else 0
-            inner = outer_stride // max(shape[length_dim], 1) * length
-        if outer * inner * b * k == 0:
+        layout = src.dtype, src.shape, src.stride(), src.device, dst.dtype, dst.shape, dst.stride(), dst.device
+        if layout != last:
+            last, plan = layout, _reorder_plan(*layout, b, k, dev, length, length_dim)
+        if plan is None:
             continue
         at, to = src.data_ptr(), dst.data_ptr()
         if out is not None and at == to:
             raise ValueError("out must not overlap the states; leave it out to reorder in place")
-        live.append((at, to, stride[0] * e, stride[1] * e, into[0] * e, into[1] * e, outer,
-                     outer_stride, inner))
+        live.append((at, to, *plan))
     with _on(dev, stream):
         st = lib.flce_beam_reorder((BeamState * len(live))(*live), len(live), _ptr(parents), b,
                                    max(k, 1), _stream_handle(dev, stream))
