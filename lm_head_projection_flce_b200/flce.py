@@ -619,18 +619,21 @@ def ce_backward(logits, labels, lse, grad_loss, *, mask=None, ignore_index: int 
 
 # ---------------------------------------------------------------- layer norm
 
-def _rows(t, h: int, name: str) -> tuple[torch.Tensor, int]:
-    """`t` [..., h] as rows [N, h] of unit stride, and their distance in elements."""
+def _rows(t, h: int, name: str) -> tuple[torch.Tensor, int, int]:
+    """`t` [..., h] as N rows of unit stride: a tensor that starts with the first of
+    them, N, and their distance in elements."""
+    if t.is_contiguous():
+        return t, t.numel() // h, h
     rows = t if t.dim() == 2 else t.reshape(-1, h)
     n = rows.shape[0]
     step, unit = rows.stride()
     if unit != 1 and h > 1:
         raise ValueError(f"{name} rows must be contiguous")
     if n <= 1:
-        return rows, h
+        return rows, n, h
     if step < h:
         raise ValueError(f"{name} rows must not overlap")
-    return rows, step
+    return rows, n, step
 
 
 def _cuda_tensor(t, dtypes, dev, name: str) -> None:
@@ -651,7 +654,7 @@ def _result(t, like, shape, dtype, name: str) -> torch.Tensor:
 
 def _result_rows(t, h: int, name: str) -> tuple[int, int]:
     """Address and row distance of an output, which must be rows of one stride in place."""
-    rows, ld = _rows(t, h, name)
+    rows, _, ld = _rows(t, h, name)
     if rows is not t and rows.data_ptr() != t.data_ptr():
         raise ValueError(f"{name}'s rows must have one stride")
     return _ptr(rows), ld
@@ -683,8 +686,8 @@ def _norm_rows(x) -> tuple[torch.Tensor, int, int, int]:
     if x.dim() == 0 or x.shape[-1] == 0:
         raise ValueError("x must be [..., hidden] with hidden >= 1")
     h = x.shape[-1]
-    rows, ldx = _rows(x, h, "x")
-    return rows, rows.shape[0], h, ldx
+    rows, n, ldx = _rows(x, h, "x")
+    return rows, n, h, ldx
 
 
 def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5,
@@ -740,7 +743,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, want=("dx", "dweight"
     if dy.shape != x.shape:
         raise ValueError("dy must have x's shape")
     w_dtype = _norm_params(weight, None, h, dev, param_dtype)
-    grads, lddy = _rows(dy, h, "dy")
+    grads, _, lddy = _rows(dy, h, "dy")
     _buffer(mean, n, torch.float32, dev, "mean")
     _buffer(rstd, n, torch.float32, dev, "rstd")
     with _on(dev, stream):
@@ -760,7 +763,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, want=("dx", "dweight"
         else:
             dbias = None
         _norm_grads(lib, grads, lddy, rows, n, h, ldx, weight, w_dtype, mean, rstd, dx,
-                    h if dx is None else _rows(dx, h, "dx")[1], dweight, dbias, workspace,
+                    h if dx is None else _rows(dx, h, "dx")[2], dweight, dbias, workspace,
                     _stream_handle(dev, stream))
     return dx, dweight, dbias
 
@@ -797,12 +800,12 @@ class _LayerNorm(torch.autograd.Function):
         h = x.shape[-1]
         dev = x.device
         dy = dy.contiguous()  # a gradient that autograd broadcast (a sum's) has rows of stride 0
-        rows, ldx = _rows(x, h, "x")
+        rows, n, ldx = _rows(x, h, "x")
         with _on(dev):
             dx = x.new_empty(x.shape) if need_x else None
             dw = x.new_empty(h, dtype=ctx.w_dtype) if need_w else None
             db = x.new_empty(h, dtype=ctx.w_dtype) if need_b else None
-            _norm_grads(_LIB, dy, h, rows, rows.shape[0], h, ldx, weight, ctx.w_dtype, mean, rstd,
+            _norm_grads(_LIB, dy, h, rows, n, h, ldx, weight, ctx.w_dtype, mean, rstd,
                         dx, h, dw, db, None, _stream_handle(dev))
         return dx, dw, db, None
 
@@ -876,14 +879,15 @@ def mxfp4_quantize(x, *, out: Mxfp4 | None = None, stream=None) -> Mxfp4:
     _cuda_tensor(x, W_DTYPES, None, "x")
     if x.dim() != 2 or x.shape[1] == 0:
         raise ValueError("x must be [rows, cols] with cols >= 1")
-    rows, ld = _rows(x, x.shape[1], "x")
     n, h = x.shape
+    rows, _, ld = _rows(x, h, "x")
     dev = x.device
     with _on(dev, stream):
         if out is None:
             codes = x.new_empty(lib.flce_mxfp4_codes_size(n, h), dtype=torch.uint8)
             scales = x.new_empty(lib.flce_mxfp4_scales_size(n, h), dtype=torch.uint8)
-            out = Mxfp4(codes, scales, n, h)
+            out = object.__new__(Mxfp4)  # nothing to check in buffers made here
+            out.__dict__.update(codes=codes, scales=scales, rows=n, cols=h)
         else:
             _mxfp4_operand(out, "out")
             if out.shape != (n, h) or out.device != dev:
@@ -927,8 +931,7 @@ def mxfp4_logits(hidden, head: Mxfp4, *, softcap: float = 0.0, unpadded_vocab: i
         raise ValueError("hidden must be [..., H] with the head's H")
     dev, h, vp = hidden.device, head.cols, head.rows
     v = vp if unpadded_vocab is None or unpadded_vocab <= 0 else int(unpadded_vocab)
-    rows, ldh = _rows(hidden, h, "hidden")
-    n = rows.shape[0]
+    rows, n, ldh = _rows(hidden, h, "hidden")
     shape = (*hidden.shape[:-1], v)
     with _on(dev, stream):
         if logits is None:
@@ -977,7 +980,7 @@ def beam_select(logits, scores, *, num_select: int | None = None, finished=None,
     if (finished is None) != (eos_token is None):
         raise ValueError("finished and eos_token go together")
     m = k if num_select is None else int(num_select)
-    rows, ld = _rows(logits, vp, "logits")
+    rows, _, ld = _rows(logits, vp, "logits")
     with _on(dev, stream):
         done = None
         if finished is not None:
