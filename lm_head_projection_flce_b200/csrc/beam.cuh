@@ -13,9 +13,12 @@
 // exponentials, and its largest element with the vector that held it.  The
 // M-th largest of the 256 threads' maxima bounds the M-th largest element from
 // below, so the M best elements of the segment all lie with the at most M
-// threads above the bound; only those threads' vectors (M / 256 of the
-// segment, now in L2) are looked at again and the few elements above the bound
-// sorted by counting.  The pass costs one exponential per element and one
+// threads above the bound.  Each thread also leaves the maximum of every few
+// batches in shared memory (16 bits of it, rounded down), so of those threads'
+// vectors only the ones that can hold such an element are loaded again (all of
+// them would be M / 256 of the segment, but in pieces of 16 bytes, which cost HBM a
+// quarter of the pass), and the few elements above the bound are sorted by
+// counting.  The pass costs one exponential per element and one
 // comparison per vector, like a plain logsumexp, and is bound by HBM.
 // A second kernel merges an item's segments: lse_k, the candidates' scores in
 // FP64 (scores of different beams lie next to one another; in FP32 their
@@ -38,6 +41,7 @@ constexpr int kBeamMaxSelect = 64;
 constexpr int kBeamUnroll = 4;            // vectors in flight per thread
 constexpr int kBeamResident = 4;          // blocks per SM the registers are limited for
 constexpr int kBeamUnits = 3;             // blocks per SM aimed at when rows are few
+constexpr int kBeamGroups = 32;           // recorded maxima per thread, at most
 constexpr int kBeamList = 1024;           // elements above the bound that are sorted in one go
 constexpr int64_t kBeamMinSegment = 4096; // elements
 constexpr int kBeamMaxItems = 4096;       // candidates merged per batch item: K x segments x M
@@ -123,6 +127,7 @@ __device__ __forceinline__ uint64_t beam_bound(uint64_t mine, int select, BeamBo
   if (in) {
     const int n = sm.n;
     int above = 0, same = 0;
+#pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const uint64_t k = sm.keys[i];
       above += k > mine ? 1 : 0;
@@ -138,6 +143,7 @@ struct BeamPartArgs {
   const void* logits;
   int64_t ld, vocab, segment;
   int splits, select;
+  int group_shift;          // batches per recorded maximum, as a power of two
   int64_t rows;
   const float* scores;      // [rows]
   const uint8_t* finished;  // [rows] or nullptr
@@ -155,6 +161,7 @@ template <typename T>
 __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_kernel(const BeamPartArgs a) {
   constexpr int VN = 16 / int(sizeof(T));
   constexpr uint32_t kNegInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+  extern __shared__ uint16_t seen[];  // [groups][threads]: the upper half of beam_order(maximum)
   __shared__ BeamBound bs;
   __shared__ uint64_t list[kBeamList];
   __shared__ int owners[kBeamMaxSelect];
@@ -195,6 +202,8 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
     }
   };
   fetch(tid);
+  float gm = -INFINITY;  // maximum of the current group of batches
+  int batch = 0;
   for (int j0 = tid; j0 < count; j0 += kBeamUnroll * kBeamThreads) {
     uint4 cur[kBeamUnroll];
 #pragma unroll
@@ -210,6 +219,10 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
       }
       bm = fmaxf(bm, vm);
     }
+    // Written at every batch; the group's last one stays.
+    gm = (batch & ((1 << a.group_shift) - 1)) == 0 ? bm : fmaxf(gm, bm);
+    seen[(batch >> a.group_shift) * kBeamThreads + tid] = uint16_t(beam_order(gm) >> 16);
+    ++batch;
     if (bm > m) {
       s2 = __fmul2_rn(s2, ln_both(fast_exp2((m - bm) * kLog2e)));
       m = bm;
@@ -259,22 +272,30 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
   __syncthreads();
 
   // Elements of the owners' vectors whose (value, vector) is not below the bound.
+  const int size = kBeamUnroll << a.group_shift;  // vectors per group
   const int per = (count + kBeamThreads - 1) / kBeamThreads;  // vectors per thread
-  const int work = n_owners * per;
+  const int groups = (per + size - 1) / size;
+  const int work = n_owners * groups;
+  const uint32_t least = uint32_t(bound >> 48);
   auto scan = [&](auto&& take) {
     for (int w = tid; w < work; w += kBeamThreads) {
-      const int q = w / per, j = owners[q] + (w - q * per) * kBeamThreads;
-      if (j >= count) continue;
-      float2 x[VN / 2];
-      beam_unpack<T>(load16_any<T>(z, begin + int64_t(j) * VN, a.vocab, kNegInf), x);
-      const uint32_t at = uint32_t(begin) + uint32_t(j) * VN;
-      auto one = [&](float v, uint32_t i) {
-        if (v > -INFINITY && beam_key(v, at) >= bound) take(beam_key(v, at + i));
-      };
+      const int q = w / groups, g = w - q * groups, owner = owners[q];
+      // the owner's last group may have no batch, and no record
+      if (owner + g * size * kBeamThreads >= count || seen[g * kBeamThreads + owner] < least) continue;
+      for (int u = 0; u < size; ++u) {
+        const int j = owner + (g * size + u) * kBeamThreads;
+        if (j >= count) break;
+        float2 x[VN / 2];
+        beam_unpack<T>(load16_any<T>(z, begin + int64_t(j) * VN, a.vocab, kNegInf), x);
+        const uint32_t at = uint32_t(begin) + uint32_t(j) * VN;
+        auto one = [&](float v, uint32_t i) {
+          if (v > -INFINITY && beam_key(v, at) >= bound) take(beam_key(v, at + i));
+        };
 #pragma unroll
-      for (int i = 0; i < VN / 2; ++i) {
-        one(x[i].x, 2 * i);
-        one(x[i].y, 2 * i + 1);
+        for (int i = 0; i < VN / 2; ++i) {
+          one(x[i].x, 2 * i);
+          one(x[i].y, 2 * i + 1);
+        }
       }
     }
   };
@@ -295,6 +316,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
     for (int i = tid; i < n; i += kBeamThreads) {
       const uint64_t key = list[i];
       int r = 0;
+#pragma unroll 4
       for (int j = 0; j < n; ++j) r += list[j] > key ? 1 : 0;
       if (r < a.select) put(r, key);
     }
@@ -361,7 +383,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
   const uint32_t vocab = uint32_t(a.vocab);
   uint64_t* tot = dyn;                                       // [items]
   uint32_t* idx = reinterpret_cast<uint32_t*>(tot + items);  // [items]
-  uint32_t* list = idx + items;                              // [items]: positions above the bound
+  uint32_t* sel_i = idx + items;                             // [items]: what is above the bound
+  uint64_t* sel_t = reinterpret_cast<uint64_t*>(sel_i + items);  // 16 bytes per item behind tot
   const int64_t b = blockIdx.x;
   const float* scores = a.scores + b * a.beams;
   const uint8_t* finished = a.finished ? a.finished + b * a.beams : nullptr;
@@ -428,16 +451,21 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
     item(i, a.cand_z[at0 + place(i)], a.cand_v[at0 + place(i)]);
   const uint64_t bound = beam_bound(top, a.select, bs);
   for (int i = tid; i < items; i += kBeamThreads)
-    if (tot[i] != 0 && tot[i] >= bound) list[atomicAdd(&n_list, 1)] = i;
+    if (tot[i] != 0 && tot[i] >= bound) {
+      const int at = atomicAdd(&n_list, 1);
+      sel_t[at] = tot[i];
+      sel_i[at] = idx[i];
+    }
   __syncthreads();
   const int n = n_list;
   for (int i = tid; i < n; i += kBeamThreads) {
-    const uint64_t t = tot[list[i]];
-    const uint32_t f = idx[list[i]];
+    const uint64_t t = sel_t[i];
+    const uint32_t f = sel_i[i];
     int r = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
-      const uint64_t tj = tot[list[j]];
-      r += tj > t || (tj == t && idx[list[j]] < f) ? 1 : 0;
+      const uint64_t tj = sel_t[j];
+      r += tj > t || (tj == t && sel_i[j] < f) ? 1 : 0;
     }
     if (r < a.select) {
       const int64_t at = b * a.select + r;
@@ -606,10 +634,14 @@ extern "C" int flce_beam_select(const void* logits, int dtype, int64_t batch, in
   {
     LaunchScope scope(KF_BEAM_PART, 0.0, double(rows) * double(vocab) * (dtype == FLCE_F32 ? 4 : 2), cs);
     const unsigned grid = unsigned(rows * p.splits);
+    const int64_t batches = cdiv(p.segment, int64_t(kBeamUnroll) * kBeamThreads * (dtype == FLCE_F32 ? 4 : 8));
+    while (cdiv(batches, int64_t(1) << a.group_shift) > kBeamGroups) ++a.group_shift;
+    const size_t seen =
+        size_t(cdiv(batches, int64_t(1) << a.group_shift)) * kBeamThreads * sizeof(uint16_t);
     if (dtype == FLCE_BF16)
-      beam_partials_kernel<__nv_bfloat16><<<grid, kBeamThreads, 0, cs>>>(a);
+      beam_partials_kernel<__nv_bfloat16><<<grid, kBeamThreads, seen, cs>>>(a);
     else
-      beam_partials_kernel<float><<<grid, kBeamThreads, 0, cs>>>(a);
+      beam_partials_kernel<float><<<grid, kBeamThreads, seen, cs>>>(a);
   }
   if (cudaGetLastError() != cudaSuccess) return FLCE_ERR_CUDA;
   BeamMergeArgs g{};
@@ -627,10 +659,10 @@ extern "C" int flce_beam_select(const void* logits, int dtype, int64_t batch, in
   g.out_scores = out_scores;
   g.parents = parents;
   g.tokens = tokens;
-  const size_t smem = size_t(beams) * size_t(p.splits) * size_t(num_select) * 16;
+  const size_t smem = size_t(beams) * size_t(p.splits) * size_t(num_select) * 24;
   if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kBeamMaxItems * 16) != cudaSuccess)
+                           kBeamMaxItems * 24) != cudaSuccess)
     return FLCE_ERR_CUDA;
   LaunchScope scope(KF_BEAM_MERGE, 0.0, double(rows) * p.splits * (12.0 + 8.0 * double(num_select)), cs);
   // Launched while the first kernel still runs; its blocks wait for that kernel's
