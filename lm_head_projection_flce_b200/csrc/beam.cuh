@@ -40,7 +40,6 @@ constexpr int kBeamMaxBeams = 64;
 constexpr int kBeamMaxSelect = 64;
 constexpr int kBeamUnroll = 4;            // vectors in flight per thread
 constexpr int kBeamResident = 4;          // blocks per SM the registers are limited for
-constexpr int kBeamUnits = 3;             // blocks per SM aimed at when rows are few
 constexpr int kBeamGroups = 32;           // recorded maxima per thread, at most
 constexpr int kBeamList = 1024;           // elements above the bound that are sorted in one go
 constexpr int64_t kBeamMinSegment = 4096; // elements
@@ -124,16 +123,19 @@ __device__ __forceinline__ uint64_t beam_bound(uint64_t mine, int select, BeamBo
   at = __shfl_sync(0xffffffffu, at, 0) + __popc(vote & ((1u << lane) - 1u));
   if (in) sm.keys[at] = mine;
   __syncthreads();
-  if (in) {
-    const int n = sm.n;
+  // Ranked by as many threads as there are keys: left where they are, they would
+  // keep every warp busy.
+  const int n = sm.n;
+  if (int(threadIdx.x) < n) {
+    const uint64_t key = sm.keys[threadIdx.x];
     int above = 0, same = 0;
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const uint64_t k = sm.keys[i];
-      above += k > mine ? 1 : 0;
-      same += k == mine ? 1 : 0;
+      above += k > key ? 1 : 0;
+      same += k == key ? 1 : 0;
     }
-    if (above < select && above + same >= select) sm.bound = mine;
+    if (above < select && above + same >= select) sm.bound = key;
   }
   __syncthreads();
   return sm.bound;
@@ -282,19 +284,30 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
       const int q = w / groups, g = w - q * groups, owner = owners[q];
       // the owner's last group may have no batch, and no record
       if (owner + g * size * kBeamThreads >= count || seen[g * kBeamThreads + owner] < least) continue;
-      for (int u = 0; u < size; ++u) {
-        const int j = owner + (g * size + u) * kBeamThreads;
-        if (j >= count) break;
-        float2 x[VN / 2];
-        beam_unpack<T>(load16_any<T>(z, begin + int64_t(j) * VN, a.vocab, kNegInf), x);
-        const uint32_t at = uint32_t(begin) + uint32_t(j) * VN;
-        auto one = [&](float v, uint32_t i) {
-          if (v > -INFINITY && beam_key(v, at) >= bound) take(beam_key(v, at + i));
-        };
+      for (int u0 = 0; u0 < size; u0 += kBeamUnroll) {
+        const int j0 = owner + (g * size + u0) * kBeamThreads;
+        uint4 raw[kBeamUnroll];  // a batch's loads before any of them is used
 #pragma unroll
-        for (int i = 0; i < VN / 2; ++i) {
-          one(x[i].x, 2 * i);
-          one(x[i].y, 2 * i + 1);
+        for (int u = 0; u < kBeamUnroll; ++u) {
+          const int j = j0 + u * kBeamThreads;
+          raw[u] = make_uint4(kNegInf, kNegInf, kNegInf, kNegInf);
+          if (j < count) raw[u] = load16_any<T>(z, begin + int64_t(j) * VN, a.vocab, kNegInf);
+        }
+#pragma unroll
+        for (int u = 0; u < kBeamUnroll; ++u) {
+          const uint32_t at = uint32_t(begin) + uint32_t(j0 + u * kBeamThreads) * VN;
+          const float top = beam_max<T>(raw[u]);
+          if (!(top > -INFINITY) || beam_key(top, at) < bound) continue;
+          float2 x[VN / 2];
+          beam_unpack<T>(raw[u], x);
+          auto one = [&](float v, uint32_t i) {
+            if (v > -INFINITY && beam_key(v, at) >= bound) take(beam_key(v, at + i));
+          };
+#pragma unroll
+          for (int i = 0; i < VN / 2; ++i) {
+            one(x[i].x, 2 * i);
+            one(x[i].y, 2 * i + 1);
+          }
         }
       }
     }
@@ -498,12 +511,14 @@ struct BeamPlan {
   size_t off_s, off_m, off_z, off_v, total;
 };
 
-// Segments per row: enough blocks for the GPU when there are few rows, none
-// shorter than kBeamMinSegment, and no more candidates per item than one block merges.
+// Segments per row: as many as keep all blocks resident at once (a second, partly
+// filled wave costs more than longer segments: 19.5 against 14.5 us for 64 rows of
+// 50001), none shorter than kBeamMinSegment, and no more candidates per item than
+// one block merges.
 static BeamPlan plan_beam(int64_t batch, int64_t beams, int64_t vocab, int64_t select) {
   BeamPlan p{};
   const int64_t rows = std::max<int64_t>(1, batch * beams);
-  int64_t s = cdiv(kBeamUnits * kLnSms, rows);
+  int64_t s = std::max<int64_t>(1, int64_t(kBeamResident) * kLnSms / rows);
   s = std::min({s, std::max<int64_t>(1, vocab / kBeamMinSegment),
                 std::max<int64_t>(1, kBeamMaxItems / (beams * select))});
   p.segment = cdiv(cdiv(vocab, s), 8) * 8;

@@ -822,7 +822,7 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
 
 # ---------------------------------------------------------------- the head in MXFP4
 
-@dataclasses.dataclass(frozen=True)
+@dataclasses.dataclass(frozen=True, eq=False)
 class Mxfp4:
     """A matrix [rows, cols] in microscaled 4-bit floating point (see include/flce.h):
     ``codes`` uint8, two E2M1 codes per byte, in tiles of 128 rows x 256 columns, and
