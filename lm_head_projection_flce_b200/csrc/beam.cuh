@@ -185,14 +185,22 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
   // The next batch is loaded before the current one is used: a block alone, or
   // with few neighbours, would otherwise leave HBM idle between its loads.
   uint4 raw[kBeamUnroll];
-  const uint4* body = reinterpret_cast<const uint4*>(z + begin);
-  // whole vectors on 16 bytes: none of them needs a look at its ends
-  const int whole =
-      (reinterpret_cast<uintptr_t>(z) & 15) == 0 ? int(min(int64_t(count), (a.vocab - begin) / VN)) : 0;
+  // Batches of whole vectors need no look at their ends: vectors [first, whole).
+  const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(z)) & 15u;
+  const uintptr_t body = reinterpret_cast<uintptr_t>(z + begin) - off;
+  const int first = off != 0 && begin == 0 ? 1 : 0;
+  const int whole = int(min(int64_t(count), (a.vocab - begin) / VN - (off != 0 ? 1 : 0)));
   auto fetch = [&](int j0) {
-    if (j0 + (kBeamUnroll - 1) * kBeamThreads < whole) {
+    if (j0 >= first && j0 + (kBeamUnroll - 1) * kBeamThreads < whole) {
+      const uintptr_t at = body + int64_t(j0) * 16;
+      if (off == 0) {
 #pragma unroll
-      for (int u = 0; u < kBeamUnroll; ++u) raw[u] = body[j0 + u * kBeamThreads];
+        for (int u = 0; u < kBeamUnroll; ++u)
+          raw[u] = *reinterpret_cast<const uint4*>(at + u * kBeamThreads * 16);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kBeamUnroll; ++u) raw[u] = load16_shifted(at + u * kBeamThreads * 16, off);
+      }
       return;
     }
 #pragma unroll

@@ -108,34 +108,37 @@ struct LnIo<float, N> {
   }
 };
 
+// 16 bytes at `off` bytes (a multiple of the element, not 0) past an aligned
+// address: cut out of the two aligned vectors around them (the second is the
+// neighbouring thread's first: an L1 hit).
+__device__ __forceinline__ uint4 load16_shifted(uintptr_t aligned_at, uint32_t off) {
+  const uint4 lo = *reinterpret_cast<const uint4*>(aligned_at);
+  const uint4 hi = *reinterpret_cast<const uint4*>(aligned_at + 16);
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (off & 8u) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (off & 4u) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const uint32_t sh = (off & 3u) * 8u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], sh);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 // 16 bytes of elements [c, c + N) of a row at any alignment; `fill` (a word of
-// them) behind `end`.  In a row that does
-// not start on 16 bytes the vector is cut out of the two aligned ones around it
-// (the second is the neighbouring thread's first: an L1 hit); the row's first and
-// last vectors, where these would reach out of the row, are read by elements.
+// them) behind `end`.  In a row that does not start on 16 bytes they are shifted
+// into place; its first and last vectors, where the aligned ones would reach out of
+// the row, are read by elements.
 template <typename T>
 __device__ __forceinline__ uint4 load16_any(const T* row, int64_t c, int64_t end, uint32_t fill) {
   constexpr int N = 16 / int(sizeof(T));
   const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
   const uint32_t off = static_cast<uint32_t>(at) & 15u;  // the same for the whole row
   if (off == 0 && c + N <= end) return *reinterpret_cast<const uint4*>(at);
-  if (off != 0 && c >= N && c + 2 * N <= end) {
-    const uint4 lo = *reinterpret_cast<const uint4*>(at - off);
-    const uint4 hi = *reinterpret_cast<const uint4*>(at - off + 16);
-    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    if (off & 8u) {
-#pragma unroll
-      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    }
-    if (off & 4u) {
-#pragma unroll
-      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    }
-    const uint32_t sh = (off & 3u) * 8u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], sh);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  if (off != 0 && c >= N && c + 2 * N <= end) return load16_shifted(at - off, off);
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
