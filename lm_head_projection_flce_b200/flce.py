@@ -21,7 +21,6 @@ FP32 head rounded to BF16).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 import os
@@ -168,19 +167,24 @@ def _stream_handle(device: torch.device, stream=None) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-_HERE = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _elsewhere(device: torch.device, stream) -> bool:
+    """True when a call has to make its tensors' device, or `stream`, current first.
+    Entry points then call themselves inside `_on`, so that whatever they allocate
+    or copy belongs to that stream as well."""
+    return stream is not None or device.index != _current_device()
 
 
 def _on(device: torch.device, stream=None):
     """Context in which `device` and `stream` (None: the device's current stream)
-    are current, so that what is allocated inside belongs to that stream."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("stream must belong to the tensors' device")
-        return torch.cuda.stream(stream)
-    if device.index == torch.cuda.current_device():
-        return _HERE
-    return torch.cuda.device(device)
+    are current."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError("stream must belong to the tensors' device")
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t: torch.Tensor | None) -> int:
@@ -681,13 +685,10 @@ def _norm_params(weight, bias, h: int, dev, param_dtype=None) -> torch.dtype:
     return dtype
 
 
-def _norm_rows(x) -> tuple[torch.Tensor, int, int, int]:
+def _norm_input(x) -> None:
     _cuda_tensor(x, W_DTYPES, None, "x")
     if x.dim() == 0 or x.shape[-1] == 0:
         raise ValueError("x must be [..., hidden] with hidden >= 1")
-    h = x.shape[-1]
-    rows, n, ldx = _rows(x, h, "x")
-    return rows, n, h, ldx
 
 
 def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5,
@@ -701,28 +702,34 @@ def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5,
     (``stats=False``: None for statistics that were not given, and not written).
     """
     lib = _LIB or load_library()
-    rows, n, h, ldx = _norm_rows(x)
+    _norm_input(x)
     dev = x.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return layer_norm_forward(x, weight, bias, eps=eps, y=y, mean=mean, rstd=rstd,
+                                      stats=stats)
+    h = x.shape[-1]
+    rows, n, ldx = _rows(x, h, "x")
     w_dtype = _norm_params(weight, bias, h, dev)
-    with _on(dev, stream):
-        if y is None:
-            y = x.new_empty(x.shape)
-            out, ldy = _ptr(y), h
-        else:
-            _result(y, x, x.shape, x.dtype, "y")
-            out, ldy = _result_rows(y, h, "y")
-        if mean is not None:
-            _buffer(mean, n, torch.float32, dev, "mean")
-        elif stats:
-            mean = x.new_empty(n, dtype=torch.float32)
-        if rstd is not None:
-            _buffer(rstd, n, torch.float32, dev, "rstd")
-        elif stats:
-            rstd = x.new_empty(n, dtype=torch.float32)
-        st = lib.flce_layer_norm_forward(_ptr(rows), W_DTYPES[x.dtype], n, h, ldx, _ptr(weight),
-                                         _ptr(bias), W_DTYPES[w_dtype], eps, out, ldy, _ptr(mean),
-                                         _ptr(rstd), _stream_handle(dev, stream))
-    _check("flce_layer_norm_forward", st)
+    if y is None:
+        y = x.new_empty(x.shape)
+        out, ldy = y.data_ptr(), h
+    else:
+        _result(y, x, x.shape, x.dtype, "y")
+        out, ldy = _result_rows(y, h, "y")
+    if mean is not None:
+        _buffer(mean, n, torch.float32, dev, "mean")
+    elif stats:
+        mean = x.new_empty(n, dtype=torch.float32)
+    if rstd is not None:
+        _buffer(rstd, n, torch.float32, dev, "rstd")
+    elif stats:
+        rstd = x.new_empty(n, dtype=torch.float32)
+    st = lib.flce_layer_norm_forward(rows.data_ptr(), W_DTYPES[x.dtype], n, h, ldx, _ptr(weight),
+                                     _ptr(bias), W_DTYPES[w_dtype], eps, out, ldy, _ptr(mean),
+                                     _ptr(rstd), _stream_handle(dev))
+    if st != FLCE_OK:
+        raise FlceError("flce_layer_norm_forward", st)
     return y, mean, rstd
 
 
@@ -734,11 +741,18 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, want=("dx", "dweight"
     not in ``want``.  ``dx`` has x's dtype, the other two the weight's
     (``param_dtype`` where there is no weight; FP32 by default)."""
     lib = _LIB or load_library()
-    rows, n, h, ldx = _norm_rows(x)
+    _norm_input(x)
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return layer_norm_backward(dy, x, mean, rstd, weight, want=want,
+                                       param_dtype=param_dtype, dx=dx, dweight=dweight,
+                                       dbias=dbias, workspace=workspace)
+    h = x.shape[-1]
+    rows, n, ldx = _rows(x, h, "x")
     unknown = set(want) - {"dx", "dweight", "dbias"}
     if unknown:
         raise ValueError(f"unknown gradients {sorted(unknown)}")
-    dev = x.device
     _cuda_tensor(dy, (x.dtype,), dev, "dy")
     if dy.shape != x.shape:
         raise ValueError("dy must have x's shape")
@@ -746,25 +760,24 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, want=("dx", "dweight"
     grads, _, lddy = _rows(dy, h, "dy")
     _buffer(mean, n, torch.float32, dev, "mean")
     _buffer(rstd, n, torch.float32, dev, "rstd")
-    with _on(dev, stream):
-        if "dx" in want:
-            dx = _result(dx, x, x.shape, x.dtype, "dx")
-            _result_rows(dx, h, "dx")
-        else:
-            dx = None
-        if "dweight" in want:
-            dweight = (x.new_empty(h, dtype=w_dtype) if dweight is None
-                       else _buffer(dweight, h, w_dtype, dev, "dweight"))
-        else:
-            dweight = None
-        if "dbias" in want:
-            dbias = (x.new_empty(h, dtype=w_dtype) if dbias is None
-                     else _buffer(dbias, h, w_dtype, dev, "dbias"))
-        else:
-            dbias = None
-        _norm_grads(lib, grads, lddy, rows, n, h, ldx, weight, w_dtype, mean, rstd, dx,
-                    h if dx is None else _rows(dx, h, "dx")[2], dweight, dbias, workspace,
-                    _stream_handle(dev, stream))
+    lddx = h
+    if "dx" in want:
+        dx = _result(dx, x, x.shape, x.dtype, "dx")
+        _, lddx = _result_rows(dx, h, "dx")
+    else:
+        dx = None
+    if "dweight" in want:
+        dweight = (x.new_empty(h, dtype=w_dtype) if dweight is None
+                   else _buffer(dweight, h, w_dtype, dev, "dweight"))
+    else:
+        dweight = None
+    if "dbias" in want:
+        dbias = (x.new_empty(h, dtype=w_dtype) if dbias is None
+                 else _buffer(dbias, h, w_dtype, dev, "dbias"))
+    else:
+        dbias = None
+    _norm_grads(lib, grads, lddy, rows, n, h, ldx, weight, w_dtype, mean, rstd, dx, lddx, dweight,
+                dbias, workspace, _stream_handle(dev))
     return dx, dweight, dbias
 
 
@@ -796,17 +809,23 @@ class _LayerNorm(torch.autograd.Function):
         # What the forward checked is not checked again: this runs in autograd's own
         # thread, where a small call's time is mostly Python.
         x, weight, mean, rstd = ctx.saved_tensors
+        dev = x.device
+        if _elsewhere(dev, None):
+            with _on(dev):
+                return _LayerNorm._grads(ctx, dy, x, weight, mean, rstd)
+        return _LayerNorm._grads(ctx, dy, x, weight, mean, rstd)
+
+    @staticmethod
+    def _grads(ctx, dy, x, weight, mean, rstd):
         need_x, need_w, need_b, _ = ctx.needs_input_grad
         h = x.shape[-1]
-        dev = x.device
         dy = dy.contiguous()  # a gradient that autograd broadcast (a sum's) has rows of stride 0
         rows, n, ldx = _rows(x, h, "x")
-        with _on(dev):
-            dx = x.new_empty(x.shape) if need_x else None
-            dw = x.new_empty(h, dtype=ctx.w_dtype) if need_w else None
-            db = x.new_empty(h, dtype=ctx.w_dtype) if need_b else None
-            _norm_grads(_LIB, dy, h, rows, n, h, ldx, weight, ctx.w_dtype, mean, rstd,
-                        dx, h, dw, db, None, _stream_handle(dev))
+        dx = x.new_empty(x.shape) if need_x else None
+        dw = x.new_empty(h, dtype=ctx.w_dtype) if need_w else None
+        db = x.new_empty(h, dtype=ctx.w_dtype) if need_b else None
+        _norm_grads(_LIB, dy, h, rows, n, h, ldx, weight, ctx.w_dtype, mean, rstd, dx, h, dw, db,
+                    None, _stream_handle(x.device))
         return dx, dw, db, None
 
 
@@ -880,20 +899,22 @@ def mxfp4_quantize(x, *, out: Mxfp4 | None = None, stream=None) -> Mxfp4:
     if x.dim() != 2 or x.shape[1] == 0:
         raise ValueError("x must be [rows, cols] with cols >= 1")
     n, h = x.shape
-    rows, _, ld = _rows(x, h, "x")
     dev = x.device
-    with _on(dev, stream):
-        if out is None:
-            codes = x.new_empty(lib.flce_mxfp4_codes_size(n, h), dtype=torch.uint8)
-            scales = x.new_empty(lib.flce_mxfp4_scales_size(n, h), dtype=torch.uint8)
-            out = object.__new__(Mxfp4)  # nothing to check in buffers made here
-            out.__dict__.update(codes=codes, scales=scales, rows=n, cols=h)
-        else:
-            _mxfp4_operand(out, "out")
-            if out.shape != (n, h) or out.device != dev:
-                raise ValueError("out must have x's shape and device")
-        st = lib.flce_mxfp4_quantize(_ptr(rows), W_DTYPES[x.dtype], n, h, ld, _ptr(out.codes),
-                                     _ptr(out.scales), _stream_handle(dev, stream))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return mxfp4_quantize(x, out=out)
+    rows, _, ld = _rows(x, h, "x")
+    if out is None:
+        codes = x.new_empty(lib.flce_mxfp4_codes_size(n, h), dtype=torch.uint8)
+        scales = x.new_empty(lib.flce_mxfp4_scales_size(n, h), dtype=torch.uint8)
+        out = object.__new__(Mxfp4)  # nothing to check in buffers made here
+        out.__dict__.update(codes=codes, scales=scales, rows=n, cols=h)
+    else:
+        _mxfp4_operand(out, "out")
+        if out.shape != (n, h) or out.device != dev:
+            raise ValueError("out must have x's shape and device")
+    st = lib.flce_mxfp4_quantize(rows.data_ptr(), W_DTYPES[x.dtype], n, h, ld, out.codes.data_ptr(),
+                                 out.scales.data_ptr(), _stream_handle(dev))
     _check("flce_mxfp4_quantize", st)
     return out
 
@@ -906,11 +927,13 @@ def mxfp4_dequantize(q: Mxfp4, dtype: torch.dtype = torch.bfloat16, *,
     if dtype not in W_DTYPES:
         raise TypeError("dtype must be bf16 or fp32")
     dev = q.device
-    with _on(dev, stream):
-        out = _result(out, q.codes, q.shape, dtype, "out")
-        rows, ld = _result_rows(out, q.cols, "out")
-        st = lib.flce_mxfp4_dequantize(_ptr(q.codes), _ptr(q.scales), q.rows, q.cols, rows,
-                                       W_DTYPES[dtype], ld, _stream_handle(dev, stream))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return mxfp4_dequantize(q, dtype, out=out)
+    out = _result(out, q.codes, q.shape, dtype, "out")
+    rows, ld = _result_rows(out, q.cols, "out")
+    st = lib.flce_mxfp4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, rows,
+                                   W_DTYPES[dtype], ld, _stream_handle(dev))
     _check("flce_mxfp4_dequantize", st)
     return out
 
@@ -930,21 +953,23 @@ def mxfp4_logits(hidden, head: Mxfp4, *, softcap: float = 0.0, unpadded_vocab: i
     if hidden.dim() == 0 or hidden.shape[-1] != head.cols:
         raise ValueError("hidden must be [..., H] with the head's H")
     dev, h, vp = hidden.device, head.cols, head.rows
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return mxfp4_logits(hidden, head, softcap=softcap, unpadded_vocab=unpadded_vocab,
+                                dtype=dtype, logits=logits, workspace=workspace)
     v = vp if unpadded_vocab is None or unpadded_vocab <= 0 else int(unpadded_vocab)
     rows, n, ldh = _rows(hidden, h, "hidden")
     shape = (*hidden.shape[:-1], v)
-    with _on(dev, stream):
-        if logits is None:
-            logits = hidden.new_empty(shape, dtype=dtype)
-            out, ldo = _ptr(logits), v
-        else:
-            _result(logits, hidden, shape, dtype, "logits")
-            out, ldo = _result_rows(logits, v, "logits")
-        ws, ws_bytes = _workspace(workspace, lib.flce_mxfp4_logits_workspace_size(n, h), dev)
-        st = lib.flce_mxfp4_logits(_ptr(rows), W_DTYPES[hidden.dtype], n, h, ldh, _ptr(head.codes),
-                                   _ptr(head.scales), vp, v, softcap, out,
-                                   W_DTYPES[dtype], ldo, _ptr(ws), ws_bytes,
-                                   _stream_handle(dev, stream))
+    if logits is None:
+        logits = hidden.new_empty(shape, dtype=dtype)
+        out, ldo = logits.data_ptr(), v
+    else:
+        _result(logits, hidden, shape, dtype, "logits")
+        out, ldo = _result_rows(logits, v, "logits")
+    ws, ws_bytes = _workspace(workspace, lib.flce_mxfp4_logits_workspace_size(n, h), dev)
+    st = lib.flce_mxfp4_logits(rows.data_ptr(), W_DTYPES[hidden.dtype], n, h, ldh,
+                               head.codes.data_ptr(), head.scales.data_ptr(), vp, v, softcap, out,
+                               W_DTYPES[dtype], ldo, ws.data_ptr(), ws_bytes, _stream_handle(dev))
     _check("flce_mxfp4_logits", st)
     return logits
 
@@ -980,22 +1005,26 @@ def beam_select(logits, scores, *, num_select: int | None = None, finished=None,
     if (finished is None) != (eos_token is None):
         raise ValueError("finished and eos_token go together")
     m = k if num_select is None else int(num_select)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return beam_select(logits, scores, num_select=num_select, finished=finished,
+                               eos_token=eos_token, unpadded_vocab=unpadded_vocab,
+                               workspace=workspace)
     rows, _, ld = _rows(logits, vp, "logits")
-    with _on(dev, stream):
-        done = None
-        if finished is not None:
-            _cuda_tensor(finished, (torch.bool, torch.uint8), dev, "finished")
-            if finished.shape != (b, k) or not finished.is_contiguous():
-                raise ValueError("finished must be a contiguous [batch, beams] tensor")
-            done = finished.view(torch.uint8)
-        out = scores.new_empty((b, m))
-        parents = scores.new_empty((b, m), dtype=torch.int64)
-        tokens = scores.new_empty((b, m), dtype=torch.int64)
-        ws, ws_bytes = _workspace(workspace, lib.flce_beam_select_workspace_size(b, k, v, m), dev)
-        st = lib.flce_beam_select(_ptr(rows), W_DTYPES[logits.dtype], b, k, v, ld, _ptr(scores),
-                                  _ptr(done), -1 if eos_token is None else int(eos_token), m,
-                                  _ptr(out), _ptr(parents), _ptr(tokens), _ptr(ws), ws_bytes,
-                                  _stream_handle(dev, stream))
+    done = 0
+    if finished is not None:
+        _cuda_tensor(finished, (torch.bool, torch.uint8), dev, "finished")
+        if finished.shape != (b, k) or not finished.is_contiguous():
+            raise ValueError("finished must be a contiguous [batch, beams] tensor")
+        done = finished.data_ptr()
+    out = scores.new_empty((b, m))
+    parents = scores.new_empty((b, m), dtype=torch.int64)
+    tokens = torch.empty_like(parents)
+    ws, ws_bytes = _workspace(workspace, lib.flce_beam_select_workspace_size(b, k, v, m), dev)
+    st = lib.flce_beam_select(rows.data_ptr(), W_DTYPES[logits.dtype], b, k, v, ld,
+                              scores.data_ptr(), done, -1 if eos_token is None else int(eos_token),
+                              m, out.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
+                              ws.data_ptr(), ws_bytes, _stream_handle(dev))
     _check("flce_beam_select", st)
     return out, parents, tokens
 
@@ -1053,6 +1082,9 @@ def beam_reorder(states, parents, *, length: int | None = None, length_dim: int 
         raise ValueError("parents must be a contiguous int64 [batch, beams] tensor")
     b, k = parents.shape
     dev = parents.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return beam_reorder(states, parents, length=length, length_dim=length_dim, out=out)
     live = []
     last = plan = None  # states of one layout (a model's layers) share its checks
     for src, dst in zip(srcs, dsts):
@@ -1064,10 +1096,10 @@ def beam_reorder(states, parents, *, length: int | None = None, length_dim: int 
         at, to = src.data_ptr(), dst.data_ptr()
         if out is not None and at == to:
             raise ValueError("out must not overlap the states; leave it out to reorder in place")
-        live.append((at, to, *plan))
-    with _on(dev, stream):
-        st = lib.flce_beam_reorder((BeamState * len(live))(*live), len(live), _ptr(parents), b,
-                                   max(k, 1), _stream_handle(dev, stream))
+        live += (at, to, *plan)
+    # flce_beam_state is nine 8-byte fields
+    st = lib.flce_beam_reorder((_c_i64 * len(live))(*live), len(live) // 9, _ptr(parents), b,
+                               max(k, 1), _stream_handle(dev))
     _check("flce_beam_reorder", st)
     return dsts[0] if single else dsts
 

@@ -85,6 +85,12 @@ def test_reorder_bad_arguments(lib):
     assert _reorder(lib, [_state()], batch=0) == 0
 
 
+def test_state_description_is_nine_words():
+    # the binding hands the library an array of 8-byte words
+    assert ctypes.sizeof(flce.BeamState) == 72
+    assert [getattr(flce.BeamState, n).offset for n, _ in flce.BeamState._fields_] == list(range(0, 72, 8))
+
+
 def test_error_word_status(lib):
     assert b"parent" in lib.flce_status_string(flce.FLCE_ERR_BAD_INDEX)
 

@@ -194,6 +194,32 @@ def test_deterministic_other_stream_and_graph(dev):
         assert all(torch.equal(a, c) for a, c in zip((gy, *grads), want))
 
 
+def test_rows_that_must_be_copied(dev):
+    """Leading dimensions without one row stride: copied on the stream the kernel runs on."""
+    x, _, w, b = _inputs(11, 60, 130, torch.bfloat16, torch.float32, dev)
+    t = x.reshape(6, 10, 130).transpose(0, 1)
+    want = flce.layer_norm_forward(t.contiguous(), w, b)
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    for stream in (None, side):
+        got = flce.layer_norm_forward(t, w, b, stream=stream)
+        dx, _, _ = flce.layer_norm_backward(t, t, got[1], got[2], w, stream=stream, want=("dx",))
+        torch.cuda.synchronize(dev)
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
+        assert dx.shape == t.shape
+    with pytest.raises(ValueError, match="one stride"):
+        flce.layer_norm_forward(t.contiguous(), w, b, y=torch.empty_like(x).reshape(6, 10, 130).transpose(0, 1))
+    with pytest.raises(ValueError, match="contiguous"):
+        flce.layer_norm_forward(torch.empty(130, 60, device=dev).t(), w, b)
+
+
+def test_no_second_derivative(dev):
+    x = torch.randn(3, 64, device=dev, requires_grad=True)
+    (g,) = torch.autograd.grad(flce.layer_norm(x).square().sum(), x)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        torch.autograd.grad(flce.layer_norm(x).square().sum(), x, create_graph=True)
+
+
 def test_norm_in_front_of_the_loss(dev):
     """fused_linear_cross_entropy with norm_weight / norm_bias equals the two calls."""
     g = torch.Generator().manual_seed(9)
