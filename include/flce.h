@@ -277,7 +277,8 @@ int flce_ce_backward(const void* logits, int dtype, const int64_t* labels, const
  *                  dbias are [H] in w_dtype, overwritten, summed over the rows
  *                  in FP32 in a fixed order (zeros when N = 0).
  *   workspace      >= flce_layer_norm_workspace_size(N, H) bytes, 16-byte
- *                  aligned; only needed with dweight or dbias.
+ *                  aligned; only needed with dweight or dbias.  Calls that may
+ *                  overlap on the GPU need one each.
  * All arithmetic between the inputs and the one rounding of each output is
  * FP32.  Outputs may not overlap inputs.
  */
@@ -319,8 +320,10 @@ int flce_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int dt
  *   v < V = unpadded_vocab (<= 0: Vp), FP32 accumulation, cap(z) =
  *   softcap * tanh(z / softcap) (0: no cap); hidden [N, H] rows ldh apart is
  *   quantised into the workspace (flce_mxfp4_logits_workspace_size(N, H) bytes,
- *   16-byte aligned); logits [N, V] rows ldo apart in out_dtype.  One token
- *   and many use the same kernel.
+ *   16-byte aligned); logits [N, V] rows ldo apart in out_dtype, any alignment of
+ *   whole elements.  FLCE_ERR_UNSUPPORTED when N or V times the columns pass
+ *   what a tensor map's 32-bit coordinates reach (about 2^31 rows of 256 codes).
+ *   Calls that may overlap on the GPU need workspaces of their own.
  */
 size_t flce_mxfp4_codes_size(int64_t rows, int64_t cols);
 size_t flce_mxfp4_scales_size(int64_t rows, int64_t cols);
@@ -344,17 +347,20 @@ int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n_tokens, int64_t h
  *              FP32 (1), the first vocab entries of it; any alignment of whole
  *              elements.  -inf excludes a token.
  *   scores     FP32 [batch, beams], cumulative log-probabilities.  A beam whose
- *              score is not finite has no candidates (give the beams beyond the
- *              first -inf in the first step); its logits are not read.
+ *              score is not finite has no candidates, finished or not (give the
+ *              beams beyond the first -inf in the first step); its logits are not
+ *              read.
  *   finished   uint8 [batch, beams] or NULL; a non-zero entry's beam has the one
  *              candidate (k, eos_token) with its score unchanged, and its logits
  *              are not read.  eos_token is only looked at with finished.
- *   num_select 1 .. 64, <= beams * vocab; beams 1 .. 64; beams * vocab < 2^31.
+ *   num_select 1 .. 64, <= beams * vocab; beams 1 .. 64; beams * vocab < 2^31 -
+ *              1024.
  *   out_scores FP32, parents and tokens int64, all [batch, num_select].
  *              Candidates with a NaN score (a NaN or +inf in the row) count as
  *              -inf; where fewer than num_select are above -inf, the rest are
  *              the lowest unused k * vocab + v with score -inf.
- *   workspace  >= flce_beam_select_workspace_size(...) bytes, 16-byte aligned.
+ *   workspace  >= flce_beam_select_workspace_size(...) bytes, 16-byte aligned;
+ *              calls that may overlap on the GPU need one each.
  * The logits are read once; sums of exponentials are held in FP32 per thread and
  * FP64 beyond, scores are compared in FP64 and rounded once.
  */

@@ -546,7 +546,7 @@ static BeamPlan plan_beam(int64_t batch, int64_t beams, int64_t vocab, int64_t s
 static bool beam_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t select) {
   return batch >= 0 && beams >= 1 && beams <= kBeamMaxBeams && vocab >= 1 && select >= 1 &&
          select <= kBeamMaxSelect && batch <= kMaxDim / kBeamMaxItems &&
-         vocab <= kMaxDim / kBeamMaxBeams && select <= beams * vocab;
+         vocab <= kMaxDim / beams && select <= beams * vocab;
 }
 
 // ---------------------------------------------------------------- reordering of states
