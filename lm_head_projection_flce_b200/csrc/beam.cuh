@@ -46,6 +46,9 @@ constexpr int kBeamResident = 4;          // blocks per SM the registers are lim
 constexpr int kBeamGroups = 32;           // recorded maxima per thread, at most
 constexpr int kBeamList = 1024;           // elements above the bound that are sorted in one go
 constexpr int64_t kBeamMinSegment = 4096; // elements
+constexpr int kBeamFew = 128;             // candidates that are cheaper to rank than to bound
+constexpr int kBeamCluster = 8;           // blocks per item when one launch does it all
+constexpr int64_t kBeamClusterShare = 16384;  // elements such a block reads, at most
 constexpr int kBeamMaxItems = 4096;       // candidates merged per batch item: K x segments x M
 
 // Total order of (value, index): larger value first, then the lower index; a key
@@ -161,22 +164,23 @@ __device__ __forceinline__ bool beam_is_live(float score) {
   return fabsf(score) <= 3.402823466e38f;  // finite
 }
 
+struct BeamUnitShared {
+  BeamBound bound;
+  uint64_t list[kBeamList];
+  int owners[kBeamMaxSelect];
+  int n_owners, n_list;
+  float red_m[kBeamThreads / 32];
+  double red_s[kBeamThreads / 32];
+};
+
+// Segment `part` of a live beam's row, by a whole block.  `seen`: [groups][threads],
+// the upper half of beam_order(maximum).
 template <typename T>
-__global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_kernel(const BeamPartArgs a) {
+__device__ __forceinline__ void beam_unit(const BeamPartArgs& a, int64_t row, int part,
+                                          BeamUnitShared& sm, uint16_t* seen) {
   constexpr int VN = 16 / int(sizeof(T));
   constexpr uint32_t kNegInf = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-  extern __shared__ uint16_t seen[];  // [groups][threads]: the upper half of beam_order(maximum)
-  __shared__ BeamBound bs;
-  __shared__ uint64_t list[kBeamList];
-  __shared__ int owners[kBeamMaxSelect];
-  __shared__ int n_owners, n_list;
-  __shared__ float red_m[kBeamThreads / 32];
-  __shared__ double red_s[kBeamThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x / a.splits;
-  const int part = int(blockIdx.x - row * a.splits);
-  if (!beam_is_live(a.scores[row]) || (a.finished && a.finished[row])) return;
-  grid_launch_dependents();
   const T* z = static_cast<const T*>(a.logits) + row * a.ld;
   const int64_t begin = int64_t(part) * a.segment, end = min(a.vocab, begin + a.segment);
   const int count = int(max(int64_t(0), (end - begin + VN - 1) / VN));  // vectors
@@ -259,24 +263,24 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
   float bm = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-  if (lane == 0) red_m[warp] = bm;
+  if (lane == 0) sm.red_m[warp] = bm;
   const uint64_t mine = best > -INFINITY ? beam_key(best, best_at) : 0;
-  if (tid == 0) n_owners = n_list = 0;
+  if (tid == 0) sm.n_owners = sm.n_list = 0;
   __syncthreads();
-  bm = red_m[0];
+  bm = sm.red_m[0];
 #pragma unroll
-  for (int w = 1; w < kBeamThreads / 32; ++w) bm = fmaxf(bm, red_m[w]);
+  for (int w = 1; w < kBeamThreads / 32; ++w) bm = fmaxf(bm, sm.red_m[w]);
   double ds = m == -INFINITY ? double(s) : double(s) * double(fast_exp2((m - bm) * kLog2e));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
-  if (lane == 0) red_s[warp] = ds;
+  if (lane == 0) sm.red_s[warp] = ds;
   // Threads' keys are distinct (no two hold the same vector), so at most
   // `select` threads reach the bound.
-  const uint64_t bound = beam_bound(mine, a.select, bs);
-  if (mine != 0 && mine >= bound) owners[atomicAdd(&n_owners, 1)] = tid;  // at most `select`
+  const uint64_t bound = beam_bound(mine, a.select, sm.bound);
+  if (mine != 0 && mine >= bound) sm.owners[atomicAdd(&sm.n_owners, 1)] = tid;  // at most `select`
   if (tid == 0) {
     double t = 0.0;
-    for (int w = 0; w < kBeamThreads / 32; ++w) t += red_s[w];
+    for (int w = 0; w < kBeamThreads / 32; ++w) t += sm.red_s[w];
     const int64_t at = row * a.splits + part;
     a.part_m[at] = bm;
     a.part_s[at] = t;
@@ -287,11 +291,11 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
   const int size = kBeamUnroll << a.group_shift;  // vectors per group
   const int per = (count + kBeamThreads - 1) / kBeamThreads;  // vectors per thread
   const int groups = (per + size - 1) / size;
-  const int work = n_owners * groups;
+  const int work = sm.n_owners * groups;
   const uint32_t least = uint32_t(bound >> 48);
   auto scan = [&](auto&& take) {
     for (int w = tid; w < work; w += kBeamThreads) {
-      const int q = w / groups, g = w - q * groups, owner = owners[q];
+      const int q = w / groups, g = w - q * groups, owner = sm.owners[q];
       // the owner's last group may have no batch, and no record
       if (owner + g * size * kBeamThreads >= count || seen[g * kBeamThreads + owner] < least) continue;
       for (int u0 = 0; u0 < size; u0 += kBeamUnroll) {
@@ -323,11 +327,11 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
     }
   };
   scan([&](uint64_t key) {
-    const int at = atomicAdd(&n_list, 1);
-    if (at < kBeamList) list[at] = key;
+    const int at = atomicAdd(&sm.n_list, 1);
+    if (at < kBeamList) sm.list[at] = key;
   });
   __syncthreads();
-  const int n = n_list;
+  const int n = sm.n_list;
   const int64_t out = (row * a.splits + part) * a.select;
   auto put = [&](int slot, uint64_t key) {
     a.cand_z[out + slot] = beam_value(uint32_t(key >> 32));
@@ -337,10 +341,10 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
     // The list's order is that of the atomics; the keys are distinct, so their
     // ranks are not.
     for (int i = tid; i < n; i += kBeamThreads) {
-      const uint64_t key = list[i];
+      const uint64_t key = sm.list[i];
       int r = 0;
 #pragma unroll 4
-      for (int j = 0; j < n; ++j) r += list[j] > key ? 1 : 0;
+      for (int j = 0; j < n; ++j) r += sm.list[j] > key ? 1 : 0;
       if (r < a.select) put(r, key);
     }
     for (int i = n + tid; i < a.select; i += kBeamThreads) a.cand_v[out + i] = -1;
@@ -355,15 +359,25 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_ker
       if (key < last && key > top) top = key;
     });
     __syncthreads();
-    bs.keys[tid] = top;
+    sm.bound.keys[tid] = top;
     __syncthreads();
     for (int h = kBeamThreads / 2; h > 0; h >>= 1) {
-      if (tid < h) bs.keys[tid] = max(bs.keys[tid], bs.keys[tid + h]);
+      if (tid < h) sm.bound.keys[tid] = max(sm.bound.keys[tid], sm.bound.keys[tid + h]);
       __syncthreads();
     }
-    last = bs.keys[0];  // never 0: more than kBeamList >= select elements qualify
+    last = sm.bound.keys[0];  // never 0: more than kBeamList >= select elements qualify
     if (tid == 0) put(slot, last);
   }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads, kBeamResident) beam_partials_kernel(const BeamPartArgs a) {
+  extern __shared__ uint64_t dyn[];
+  __shared__ BeamUnitShared sm;
+  const int64_t row = blockIdx.x / a.splits;
+  if (!beam_is_live(a.scores[row]) || (a.finished && a.finished[row])) return;
+  grid_launch_dependents();
+  beam_unit<T>(a, row, int(blockIdx.x - row * a.splits), sm, reinterpret_cast<uint16_t*>(dyn));
 }
 
 struct BeamMergeArgs {
@@ -390,13 +404,16 @@ __device__ __forceinline__ double beam_value64(uint64_t o) {
   return __longlong_as_double(static_cast<long long>((o >> 63) ? (o & ~(uint64_t(1) << 63)) : ~o));
 }
 
-// One block per batch item.
-__global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMergeArgs a) {
-  extern __shared__ uint64_t dyn[];
-  __shared__ BeamBound bs;
-  __shared__ double lse[kBeamMaxBeams];
-  __shared__ int n_list;
-  __shared__ uint32_t chosen[kBeamMaxSelect];
+struct BeamMergeShared {
+  BeamBound bound;
+  double lse[kBeamMaxBeams];
+  int n_list;
+  uint32_t chosen[kBeamMaxSelect];
+};
+
+// Batch item b, by a whole block; dyn: 24 bytes per candidate.
+__device__ __forceinline__ void beam_merge_item(const BeamMergeArgs& a, int64_t b,
+                                                BeamMergeShared& sm, uint64_t* dyn) {
   constexpr int kAhead = 4;  // items per thread loaded before the sums are known
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // Item i is candidate i / lists of list i % lists: the lists are sorted, and dealt
@@ -408,12 +425,10 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
   uint32_t* idx = reinterpret_cast<uint32_t*>(tot + items);  // [items]
   uint32_t* sel_i = idx + items;                             // [items]: what is above the bound
   uint64_t* sel_t = reinterpret_cast<uint64_t*>(sel_i + items);  // 16 bytes per item behind tot
-  const int64_t b = blockIdx.x;
   const float* scores = a.scores + b * a.beams;
   const uint8_t* finished = a.finished ? a.finished + b * a.beams : nullptr;
   const int64_t at0 = b * items;
   auto place = [&](int i) { return (i % lists) * a.select + i / lists; };
-  grid_dependency_wait();
   float az[kAhead];
   int av[kAhead];
 #pragma unroll
@@ -423,7 +438,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
     az[u] = i < items ? a.cand_z[at0 + place(i)] : 0.0f;
     av[u] = i < items ? a.cand_v[at0 + place(i)] : -1;
   }
-  if (tid == 0) n_list = 0;
+  if (tid == 0) sm.n_list = 0;
   const double ninf = -static_cast<double>(INFINITY);
   for (int k = warp; k < a.beams; k += kBeamThreads / 32) {
     const int64_t at = (b * a.beams + k) * a.splits;
@@ -445,7 +460,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) lse[k] = double(m) + log(s);
+    if (lane == 0) sm.lse[k] = double(m) + log(s);
   }
   __syncthreads();
 
@@ -459,7 +474,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
         v = int(a.eos);
         if (i == k * a.splits) t = double(s);
       } else if (v >= 0) {
-        t = double(s) + double(z) - lse[k];
+        t = double(s) + double(z) - sm.lse[k];
       }
     }
     const uint64_t o = t > ninf ? beam_order64(t) : 0;  // NaN and -inf: none
@@ -472,15 +487,20 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
     if (tid + u * kBeamThreads < items) item(tid + u * kBeamThreads, az[u], av[u]);
   for (int i = tid + kAhead * kBeamThreads; i < items; i += kBeamThreads)
     item(i, a.cand_z[at0 + place(i)], a.cand_v[at0 + place(i)]);
-  const uint64_t bound = beam_bound(top, a.select, bs);
+  // Up to kBeamFew candidates are ranked as they are.
+  uint64_t bound = 0;
+  if (items > kBeamFew)  // the same for the whole block
+    bound = beam_bound(top, a.select, sm.bound);
+  else
+    __syncthreads();
   for (int i = tid; i < items; i += kBeamThreads)
     if (tot[i] != 0 && tot[i] >= bound) {
-      const int at = atomicAdd(&n_list, 1);
+      const int at = atomicAdd(&sm.n_list, 1);
       sel_t[at] = tot[i];
       sel_i[at] = idx[i];
     }
   __syncthreads();
-  const int n = n_list;
+  const int n = sm.n_list;
   for (int i = tid; i < n; i += kBeamThreads) {
     const uint64_t t = sel_t[i];
     const uint32_t f = sel_i[i];
@@ -495,7 +515,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
       a.out_scores[at] = float(beam_value64(t));
       a.parents[at] = int64_t(f / vocab);
       a.tokens[at] = int64_t(f % vocab);
-      chosen[r] = f;
+      sm.chosen[r] = f;
     }
   }
   __syncthreads();
@@ -503,7 +523,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
     uint32_t f = 0;
     for (int r = n; r < a.select; ++r, ++f) {
       for (int j = 0; j < n; ++j)
-        if (chosen[j] == f) {
+        if (sm.chosen[j] == f) {
           ++f;
           j = -1;
         }
@@ -515,7 +535,39 @@ __global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMerg
   }
 }
 
+// One block per batch item.
+__global__ void __launch_bounds__(kBeamThreads) beam_merge_kernel(const BeamMergeArgs a) {
+  extern __shared__ uint64_t dyn[];
+  __shared__ BeamMergeShared sm;
+  grid_dependency_wait();
+  beam_merge_item(a, blockIdx.x, sm, dyn);
+}
+
+// Few items with little to read: a cluster of blocks per item, a segment each, and the
+// first block merges them once all have arrived at the cluster's barrier: one launch.
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads, 1)
+    beam_cluster_kernel(const BeamPartArgs a, const BeamMergeArgs g) {
+  extern __shared__ uint64_t dyn[];
+  __shared__ union {
+    BeamUnitShared unit;
+    BeamMergeShared merge;
+  } sm;
+  const int64_t b = blockIdx.x / kBeamCluster;
+  const uint32_t rank = cluster_cta_rank();
+  for (int u = int(rank); u < g.beams * a.splits; u += kBeamCluster) {
+    const int k = u / a.splits;
+    const int64_t row = b * g.beams + k;
+    if (beam_is_live(a.scores[row]) && !(a.finished && a.finished[row]))
+      beam_unit<T>(a, row, u - k * a.splits, sm.unit, reinterpret_cast<uint16_t*>(dyn));
+    __syncthreads();  // the next segment uses the same shared memory
+  }
+  cluster_sync_all();  // the other blocks' partials are written
+  if (rank == 0) beam_merge_item(g, b, sm.merge, dyn);
+}
+
 struct BeamPlan {
+  bool cluster;
   int splits;
   int64_t segment;
   size_t off_s, off_m, off_z, off_v, total;
@@ -531,6 +583,16 @@ static BeamPlan plan_beam(int64_t batch, int64_t beams, int64_t vocab, int64_t s
   int64_t s = std::max<int64_t>(1, int64_t(kBeamResident) * kLnSms / rows);
   s = std::min({s, std::max<int64_t>(1, vocab / kBeamMinSegment),
                 std::max<int64_t>(1, kBeamMaxItems / (beams * select))});
+  // A cluster per item while all of them fit at once and each of its blocks has at most
+  // one segment to read, and a short one (14 x 1 beam x 31398 FP32: 16.8 us per call
+  // and 9.9 on the device in one launch, 18.3 and 10.7 in two; with two segments per
+  // block 22.5 against 18.1 us per call, with 65536 elements per block 14.2 against
+  // 10.8 us on the device).
+  p.cluster = batch * kBeamCluster <= kLnSms && beams <= kBeamCluster &&
+              beams * vocab <= kBeamCluster * kBeamClusterShare;
+  if (p.cluster)
+    s = std::min<int64_t>({kBeamCluster / beams, std::max<int64_t>(1, vocab / kBeamMinSegment),
+                           std::max<int64_t>(1, kBeamMaxItems / (beams * select))});
   p.segment = cdiv(cdiv(vocab, s), 8) * 8;
   p.splits = int(cdiv(vocab, p.segment));
   const size_t units = size_t(rows) * size_t(p.splits);
@@ -541,6 +603,30 @@ static BeamPlan plan_beam(int64_t batch, int64_t beams, int64_t vocab, int64_t s
   p.off_v = o;  o = align_up(o + units * size_t(select) * 4);
   p.total = o;
   return p;
+}
+
+template <typename T>
+static int beam_launch_cluster(const BeamPartArgs& a, const BeamMergeArgs& g, int64_t batch,
+                               size_t smem, cudaStream_t cs) {
+  auto kern = beam_cluster_kernel<T>;
+  if (smem > 32 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBeamMaxItems * 24) !=
+          cudaSuccess)
+    return FLCE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(batch * kBeamCluster));
+  cfg.blockDim = dim3(kBeamThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = cs;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kBeamCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, a, g) != cudaSuccess) return FLCE_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 
 static bool beam_sizes_ok(int64_t batch, int64_t beams, int64_t vocab, int64_t select) {
@@ -657,19 +743,6 @@ extern "C" int flce_beam_select(const void* logits, int dtype, int64_t batch, in
   a.part_m = reinterpret_cast<float*>(ws + p.off_m);
   a.cand_z = reinterpret_cast<float*>(ws + p.off_z);
   a.cand_v = reinterpret_cast<int*>(ws + p.off_v);
-  {
-    LaunchScope scope(KF_BEAM_PART, 0.0, double(rows) * double(vocab) * (dtype == FLCE_F32 ? 4 : 2), cs);
-    const unsigned grid = unsigned(rows * p.splits);
-    const int64_t batches = cdiv(p.segment, int64_t(kBeamUnroll) * kBeamThreads * (dtype == FLCE_F32 ? 4 : 8));
-    while (cdiv(batches, int64_t(1) << a.group_shift) > kBeamGroups) ++a.group_shift;
-    const size_t seen =
-        size_t(cdiv(batches, int64_t(1) << a.group_shift)) * kBeamThreads * sizeof(uint16_t);
-    if (dtype == FLCE_BF16)
-      beam_partials_kernel<__nv_bfloat16><<<grid, kBeamThreads, seen, cs>>>(a);
-    else
-      beam_partials_kernel<float><<<grid, kBeamThreads, seen, cs>>>(a);
-  }
-  if (cudaGetLastError() != cudaSuccess) return FLCE_ERR_CUDA;
   BeamMergeArgs g{};
   g.beams = int(beams);
   g.splits = p.splits;
@@ -686,6 +759,25 @@ extern "C" int flce_beam_select(const void* logits, int dtype, int64_t batch, in
   g.parents = parents;
   g.tokens = tokens;
   const size_t smem = size_t(beams) * size_t(p.splits) * size_t(num_select) * 24;
+  const int64_t batches = cdiv(p.segment, int64_t(kBeamUnroll) * kBeamThreads * (dtype == FLCE_F32 ? 4 : 8));
+  while (cdiv(batches, int64_t(1) << a.group_shift) > kBeamGroups) ++a.group_shift;
+  const size_t seen =
+      size_t(cdiv(batches, int64_t(1) << a.group_shift)) * kBeamThreads * sizeof(uint16_t);
+  const double bytes = double(rows) * double(vocab) * (dtype == FLCE_F32 ? 4 : 2);
+  if (p.cluster) {
+    LaunchScope scope(KF_BEAM_PART, 0.0, bytes, cs);
+    return dtype == FLCE_BF16 ? beam_launch_cluster<__nv_bfloat16>(a, g, batch, std::max(seen, smem), cs)
+                              : beam_launch_cluster<float>(a, g, batch, std::max(seen, smem), cs);
+  }
+  {
+    LaunchScope scope(KF_BEAM_PART, 0.0, bytes, cs);
+    const unsigned grid = unsigned(rows * p.splits);
+    if (dtype == FLCE_BF16)
+      beam_partials_kernel<__nv_bfloat16><<<grid, kBeamThreads, seen, cs>>>(a);
+    else
+      beam_partials_kernel<float><<<grid, kBeamThreads, seen, cs>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return FLCE_ERR_CUDA;
+  }
   if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kBeamMaxItems * 24) != cudaSuccess)
