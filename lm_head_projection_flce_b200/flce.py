@@ -1045,8 +1045,12 @@ def _reorder_plan(dtype, shape, stride, device, to_dtype, to_shape, into, to_dev
         if n > 1 and (stride[i] * e != inner or into[i] * e != inner):
             raise ValueError("states must be contiguous behind [batch, beams]")
         inner *= n
-    if (b > 1 and into[0] == 0) or (k > 1 and into[1] == 0):
-        raise ValueError("a state's beams must not share memory")
+    extent = inner
+    for step, n in sorted(((into[0] * e, b), (into[1] * e, k))):
+        if n > 1:
+            if step < extent:
+                raise ValueError("a state's beams must not share memory")
+            extent += step * (n - 1)
     if length is not None:
         if not 2 <= length_dim < len(shape) or not 0 <= length <= shape[length_dim]:
             raise ValueError("length must lie within the states' length_dim")
@@ -1132,8 +1136,9 @@ class CapturedBeamStep:
             raise ValueError("states follow as many beams as there are: num_select must be beams")
         dev = hidden.device
         self.hidden = hidden.detach().clone(memory_format=torch.contiguous_format)
-        self.scores = scores.clone()
-        self.finished = None if finished is None else finished.clone()
+        self.scores = scores.detach().clone(memory_format=torch.contiguous_format)
+        self.finished = (None if finished is None
+                         else finished.clone(memory_format=torch.contiguous_format))
         self.head, self.norm, self.states = head, (norm_weight, norm_bias, norm_eps), states
         self.kw = dict(softcap=softcap, unpadded_vocab=unpadded_vocab, dtype=dtype)
         self.select = dict(num_select=num_select, finished=self.finished, eos_token=eos_token)

@@ -105,3 +105,21 @@ def test_binding_refuses():
         flce.beam_reorder(torch.zeros(1, 2, 3), torch.zeros(1, 2, dtype=torch.int64))
     with pytest.raises(TypeError):
         flce.beam_reorder(torch.zeros(1, 2, 3), torch.zeros(1, 2))
+
+
+@pytest.mark.parametrize("stride", [(0, 6, 1), (12, 0, 1), (12, 5, 1), (10, 6, 1), (6, 6, 1), (3, 12, 1)])
+def test_binding_refuses_beams_that_share_memory(stride):
+    """[2, 2, 6] entries of which two overlap, wholly or in part."""
+    with pytest.raises(ValueError, match="share memory"):
+        flce._reorder_plan(torch.float32, (2, 2, 6), stride, "d", torch.float32, (2, 2, 6), stride, "d",
+                           2, 2, "d", None, 2)
+
+
+@pytest.mark.parametrize("stride", [(12, 6, 1), (6, 12, 1), (18, 6, 1), (7, 14, 1), (100, 6, 1)])
+def test_binding_takes_beams_in_any_order(stride):
+    plan = flce._reorder_plan(torch.float32, (2, 2, 6), stride, "d", torch.float32, (2, 2, 6), stride, "d",
+                              2, 2, "d", None, 2)
+    assert plan == (4 * stride[0], 4 * stride[1], 4 * stride[0], 4 * stride[1], 1, 0, 24)
+    # one beam: its stride does not matter
+    assert flce._reorder_plan(torch.float32, (2, 1, 6), (6, 0, 1), "d", torch.float32, (2, 1, 6), (6, 0, 1),
+                              "d", 2, 1, "d", None, 2) is not None

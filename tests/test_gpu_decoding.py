@@ -121,6 +121,21 @@ def test_captured_step_refusals(dev):
         step.set_inputs(hidden=hidden[:, :1])
 
 
+def test_captured_step_owns_its_inputs(dev):
+    """Scores that carry a gradient or lie transposed are copied as plain rows."""
+    embed, mix, w, b, head, start = _problem(dev)
+    q = flce.mxfp4_quantize(head)
+    hidden = _grid(start[:, None, :].repeat(1, K, 1))
+    scores = -torch.arange(float(B * K), device=dev).view(K, B).t()
+    done = torch.zeros(K, B, dtype=torch.bool, device=dev).t()
+    step = flce.CapturedBeamStep(hidden, q, scores.clone().requires_grad_(), finished=done, eos_token=EOS)
+    assert not step.scores.requires_grad and step.scores.is_contiguous() and step.finished.is_contiguous()
+    step.set_inputs(scores=scores, finished=done)
+    want = flce.beam_select(flce.mxfp4_logits(hidden, q), scores.contiguous(), finished=done.contiguous(),
+                            eos_token=EOS)
+    assert all(torch.equal(x, y) for x, y in zip(step.replay(), want))
+
+
 def test_training_step_gradients_against_differences(dev):
     """norm -> loss: the gradients of the norm's parameters against differences of the 64-bit loss."""
     g = torch.Generator().manual_seed(23)
