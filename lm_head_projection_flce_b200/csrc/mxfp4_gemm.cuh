@@ -56,7 +56,7 @@ struct MxGemmArgs {
   float softcap, inv_softcap;
   void* out;
   int64_t ldo;
-  int v4, v8;         // rows of logits start on 16, on 32 bytes
+  int v8;             // all rows of logits start on 32 bytes
   unsigned* err;
   uint64_t timeout_ns;
 };
@@ -123,6 +123,51 @@ __host__ __device__ constexpr uint32_t mma_idesc_mxf4(int m, int n) {
 __device__ __forceinline__ uint64_t mx_scale_desc(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(1) << 16) |
          (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// c tanh(z / c) of a thread's 32 values, to a few units in the last place of FP32.  With
+// x = z / c and |x| <= 5/8 it is z + z t(x^2), t the odd series' tail as a polynomial
+// of five terms fitted for the least largest relative error (4e-9), and no special
+// function; beyond, c - 2c / (exp(2 |x|) + 1) with z's sign.  A warp whose values are
+// all small, as most logits of a cap are, skips the second: 1024 x 4096 x 65536 takes
+// 109 us then, as without a cap, and 129 us with large values (tanhf for every
+// value: 130 us either way).  One reciprocal for two values gained nothing.
+__device__ __forceinline__ void mx_softcap(float (&z)[32], float c, float inv_c) {
+  constexpr float kSmall = 0.625f;
+  float top = 0.0f;  // a NaN passes through either branch
+#pragma unroll
+  for (int j = 0; j < 32; ++j) top = fmaxf(top, fabsf(z[j]));
+  const bool small = __all_sync(0xffffffffu, top * inv_c <= kSmall) != 0;
+  auto both = [](float v) { return make_float2(v, v); };
+  auto series = [&](float2 v, float2 x) {
+    const float2 u = __fmul2_rn(x, x);
+    float2 t = __ffma2_rn(both(-0.00570497848f), u, both(0.0206390787f));
+    t = __ffma2_rn(t, u, both(-0.0537397116f));
+    t = __ffma2_rn(t, u, both(0.133314416f));
+    t = __ffma2_rn(t, u, both(-0.333332807f));
+    return __ffma2_rn(__fmul2_rn(t, u), v, v);
+  };
+  if (small) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float2 v = make_float2(z[j], z[j + 1]);
+      const float2 y = series(v, __fmul2_rn(v, both(inv_c)));
+      z[j] = y.x;
+      z[j + 1] = y.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float2 v = make_float2(z[j], z[j + 1]), x = __fmul2_rn(v, both(inv_c));
+      const float2 y = series(v, x);
+      auto large = [&](float xi, float yi) {
+        const float r = fast_rcp(fast_exp2(fabsf(xi) * (2.0f * kLog2e)) + 1.0f);
+        return fabsf(xi) <= kSmall ? yi : copysignf(fmaf(-2.0f * c, r, c), xi);
+      };
+      z[j] = large(x.x, y.x);
+      z[j + 1] = large(x.y, y.y);
+    }
+  }
 }
 
 __host__ __device__ __forceinline__ int mxg_scale_tiles(int tile_n) { return tile_n > 128 ? 2 : 1; }
@@ -376,11 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c0 = 0; c0 < cols; c0 += 32) {
         float x[32];
         tmem_load_32cols(taddr + c0, x);
-        if (!live) continue;  // the load above is for the whole warp
-        if (capped) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = g.softcap * tanhf(x[j] * g.inv_softcap);
-        }
+        if (capped) mx_softcap(x, g.softcap, g.inv_softcap);
+        if (!live) continue;  // what is above is for the whole warp
         TO* out = static_cast<TO*>(g.out) + (n0 + c0) * g.ldo + row;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
@@ -450,21 +492,87 @@ __device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d, uint64_t a, uint64_
       : "memory");
 }
 
-// Exchanges rows and columns of a 32 x 32 block that a warp holds a row per lane.
-__device__ __forceinline__ void warp_transpose(float (&x)[32]) {
-  const int lane = threadIdx.x & 31;
+// `bytes` (< 32) of the words at `to`, 16-byte aligned, in pieces of 16, 8, 4 and 2.
+__device__ __forceinline__ void store_pieces(uint8_t* to, const uint32_t (&w)[8], int bytes) {
+  const bool b16 = (bytes & 16) != 0, b8 = (bytes & 8) != 0, b4 = (bytes & 4) != 0;
+  if (b16) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+  uint32_t v[4], u[2];
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
-    const bool upper = (lane & s) != 0;
+  for (int i = 0; i < 4; ++i) v[i] = b16 ? w[i + 4] : w[i];
+  to += bytes & 16;
+  if (b8) *reinterpret_cast<uint2*>(to) = make_uint2(v[0], v[1]);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (i & s) continue;
-      const float got = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[i + s], s);
-      if (upper)
-        x[i] = got;
-      else
-        x[i + s] = got;
+  for (int i = 0; i < 2; ++i) u[i] = b8 ? v[i + 2] : v[i];
+  to += bytes & 8;
+  if (b4) *reinterpret_cast<uint32_t*>(to) = u[0];
+  to += bytes & 4;
+  if (bytes & 2) *reinterpret_cast<uint16_t*>(to) = uint16_t(b4 ? u[1] : u[0]);
+}
+// `count` (<= 128) consecutive logits of a row at any alignment, from one thread: up to
+// the first 32-byte boundary in pieces of 1, 2, 4 and 8 elements, each aligned to its
+// size, then 32 bytes at a time, cut out of the words around them by a shift of 4, 2
+// and 1 words, and the end in pieces again.  (Blocks of 32 x 32 transposed by
+// shuffles, so that the lanes' 2-byte stores were consecutive, took a 1561 x 104 x
+// 25615 product 87 us against 41.)
+template <typename TO>
+__device__ __forceinline__ void store_run(TO* out, const float (&x)[4][32], int count) {
+  constexpr int kWords = 32 * int(sizeof(TO)), kPer = 32 / int(sizeof(TO));  // elements in 32 bytes
+  if (count < kPer) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const float one[1] = {x[0][j]};
+      if (j < count) LnIo<TO, 1>::store(out + j, one);
     }
+    return;
+  }
+  uint32_t w[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    if constexpr (sizeof(TO) == 4)
+      w[i] = __float_as_uint(x[i / 32][i % 32]);
+    else
+      w[i] = pack_bf16x2(x[i / 16][2 * i % 32], x[i / 16][2 * i % 32 + 1]);
+  }
+  uint8_t* at = reinterpret_cast<uint8_t*>(out);
+  const uint32_t head = (32u - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(out)) & 31u)) & 31u;
+  const bool b4 = (head & 4u) != 0, b8 = (head & 8u) != 0, b16 = (head & 16u) != 0;
+  if constexpr (sizeof(TO) == 2) {
+    if (head & 2u) *reinterpret_cast<uint16_t*>(at) = uint16_t(w[0]);
+    at += head & 2u;
+    const uint32_t sh = (head & 2u) * 8u;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(w[i], i + 1 < kWords ? w[i + 1] : 0u, sh);
+  }
+  {
+    uint32_t v[6], u[4];
+    if (b4) *reinterpret_cast<uint32_t*>(at) = w[0];
+    at += head & 4u;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = b4 ? w[i + 1] : w[i];
+    if (b8) *reinterpret_cast<uint2*>(at) = make_uint2(v[0], v[1]);
+    at += head & 8u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = b8 ? v[i + 2] : v[i];
+    if (b16) *reinterpret_cast<uint4*>(at) = make_uint4(u[0], u[1], u[2], u[3]);
+    at += head & 16u;
+  }
+  int left = count * int(sizeof(TO)) - int(head);  // bytes
+#pragma unroll
+  for (int k = 0; k < kWords; k += 8) {
+    auto word = [&](int i) { return k + i < kWords ? w[(k + i) % kWords] : 0u; };
+    uint32_t v[11], u[9], e[8];
+#pragma unroll
+    for (int i = 0; i < 11; ++i) v[i] = b16 ? word(i + 4) : word(i);
+#pragma unroll
+    for (int i = 0; i < 9; ++i) u[i] = b8 ? v[i + 2] : v[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = b4 ? u[i + 1] : u[i];
+    if (left >= 32)
+      st_global_v8(at, e[0], e[1], e[2], e[3], e[4], e[5], e[6], e[7]);
+    else if (left > 0)
+      store_pieces(at, e, left);
+    at += 32;
+    left -= 32;
   }
 }
 
@@ -663,57 +771,31 @@ __global__ void __launch_bounds__(kMxpThreads, 1)
       if (lane == 0) mbar_arrive_cluster(leader_tempty);
       const int64_t row = (2 * mt + rank) * kMxgM + quarter * 32 + lane;
       const int64_t c0 = nt * kMxpN + half * 128;
-      if (!g.v4) {
-        // Rows of logits at any alignment: lanes take turns with the tokens, so that a
-        // store covers 32 consecutive logits of one token.
-        const int rows = int(min(int64_t(32), g.rows_m - (row - lane)));
+      if (capped) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t c = c0 + 32 * q + lane;
-          if (c - lane >= g.rows_n) break;  // the same for the whole warp
-          if (capped) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[q][j] = g.softcap * tanhf(x[q][j] * g.inv_softcap);
-          }
-          warp_transpose(x[q]);
-          TO* out = static_cast<TO*>(g.out) + (row - lane) * g.ldo + c;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float one[1] = {x[q][j]};
-            if (j < rows && c < g.rows_n) LnIo<TO, 1>::store(out + int64_t(j) * g.ldo, one);
-          }
-        }
-        continue;
+        for (int q = 0; q < 4; ++q) mx_softcap(x[q], g.softcap, g.inv_softcap);
       }
-      if (row >= g.rows_m) continue;
+      if (row >= g.rows_m || c0 >= g.rows_n) continue;
       // 128 consecutive logits of a token
       TO* out = static_cast<TO*>(g.out) + row * g.ldo + c0;
+      if (!g.v8) {
+        store_run(out, x, int(min(int64_t(128), g.rows_n - c0)));
+        continue;
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int64_t left = g.rows_n - (c0 + 32 * q);
         if (left <= 0) break;
-        if (capped) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[q][j] = g.softcap * tanhf(x[q][j] * g.inv_softcap);
-        }
         if (left >= 32) {
           if constexpr (sizeof(TO) == 2) {
-            store_bf16x32(reinterpret_cast<uint4*>(out + 32 * q), x[q], g.v8 != 0);
+            store_bf16x32(reinterpret_cast<uint4*>(out + 32 * q), x[q], true);
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              if (g.v8) {
-                st_global_v8(out + 32 * q + j, __float_as_uint(x[q][j]), __float_as_uint(x[q][j + 1]),
-                             __float_as_uint(x[q][j + 2]), __float_as_uint(x[q][j + 3]),
-                             __float_as_uint(x[q][j + 4]), __float_as_uint(x[q][j + 5]),
-                             __float_as_uint(x[q][j + 6]), __float_as_uint(x[q][j + 7]));
-              } else {
-                *reinterpret_cast<float4*>(out + 32 * q + j) =
-                    make_float4(x[q][j], x[q][j + 1], x[q][j + 2], x[q][j + 3]);
-                *reinterpret_cast<float4*>(out + 32 * q + j + 4) =
-                    make_float4(x[q][j + 4], x[q][j + 5], x[q][j + 6], x[q][j + 7]);
-              }
-            }
+            for (int j = 0; j < 32; j += 8)
+              st_global_v8(out + 32 * q + j, __float_as_uint(x[q][j]), __float_as_uint(x[q][j + 1]),
+                           __float_as_uint(x[q][j + 2]), __float_as_uint(x[q][j + 3]),
+                           __float_as_uint(x[q][j + 4]), __float_as_uint(x[q][j + 5]),
+                           __float_as_uint(x[q][j + 6]), __float_as_uint(x[q][j + 7]));
           }
         } else {
 #pragma unroll
@@ -858,7 +940,6 @@ extern "C" int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n, int64
   g.inv_softcap = softcap > 0.0f ? 1.0f / softcap : 0.0f;
   g.out = logits;
   g.ldo = ld;
-  g.v4 = aligned(logits, 16) && (ld * esz) % 16 == 0;
   g.v8 = aligned(logits, 32) && (ld * esz) % 32 == 0;
   g.err = dev->err;
   g.timeout_ns = kDefaultTimeoutNs;

@@ -181,3 +181,55 @@ def test_loss_of_the_quantised_head(dev):
     top = z.max(axis=1)
     ref = top + np.log(np.exp(z - top[:, None]).sum(axis=1))
     assert np.max(np.abs(_np(lse) - ref)) <= 2e-3
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("v,pad", [(v, p) for v in (1, 7, 15, 16, 17, 100, 128, 129, 250, 257, 400)
+                                   for p in (0, 1, 3)] + [(384, p) for p in range(16)])
+def test_logits_rows_of_every_alignment_and_end(dev, v, pad, out):
+    """The many-token kernel's stores: runs that start and end anywhere, nothing beside them."""
+    n, h = 200, 64
+    g = torch.Generator().manual_seed(v + pad)
+    hidden = torch.randn(n, h, generator=g)
+    weight = torch.randn(v, h, generator=g)
+    head = flce.mxfp4_quantize(weight.to(dev))
+    buf = torch.full((n * (v + pad) + 40,), 7.0, dtype=out, device=dev)
+    at = pad % 5
+    rows = buf[at:at + n * (v + pad)].view(n, v + pad)
+    flce.mxfp4_logits(hidden.to(dev), head, dtype=out, logits=rows[:, :v])
+    _check_logits(hidden, weight, rows[:, :v], 0.0)
+    assert torch.all(rows[:, v:] == 7.0) and torch.all(buf[:at] == 7.0)
+    assert torch.all(buf[at + n * (v + pad):] == 7.0)
+
+
+@pytest.mark.parametrize("n", [3, 300])
+@pytest.mark.parametrize("v", [300, 304])
+@pytest.mark.parametrize("cap", [1e-3, 0.5, 20.0, 30.0, 1e6])
+def test_softcap_small_and_large_values(dev, n, v, cap):
+    """The cap's value itself: of the uncapped logits in FP32 it is off by the rounding of a few
+    operations (their errors sum to 4 units of 2^-24 on the series' side, 7 beyond: exp2
+    and the reciprocal to 2^-22, each times at most 0.35, and four roundings)."""
+    g = torch.Generator().manual_seed(n + v)
+    hidden = torch.randn(n, 96, generator=g).to(dev)
+    weight = torch.randn(v, 96, generator=g) * torch.logspace(-4, 2, v)[:, None]
+    head = flce.mxfp4_quantize(weight.to(dev))
+    z = flce.mxfp4_logits(hidden, head, dtype=torch.float32).double()
+    got = flce.mxfp4_logits(hidden, head, dtype=torch.float32, softcap=cap)
+    want = cap * torch.tanh(z / cap)
+    err = (got.double() - want).abs()
+    assert torch.all(err <= 8 * 2.0 ** -24 * want.abs()), float((err / want.abs()).nan_to_num().max() * 2 ** 24)
+    assert torch.equal(got.sign(), z.float().sign())
+    low = flce.mxfp4_logits(hidden, head, softcap=cap)
+    assert torch.equal(low, got.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("n", [3, 300])
+def test_softcap_of_nan(dev, n):
+    g = torch.Generator().manual_seed(n)
+    hidden, weight = torch.randn(n, 64, generator=g), torch.randn(200, 64, generator=g)
+    hidden[1, 5] = float("nan")
+    weight[150, 40] = float("inf")
+    z = flce.mxfp4_logits(hidden.to(dev), flce.mxfp4_quantize(weight.to(dev)), dtype=torch.float32, softcap=5.0)
+    bad = torch.zeros(n, 200, dtype=torch.bool, device=dev)
+    bad[1], bad[:, 150] = True, True
+    assert torch.equal(z.isnan(), bad)
