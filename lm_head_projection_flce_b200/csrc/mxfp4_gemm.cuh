@@ -20,8 +20,10 @@
 // bulk copy.  Warp 1 copies the stage's scales to tensor memory (tcgen05.cp, 32
 // lanes x 16 bytes replicated to the four lane quarters) and issues the MMAs; both
 // run in issue order, and each stage has scale columns of its own, rewritten only
-// after the MMAs that read them completed (the stage's empty barrier).  Warps 2..5
-// store the accumulator, of which there are two.  Every wait is bounded.
+// after the MMAs that read them completed (the stage's empty barrier).  Warps 2..9
+// store the accumulator, of which there are two, every other 32 tokens each (with
+// four warps 142 tokens x 512 x 69658 took 26 us against 20: a warp per scheduler
+// waits for its own instructions).  Every wait is bounded.
 //
 // Measured on one B200: 8 tokens x 4096 x 128256 in 49 us with the quantisation of
 // the tokens (5.8 TB/s, 89% of the copy bandwidth; without the product's
@@ -39,6 +41,8 @@ constexpr int kMxgKBytes = 128;        // bytes of codes per row and stage
 constexpr int kMxgBlocks = 8;          // scale blocks (256 elements) per stage
 constexpr int kMxgM = 128;             // rows on the M side of a tile
 constexpr int kMxgMaxN = 192;          // on the N side: two accumulators and the scales fit
+constexpr int kMxgEpiWarps = 8;
+constexpr int kMxgThreads = 64 + 32 * kMxgEpiWarps;
 constexpr int kMxgMaxStages = 12;
 constexpr int kMxgSmem = 225 * 1024;   // shared memory for the stages
 
@@ -179,7 +183,7 @@ __host__ __device__ __forceinline__ uint32_t mxg_stage_bytes(int tile_n) {
 
 // kSft: scale tiles of 128 rows that a tile's N side touches (2 above 128 rows).
 template <typename TO, int kSft>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kMxgThreads, 1)
     mx_gemm_kernel(const MxGemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kMxgMaxStages + 5];
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), kEpiWarps);
+      mbar_init(tempty_bar(a), kMxgEpiWarps);
     }
     mbar_init(drain_bar, 1);
     ctl->abort = 0;
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // -------------------------------------------------- epilogue: lanes are M rows
     grid_dependency_wait();  // before anything is stored
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, half = (warp - 2) >> 2;  // every other 32 columns
     int acc = 0;
     uint32_t acc_ph = 0;
     const bool capped = g.softcap > 0.0f;
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cols = int(min(int64_t(g.tile_n), g.rows_n - n0));
       const uint32_t taddr =
           tmem + (static_cast<uint32_t>(quarter * 32) << 16) + uint32_t(acc) * uint32_t(g.tile_n);
-      for (int c0 = 0; c0 < cols; c0 += 32) {
+      for (int c0 = 32 * half; c0 < cols; c0 += 64) {
         float x[32];
         tmem_load_32cols(taddr + c0, x);
         if (capped) mx_softcap(x, g.softcap, g.inv_softcap);
@@ -453,7 +457,7 @@ static int mx_launch_gemm(const MxGemmArgs& g, int grid, cudaStream_t cs) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
       cudaSuccess)
     return FLCE_ERR_CUDA;
-  return launch_dependent(kern, dim3(unsigned(grid)), dim3(kThreads), smem, cs, g);
+  return launch_dependent(kern, dim3(unsigned(grid)), dim3(kMxgThreads), smem, cs, g);
 }
 
 // ---------------------------------------------------------------- CTA pairs
