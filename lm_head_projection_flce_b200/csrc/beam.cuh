@@ -10,9 +10,9 @@
 //
 // One pass over the logits finds both sums and candidates: a block streams a
 // segment of a beam's row, each thread keeping its running maximum and sum of
-// exponentials, and its largest element with the vector that held it.  The
-// M-th largest of the 256 threads' maxima bounds the M-th largest element from
-// below, so the M best elements of the segment all lie with the at most M
+// exponentials, and its largest element with the vector that held it.  A value
+// that M of the 256 threads' maxima reach bounds the M-th largest element from
+// below, so the M best elements of the segment all lie with the few more than M
 // threads above the bound.  Each thread also leaves the maximum of every few
 // batches in shared memory (16 bits of it, rounded down), so of those threads'
 // vectors only the ones that can hold such an element are loaded again (all of
@@ -22,7 +22,7 @@
 // comparison per vector, like a plain logsumexp, and is bound by HBM; what comes
 // after it (bound, second look, ranks) is latency that nothing hides when all
 // blocks fit at once.  32 x 8 beams x 200000 FP32: 43 us (4.8 TB/s), 34 us without
-// that end; the merge takes 6 more.
+// that end; the merge takes 5 more.
 // A second kernel merges an item's segments: lse_k, the candidates' scores in
 // FP64 (scores of different beams lie next to one another; in FP32 their
 // rounding would decide), and the M best, by the same bound.
