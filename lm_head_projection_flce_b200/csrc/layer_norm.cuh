@@ -12,11 +12,20 @@
 // x, y, dy and dx are BF16 or FP32; everything between is FP32.  Both passes
 // are bound by HBM: the forward reads x and writes y, the backward reads x and
 // dy and writes dx, so a row is loaded once and held in registers, where the
-// variance takes its second look at it (centred, so a large mean costs no
-// digits).  A thread owns the same columns of every row it sees: the weights
-// stay in its registers, and so do its shares of dw and db, which leave the
-// block once, as one row of FP32 partials per block; a second kernel adds the
-// partials in a fixed order (no atomics: the same inputs give the same bits).
+// variance takes its second look at it.
+//
+// A mean in FP32, m0, is off by roundings of the row's magnitude.  So the second look
+// also sums what it leaves, r = sum_h (x[n,h] - m0) / H, and
+//   xhat = ((x - m0) - r) rstd_n      var_n = sum_h (x - m0)^2 / H - r^2
+// are off by roundings of the row's spread only, however large the mean: FP32 rows of
+// unit spread around 1000 by about 2e-7, where x - m0 alone is off by 1e-4, and the
+// xhat of a constant row is 0.  The backward is given the mean rounded to FP32; where
+// that is large against the spread, r is summed and taken out once more.
+//
+// A thread owns the same columns of every row it sees: the weights stay in its
+// registers, and so do its shares of dw and db, which leave the block once, as one row
+// of FP32 partials per block; a second kernel adds the partials in a fixed order (no
+// atomics: the same inputs give the same bits).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -152,35 +161,66 @@ __device__ __forceinline__ uint4 load16_any(const T* row, int64_t c, int64_t end
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// Sum of a pair over a row's threads: a warp, or the whole block through
-// shared memory.  `buf` alternates between calls, so one barrier per call is
-// enough: a buffer is written again only after every thread passed the barrier
-// of the call in between.
+// Sums of two or four values over a row's threads: a warp, or the whole block (at most
+// 16 warps) through shared memory.  The values are folded into one another on the
+// way: after the first exchange half of the warp carries one half of them, so two
+// values take 5 shuffles and four take 6.  `buf` alternates between calls, so one
+// barrier per call is enough: a buffer is written again only after every thread
+// passed the barrier of the call in between.
+constexpr int kLnMaxWarps = kLnMaxThreads / 32;
 template <bool kWarpRow>
-__device__ __forceinline__ float2 ln_row_sum(float2 v, float2 (*red)[32], int& buf) {
+__device__ __forceinline__ float2 ln_row_sum(float2 v, float (*red)[4 * kLnMaxWarps], int& buf) {
+  static_assert(kLnMaxWarps == 16, "half a warp adds the warps' sums");
+  const int lane = threadIdx.x & 31;
+  const bool up = (lane & 16) != 0;  // these lanes carry v.y
+  float s = (up ? v.y : v.x) + __shfl_xor_sync(0xffffffffu, up ? v.x : v.y, 16);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
-  if constexpr (kWarpRow) return v;
-  const int lane = threadIdx.x & 31, warps = int(blockDim.x >> 5);
-  if (lane == 0) red[buf][threadIdx.x >> 5] = v;
-  __syncthreads();
-  // Up to 16 warps both halves of a warp add the same 16 values.
-  const int from = warps > 16 ? lane : lane & 15;
-  v = from < warps ? red[buf][from] : make_float2(0.0f, 0.0f);
-  if (warps > 16) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, 16);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
-  }
+  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if constexpr (!kWarpRow) {
+    if ((lane & 15) == 0) red[buf][(lane & 16) + (threadIdx.x >> 5)] = s;
+    __syncthreads();
+    s = (lane & 15) < int(blockDim.x >> 5) ? red[buf][lane] : 0.0f;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    buf ^= 1;
   }
-  buf ^= 1;
-  return v;
+  const float other = __shfl_xor_sync(0xffffffffu, s, 16);
+  return up ? make_float2(other, s) : make_float2(s, other);
+}
+template <bool kWarpRow>
+__device__ __forceinline__ float4 ln_row_sum(float4 v, float (*red)[4 * kLnMaxWarps], int& buf) {
+  const int lane = threadIdx.x & 31;
+  const bool up = (lane & 16) != 0, mid = (lane & 8) != 0;  // lane / 8: the value carried
+  const float a = (up ? v.z : v.x) + __shfl_xor_sync(0xffffffffu, up ? v.x : v.z, 16);
+  const float b = (up ? v.w : v.y) + __shfl_xor_sync(0xffffffffu, up ? v.y : v.w, 16);
+  float s = (mid ? b : a) + __shfl_xor_sync(0xffffffffu, mid ? a : b, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if constexpr (!kWarpRow) {
+    const int warps = int(blockDim.x >> 5), i = lane & 7;
+    if (i == 0) red[buf][(lane >> 3) * kLnMaxWarps + (threadIdx.x >> 5)] = s;
+    __syncthreads();
+    const float* of = red[buf] + (lane >> 3) * kLnMaxWarps;
+    s = (i < warps ? of[i] : 0.0f) + (i + 8 < warps ? of[i + 8] : 0.0f);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    buf ^= 1;
+  }
+  return make_float4(__shfl_sync(0xffffffffu, s, 0), __shfl_sync(0xffffffffu, s, 8),
+                     __shfl_sync(0xffffffffu, s, 16), __shfl_sync(0xffffffffu, s, 24));
+}
+
+// What a row's sums say: of x - m0 and of its squares.
+struct LnStats {
+  float mean, rest, rstd;  // rest: r
+};
+__device__ __forceinline__ LnStats ln_stats(float m0, float sum, float squares, float inv_h, float eps) {
+  LnStats s;
+  s.rest = sum * inv_h;
+  const float var = fmaf(-s.rest, s.rest, squares * inv_h);
+  s.rstd = 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);  // a NaN stays one
+  s.mean = m0 + s.rest;
+  return s;
 }
 
 struct LnArgs {
@@ -252,16 +292,23 @@ __device__ __forceinline__ float ln_share_sum(const float2 (&v)[8]) {
   for (int i = 1; i < 8; ++i) s = __fadd2_rn(s, v[i]);
   return s.x + s.y;
 }
-// Subtracts the mean; returns the share's sum of squares.
+// Subtracts m0; returns the share's sum and sum of squares.
 template <int VN, bool kExact>
-__device__ __forceinline__ float ln_share_centre(float mean, int t, int tpr, int h, float2 (&v)[8]) {
+__device__ __forceinline__ float2 ln_share_centre(float m0, int t, int tpr, int h, float2 (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __fadd2_rn(v[i], ln_both(-mean));
+  for (int i = 0; i < 8; ++i) v[i] = __fadd2_rn(v[i], ln_both(-m0));
   if constexpr (!kExact) ln_share_clip<VN>(t, tpr, h, v);
-  float2 s = __fmul2_rn(v[0], v[0]);
+  float2 q = __fmul2_rn(v[0], v[0]);
 #pragma unroll
-  for (int i = 1; i < 8; ++i) s = __ffma2_rn(v[i], v[i], s);
-  return s.x + s.y;
+  for (int i = 1; i < 8; ++i) q = __ffma2_rn(v[i], v[i], q);
+  return make_float2(ln_share_sum(v), q.x + q.y);
+}
+// y in place of x - m0.
+__device__ __forceinline__ void ln_share_y(const LnStats& s, const float2 (&w)[8], const float2 (&b)[8],
+                                           float2 (&v)[8]) {
+  const float2 k = ln_both(s.rstd), c = ln_both(-s.rest * s.rstd);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __ffma2_rn(__ffma2_rn(v[i], k, c), w[i], b[i]);
 }
 // xhat in place of x, the row's shares of dw and db, g = dy w in place of dy;
 // returns the shares of sum g and sum g xhat.  Behind the row's end dy is 0.
@@ -294,7 +341,7 @@ __device__ __forceinline__ void ln_share_dx(float2 means, float rstd, const floa
 template <typename T, typename W, int VN, bool kWarpRow>
 __global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarpRows : kLnMaxThreads)
     ln_forward_kernel(const LnArgs a) {
-  __shared__ float2 red[2][32];
+  __shared__ float red[2][4 * kLnMaxWarps];
   const int tpr = kWarpRow ? 32 : int(blockDim.x), h = int(a.h);
   const int t = kWarpRow ? int(threadIdx.x & 31) : int(threadIdx.x);
   const int rpb = kWarpRow ? int(blockDim.x >> 5) : 1;
@@ -309,13 +356,12 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarpRows : kLnMaxThreads)
   }
   if (a.w) ln_share_load<W, VN, false>(static_cast<const W*>(a.w), t, tpr, h, 0.0f, w);
   if (a.b) ln_share_load<W, VN, false>(static_cast<const W*>(a.b), t, tpr, h, 0.0f, b);
-  auto finish = [&](int64_t r, float2 (&v)[8], float mean, float rstd) {
+  auto finish = [&](int64_t r, float2 (&v)[8], const LnStats& s) {
     if (t == 0) {
-      if (a.mean) a.mean[r] = mean;
-      if (a.rstd) a.rstd[r] = rstd;
+      if (a.mean) a.mean[r] = s.mean;
+      if (a.rstd) a.rstd[r] = s.rstd;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __ffma2_rn(__fmul2_rn(v[i], ln_both(rstd)), w[i], b[i]);
+    ln_share_y(s, w, b, v);
     ln_share_store<T, VN, false>(static_cast<T*>(a.y) + r * a.ldy, t, tpr, h, v);
   };
   // The loop is uniform over the threads that share a row.
@@ -328,13 +374,13 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarpRows : kLnMaxThreads)
     for (int k = 0; k < 8; ++k) v1[k] = ln_both(0.0f);
     ln_share_load<T, VN, false>(x, t, tpr, h, 0.0f, v0);
     if (two) ln_share_load<T, VN, false>(x + step * a.ldx, t, tpr, h, 0.0f, v1);
-    float2 s = ln_row_sum<kWarpRow>(make_float2(ln_share_sum(v0), ln_share_sum(v1)), red, buf);
+    const float2 s = ln_row_sum<kWarpRow>(make_float2(ln_share_sum(v0), ln_share_sum(v1)), red, buf);
     const float m0 = s.x * inv_h, m1 = s.y * inv_h;
-    s = make_float2(ln_share_centre<VN, false>(m0, t, tpr, h, v0),
-                    ln_share_centre<VN, false>(m1, t, tpr, h, v1));
-    s = ln_row_sum<kWarpRow>(s, red, buf);
-    finish(r, v0, m0, 1.0f / sqrtf(s.x * inv_h + a.eps));
-    if (two) finish(r + step, v1, m1, 1.0f / sqrtf(s.y * inv_h + a.eps));
+    const float2 c0 = ln_share_centre<VN, false>(m0, t, tpr, h, v0);
+    const float2 c1 = ln_share_centre<VN, false>(m1, t, tpr, h, v1);
+    const float4 c = ln_row_sum<kWarpRow>(make_float4(c0.x, c0.y, c1.x, c1.y), red, buf);
+    finish(r, v0, ln_stats(m0, c.x, c.y, inv_h, a.eps));
+    if (two) finish(r + step, v1, ln_stats(m1, c.z, c.w, inv_h, a.eps));
   }
 }
 
@@ -413,7 +459,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     ln_forward_ring_kernel(const LnArgs a, const LnRing g) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(8) uint64_t full[kLnSlots];
-  __shared__ float2 red[2][32];
+  __shared__ float red[2][4 * kLnMaxWarps];
   __shared__ PipeCtl ctl;
   const int t = threadIdx.x, tpr = blockDim.x, h = int(a.h);
   const int count = int((a.n - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this block's rows
@@ -455,13 +501,12 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     ln_ring_read<T, VN, kExact>(ring + uint32_t(get.slot) * g.slot_bytes, a.x, a.ldx, a.n, h, r, v);
     get.advance(g.slots);
   };
-  auto finish = [&](int64_t r, float2 (&v)[8], float mean, float rstd) {
+  auto finish = [&](int64_t r, float2 (&v)[8], const LnStats& s) {
     if (t == 0) {
-      if (a.mean) a.mean[r] = mean;
-      if (a.rstd) a.rstd[r] = rstd;
+      if (a.mean) a.mean[r] = s.mean;
+      if (a.rstd) a.rstd[r] = s.rstd;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __ffma2_rn(__fmul2_rn(v[i], ln_both(rstd)), w[i], b[i]);
+    ln_share_y(s, w, b, v);
     ln_share_store<T, VN, kExact>(static_cast<T*>(a.y) + r * a.ldy, t, tpr, h, v);
   };
   int64_t r = blockIdx.x;
@@ -472,49 +517,74 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     for (int k = 0; k < 8; ++k) v1[k] = ln_both(0.0f);
     fetch(r, v0);
     if (two) fetch(r + gridDim.x, v1);
-    float2 s = ln_row_sum<false>(make_float2(ln_share_sum(v0), ln_share_sum(v1)), red, buf);
+    const float2 s = ln_row_sum<false>(make_float2(ln_share_sum(v0), ln_share_sum(v1)), red, buf);
     if (t == 0) {
       issue();
       if (two) issue();
     }
     const float m0 = s.x * inv_h, m1 = s.y * inv_h;
-    s = make_float2(ln_share_centre<VN, kExact>(m0, t, tpr, h, v0),
-                    ln_share_centre<VN, kExact>(m1, t, tpr, h, v1));
-    s = ln_row_sum<false>(s, red, buf);
-    finish(r, v0, m0, 1.0f / sqrtf(s.x * inv_h + a.eps));
-    if (two) finish(r + gridDim.x, v1, m1, 1.0f / sqrtf(s.y * inv_h + a.eps));
+    const float2 c0 = ln_share_centre<VN, kExact>(m0, t, tpr, h, v0);
+    const float2 c1 = ln_share_centre<VN, kExact>(m1, t, tpr, h, v1);
+    const float4 c = ln_row_sum<false>(make_float4(c0.x, c0.y, c1.x, c1.y), red, buf);
+    finish(r, v0, ln_stats(m0, c.x, c.y, inv_h, a.eps));
+    if (two) finish(r + gridDim.x, v1, ln_stats(m1, c.z, c.w, inv_h, a.eps));
   }
 }
 
 // Rows too long for the registers of one block: three looks at the row, the
-// later ones from L2.
+// later ones from L2.  A thread's share has no bound here: the mean is summed in
+// FP64, 32 elements of the thread at a time, and its remainder as above.
+constexpr int kLnLongThreads = 1024;
+// Sum over a block of whole warps, in FP64.
+__device__ __forceinline__ double ln_block_sum(double v) {
+  __shared__ double red[32];
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();  // the last call's values have been read
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < int(blockDim.x >> 5) ? red[lane] : 0.0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 template <typename T, typename W>
-__global__ void __launch_bounds__(1024) ln_forward_long_kernel(const LnArgs a) {
-  __shared__ float2 red[2][32];
-  int buf = 0;
+__global__ void __launch_bounds__(kLnLongThreads) ln_forward_long_kernel(const LnArgs a) {
   for (int64_t r = blockIdx.x; r < a.n; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ldx;
     T* y = static_cast<T*>(a.y) + r * a.ldy;
-    float2 s = make_float2(0.0f, 0.0f);
     float v[1], w[1], b[1];
-    for (int64_t c = threadIdx.x; c < a.h; c += blockDim.x) {
-      LnIo<T, 1>::load(x + c, v);
-      s.x += v[0];
+    double sum = 0.0;
+    for (int64_t c0 = threadIdx.x; c0 < a.h; c0 += 32 * kLnLongThreads) {
+      const int64_t end = min(a.h, c0 + 32 * kLnLongThreads);
+      float part = 0.0f;
+      for (int64_t c = c0; c < end; c += kLnLongThreads) {
+        LnIo<T, 1>::load(x + c, v);
+        part += v[0];
+      }
+      sum += double(part);
     }
-    const float mean = ln_row_sum<false>(s, red, buf).x / float(a.h);
-    s = make_float2(0.0f, 0.0f);
-    for (int64_t c = threadIdx.x; c < a.h; c += blockDim.x) {
+    const double inv_h = 1.0 / double(a.h);
+    const float m0 = float(ln_block_sum(sum) * inv_h);
+    float left = 0.0f, squares = 0.0f;
+    for (int64_t c = threadIdx.x; c < a.h; c += kLnLongThreads) {
       LnIo<T, 1>::load(x + c, v);
-      s.x += (v[0] - mean) * (v[0] - mean);
+      v[0] -= m0;
+      left += v[0];
+      squares += v[0] * v[0];
     }
-    const float rstd = 1.0f / sqrtf(ln_row_sum<false>(s, red, buf).x / float(a.h) + a.eps);
+    const double rest = ln_block_sum(double(left)) * inv_h;
+    const double var = ln_block_sum(double(squares)) * inv_h - rest * rest;
+    const float rstd = 1.0f / sqrtf(float(var < 0.0 ? 0.0 : var) + a.eps);
     if (threadIdx.x == 0) {
-      if (a.mean) a.mean[r] = mean;
+      if (a.mean) a.mean[r] = float(double(m0) + rest);
       if (a.rstd) a.rstd[r] = rstd;
     }
-    for (int64_t c = threadIdx.x; c < a.h; c += blockDim.x) {
+    const float shift = float(-rest * double(rstd));
+    for (int64_t c = threadIdx.x; c < a.h; c += kLnLongThreads) {
       LnIo<T, 1>::load(x + c, v);
-      v[0] = (v[0] - mean) * rstd;
+      v[0] = fmaf(v[0] - m0, rstd, shift);
       if (a.w) {
         LnIo<W, 1>::load(static_cast<const W*>(a.w) + c, w);
         v[0] *= w[0];
@@ -543,10 +613,91 @@ struct LnBwdArgs {
   float* part_b;
 };
 
+// The backward's mean is off by a rounding, 2^-24 |mean|, and with it xhat by that times
+// rstd: for a mean within 16 standard deviations 1e-6 at most, no more than by the sums'
+// roundings.  Rows beyond are rare, and a block does them once more behind its other
+// rows (where all of them are, 16384 x 8192 BF16 takes 724 us against 135): what the
+// means leave over, summed for every row within its loop, cost all backwards 2% at that
+// size, 9% at 4096 x 8191, and 28% where dx is not wanted.
+__device__ __forceinline__ bool ln_far(float mean, float rstd) { return fabsf(mean) * rstd > 16.0f; }
+// Whether a thread sees such a row, when the block deals out the rows first, first + step, ...
+__device__ __forceinline__ bool ln_sees_far(const LnBwdArgs& a, int64_t first, int64_t step) {
+  bool any = false;
+  for (int64_t r = first + threadIdx.x * step; r < a.n; r += blockDim.x * step)
+    any |= ln_far(a.mean[r], a.rstd[r]);
+  return any;
+}
+// Of the rows [r, r + kRun), r = first, first + step, ..., by a whole block: dx is written
+// again, and `part_w`, the row of partials that holds these rows' shares of dw, put
+// right; either may be nullptr.  any: whether this thread saw a row to do.
+template <typename T, typename W, int VN, int kRun>
+__device__ __forceinline__ void ln_backward_far(const LnBwdArgs& a, bool any, float* part_w,
+                                                int64_t first, int64_t step) {
+  if (!__syncthreads_or(any)) return;  // the block's partials and dx are written, too
+  if (part_w == nullptr && a.dx == nullptr) return;
+  const double inv_h = 1.0 / double(a.h);
+  for (int64_t r = first, i = 0; r - i < a.n; i + 1 < kRun ? (++i, ++r) : (r += step - i, i = 0)) {
+    if (r >= a.n) continue;
+    const float mean = a.mean[r], rstd = a.rstd[r];
+    if (!ln_far(mean, rstd)) continue;  // the same for every thread
+    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+    const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
+    float v[VN], g[VN], w[VN];
+    auto xhat = [&](int64_t c) {
+      LnIo<T, VN>::load(x + c, v);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) v[j] = (v[j] - mean) * rstd;
+    };
+    auto weight = [&](int64_t c) {
+#pragma unroll
+      for (int j = 0; j < VN; ++j) w[j] = 1.0f;
+      if (a.w) LnIo<W, VN>::load(static_cast<const W*>(a.w) + c, w);
+    };
+    const int64_t t = int64_t(threadIdx.x) * VN, next = int64_t(blockDim.x) * VN;
+    float s = 0.0f;
+    for (int64_t c = t; c < a.h; c += next) {
+      xhat(c);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) s += v[j];
+    }
+    const float rest = float(ln_block_sum(double(s)) * inv_h);
+    float m1 = 0.0f, m2 = 0.0f;
+    if (a.dx) {
+      for (int64_t c = t; c < a.h; c += next) {
+        xhat(c);
+        LnIo<T, VN>::load(dy + c, g);
+        weight(c);
+#pragma unroll
+        for (int j = 0; j < VN; ++j) {
+          m1 += g[j] * w[j];
+          m2 += g[j] * w[j] * (v[j] - rest);
+        }
+      }
+      m1 = float(ln_block_sum(double(m1)) * inv_h);
+      m2 = float(ln_block_sum(double(m2)) * inv_h);
+    }
+    for (int64_t c = t; c < a.h; c += next) {
+      LnIo<T, VN>::load(dy + c, g);
+      if (part_w) {
+        LnIo<float, VN>::load(part_w + c, w);
+#pragma unroll
+        for (int j = 0; j < VN; ++j) w[j] -= g[j] * rest;
+        LnIo<float, VN>::store(part_w + c, w);
+      }
+      if (a.dx == nullptr) continue;
+      xhat(c);
+      weight(c);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) g[j] = rstd * (g[j] * w[j] - m1 - (v[j] - rest) * m2);
+      LnIo<T, VN>::store(static_cast<T*>(a.dx) + r * a.lddx + c, g);
+    }
+  }
+}
+
 template <typename T, typename W, int VN, bool kWarpRow>
 __global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarpRows : kLnMaxThreads)
     ln_backward_kernel(const LnBwdArgs a) {
-  __shared__ float2 red[2][32];
+  __shared__ float red[2][4 * kLnMaxWarps];
   __shared__ __align__(16) float part[kWarpRow ? kLnWarpRows : 1][kWarpRow ? kLnWarpCols : 4];
   grid_launch_dependents();
   const int tpr = kWarpRow ? 32 : int(blockDim.x), h = int(a.h);
@@ -563,8 +714,10 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarpRows : kLnMaxThreads)
     aw[i] = ab[i] = ln_both(0.0f);
   }
   if (a.w) ln_share_load<W, VN, false>(static_cast<const W*>(a.w), t, tpr, h, 0.0f, w);
+  bool far = false;
   for (int64_t r = int64_t(blockIdx.x) * rpb + (kWarpRow ? warp : 0); r < a.n; r += step) {
     const float mean = a.mean[r], rstd = a.rstd[r];
+    far |= ln_far(mean, rstd);
     float2 xh[8], d[8];
     ln_share_load<T, VN, false>(static_cast<const T*>(a.x) + r * a.ldx, t, tpr, h, 0.0f, xh);
     ln_share_load<T, VN, false>(static_cast<const T*>(a.dy) + r * a.lddy, t, tpr, h, 0.0f, d);
@@ -596,6 +749,8 @@ __global__ void __launch_bounds__(kWarpRow ? 32 * kLnWarpRows : kLnMaxThreads)
       __syncthreads();
     }
   }
+  ln_backward_far<T, W, VN, kWarpRow ? kLnWarpRows : 1>(
+      a, far, a.part_w ? a.part_w + int64_t(blockIdx.x) * h : nullptr, int64_t(blockIdx.x) * rpb, step);
 }
 
 // The backward through the ring: a slot holds the row of x and the row of dy.
@@ -604,7 +759,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     ln_backward_ring_kernel(const LnBwdArgs a, const LnRing g) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(8) uint64_t full[kLnSlots];
-  __shared__ float2 red[2][32];
+  __shared__ float red[2][4 * kLnMaxWarps];
   __shared__ PipeCtl ctl;
   const int t = threadIdx.x, tpr = blockDim.x, h = int(a.h);
   const int count = int((a.n - blockIdx.x + gridDim.x - 1) / gridDim.x);
@@ -669,13 +824,14 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
   }
   if (a.part_w) ln_share_store<float, VN, kExact>(a.part_w + int64_t(blockIdx.x) * h, t, tpr, h, aw);
   if (a.part_b) ln_share_store<float, VN, kExact>(a.part_b + int64_t(blockIdx.x) * h, t, tpr, h, ab);
+  ln_backward_far<T, W, VN, 1>(a, ln_sees_far(a, blockIdx.x, gridDim.x),
+                               a.part_w ? a.part_w + int64_t(blockIdx.x) * h : nullptr, blockIdx.x,
+                               gridDim.x);
 }
 
 // Long rows: dx row by row (two looks at x and dy) ...
 template <typename T, typename W>
-__global__ void __launch_bounds__(1024) ln_backward_long_dx_kernel(const LnBwdArgs a) {
-  __shared__ float2 red[2][32];
-  int buf = 0;
+__global__ void __launch_bounds__(kLnLongThreads) ln_backward_long_dx_kernel(const LnBwdArgs a) {
   for (int64_t r = blockIdx.x; r < a.n; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ldx;
     const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
@@ -683,15 +839,15 @@ __global__ void __launch_bounds__(1024) ln_backward_long_dx_kernel(const LnBwdAr
     const float mean = a.mean[r], rstd = a.rstd[r];
     float v[1], g[1], w[1] = {1.0f};
     float2 s = make_float2(0.0f, 0.0f);
-    for (int64_t c = threadIdx.x; c < a.h; c += blockDim.x) {
+    for (int64_t c = threadIdx.x; c < a.h; c += kLnLongThreads) {
       LnIo<T, 1>::load(x + c, v);
       LnIo<T, 1>::load(dy + c, g);
       if (a.w) LnIo<W, 1>::load(static_cast<const W*>(a.w) + c, w);
       s.x += g[0] * w[0];
       s.y += g[0] * w[0] * ((v[0] - mean) * rstd);
     }
-    s = ln_row_sum<false>(s, red, buf);
-    const float m1 = s.x / float(a.h), m2 = s.y / float(a.h);
+    const float m1 = float(ln_block_sum(double(s.x)) / double(a.h));
+    const float m2 = float(ln_block_sum(double(s.y)) / double(a.h));
     for (int64_t c = threadIdx.x; c < a.h; c += blockDim.x) {
       LnIo<T, 1>::load(x + c, v);
       LnIo<T, 1>::load(dy + c, g);
@@ -716,6 +872,14 @@ __global__ void __launch_bounds__(256) ln_backward_long_dw_kernel(const LnBwdArg
   }
   if (a.part_w) a.part_w[int64_t(blockIdx.y) * a.h + c] = sw;
   if (a.part_b) a.part_b[int64_t(blockIdx.y) * a.h + c] = sb;
+}
+
+// ... and the rows whose mean is large once more, a block per row of partials.
+template <typename T, typename W>
+__global__ void __launch_bounds__(kLnLongThreads) ln_backward_long_far_kernel(const LnBwdArgs a) {
+  ln_backward_far<T, W, 1, 1>(a, ln_sees_far(a, blockIdx.x, gridDim.x),
+                              a.part_w ? a.part_w + int64_t(blockIdx.x) * a.h : nullptr, blockIdx.x,
+                              gridDim.x);
 }
 
 // dw and db (blockIdx.y = 0, 1) from the `parts` rows of partials, in a fixed
@@ -824,7 +988,7 @@ template <typename T, typename W>
 static void ln_dispatch_fwd(const LnArgs& a, const LnShape& s, int grid, cudaStream_t st) {
   constexpr int kFull = 16 / int(sizeof(T));
   if (s.vn == 0)
-    ln_forward_long_kernel<T, W><<<grid, 1024, 0, st>>>(a);
+    ln_forward_long_kernel<T, W><<<grid, kLnLongThreads, 0, st>>>(a);
   else if (s.vn == 1 && s.warp_row)
     ln_forward_kernel<T, W, 1, true><<<grid, s.threads, 0, st>>>(a);
   else if (s.vn == 1)
@@ -979,13 +1143,13 @@ extern "C" int flce_layer_norm_backward(const void* dy, int64_t lddy, const void
         const int grid = int(std::min<int64_t>(n, int64_t(dev->num_sms) * 2));
         LaunchScope scope(KF_LN_BWD, 0.0, bytes, cs);
         if (dtype == FLCE_BF16 && w_dtype == FLCE_BF16)
-          ln_backward_long_dx_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 1024, 0, cs>>>(a);
+          ln_backward_long_dx_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kLnLongThreads, 0, cs>>>(a);
         else if (dtype == FLCE_BF16)
-          ln_backward_long_dx_kernel<__nv_bfloat16, float><<<grid, 1024, 0, cs>>>(a);
+          ln_backward_long_dx_kernel<__nv_bfloat16, float><<<grid, kLnLongThreads, 0, cs>>>(a);
         else if (w_dtype == FLCE_BF16)
-          ln_backward_long_dx_kernel<float, __nv_bfloat16><<<grid, 1024, 0, cs>>>(a);
+          ln_backward_long_dx_kernel<float, __nv_bfloat16><<<grid, kLnLongThreads, 0, cs>>>(a);
         else
-          ln_backward_long_dx_kernel<float, float><<<grid, 1024, 0, cs>>>(a);
+          ln_backward_long_dx_kernel<float, float><<<grid, kLnLongThreads, 0, cs>>>(a);
         if (cudaGetLastError() != cudaSuccess) return FLCE_ERR_CUDA;
       }
       if (params) {
@@ -996,6 +1160,19 @@ extern "C" int flce_layer_norm_backward(const void* dy, int64_t lddy, const void
           ln_backward_long_dw_kernel<__nv_bfloat16><<<grid, 256, 0, cs>>>(a);
         else
           ln_backward_long_dw_kernel<float><<<grid, 256, 0, cs>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return FLCE_ERR_CUDA;
+      }
+      if (dx != nullptr || dweight != nullptr) {
+        const int grid = int(std::min<int64_t>(n, kLnSms));  // as many as rows of partials
+        LaunchScope scope(KF_LN_BWD, 0.0, 8.0 * double(n), cs);
+        if (dtype == FLCE_BF16 && w_dtype == FLCE_BF16)
+          ln_backward_long_far_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kLnLongThreads, 0, cs>>>(a);
+        else if (dtype == FLCE_BF16)
+          ln_backward_long_far_kernel<__nv_bfloat16, float><<<grid, kLnLongThreads, 0, cs>>>(a);
+        else if (w_dtype == FLCE_BF16)
+          ln_backward_long_far_kernel<float, __nv_bfloat16><<<grid, kLnLongThreads, 0, cs>>>(a);
+        else
+          ln_backward_long_far_kernel<float, float><<<grid, kLnLongThreads, 0, cs>>>(a);
       }
     } else {
       parts = int(ln_parts(n, s));
