@@ -26,6 +26,7 @@ import dataclasses
 import os
 
 import torch
+from torch.autograd import forward_ad
 
 from . import build as _build
 
@@ -794,6 +795,13 @@ def _norm_grads(lib, dy, lddy, x, n, h, ldx, weight, w_dtype, mean, rstd, dx, ld
     _check("flce_layer_norm_backward", st)
 
 
+def _has_tangent(*tensors) -> bool:
+    """True when one of the tensors carries a forward-mode derivative."""
+    if getattr(forward_ad, "_current_level", 0) < 0:  # outside every dual level: none does
+        return False
+    return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
@@ -806,6 +814,8 @@ class _LayerNorm(torch.autograd.Function):
     def backward(ctx, dy):
         if torch.is_grad_enabled():
             raise RuntimeError("layer_norm's gradient has no gradient of its own (create_graph)")
+        if _has_tangent(dy):
+            raise NotImplementedError("layer_norm's gradient has no forward-mode derivative")
         # What the forward checked is not checked again: this runs in autograd's own
         # thread, where a small call's time is mostly Python.
         x, weight, mean, rstd = ctx.saved_tensors
@@ -831,10 +841,12 @@ class _LayerNorm(torch.autograd.Function):
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5):
     """Autograd-aware layer norm over the last dimension: ``(x - mean) * rstd *
-    weight + bias``; gradients flow to ``x``, ``weight`` and ``bias``."""
+    weight + bias``; gradients flow to ``x``, ``weight`` and ``bias``.  Reverse mode and
+    once only: tensors with a forward-mode tangent are refused."""
     if not (torch.is_grad_enabled() and (x.requires_grad
                                          or (weight is not None and weight.requires_grad)
-                                         or (bias is not None and bias.requires_grad))):
+                                         or (bias is not None and bias.requires_grad))
+            or _has_tangent(x, weight, bias)):
         return layer_norm_forward(x, weight, bias, eps=eps, stats=False)[0]
     return _LayerNorm.apply(x, weight, bias, eps)
 
