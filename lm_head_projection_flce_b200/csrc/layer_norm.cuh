@@ -1000,7 +1000,9 @@ static void ln_dispatch_fwd(const LnArgs& a, const LnShape& s, int grid, cudaStr
 }
 template <typename Kern, typename Args>
 static int ln_launch_ring(Kern kern, const Args& a, const LnRingShape& s, int grid, cudaStream_t st) {
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(s.smem)) !=
+  // The limit belongs to the kernel, not to the launch: always the same, so that a call
+  // of another thread cannot lower it before this one launches.
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLnRingBytes) !=
       cudaSuccess)
     return FLCE_ERR_CUDA;
   kern<<<grid, s.threads, s.smem, st>>>(a, s.ring);

@@ -454,7 +454,9 @@ template <typename TO, int kSft>
 static int mx_launch_gemm(const MxGemmArgs& g, int grid, cudaStream_t cs) {
   auto kern = mx_gemm_kernel<TO, kSft>;
   const size_t smem = 1024 + size_t(g.stages) * mxg_stage_bytes(g.tile_n);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) !=
+  // The limit belongs to the kernel, not to the launch: always the same, so that a call
+  // of another thread cannot lower it before this one launches.
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kMxgSmem) !=
       cudaSuccess)
     return FLCE_ERR_CUDA;
   return launch_dependent(kern, dim3(unsigned(grid)), dim3(kMxgThreads), smem, cs, g);
