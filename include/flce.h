@@ -381,8 +381,10 @@ int flce_beam_select(const void* logits, int dtype, int64_t batch, int64_t beams
  *            src_batch_stride + k * src_beam_stride (bytes), likewise dst.  What
  *            lies between and behind the pieces is left as it was.
  *            dst == src (with the same strides): in place, without scratch.
- *            Otherwise dst must not overlap any src.  Entries of dst must not
- *            overlap one another; the same dst twice is refused.
+ *            Otherwise a dst that shares bytes with a src, with another state's
+ *            dst or with the parents is refused (FLCE_ERR_INVALID_ARG); states
+ *            that interleave without sharing any are fine.  Entries of one dst
+ *            must not overlap one another.
  *   parents  int64 [batch, beams], any map (the same parent may repeat).  An
  *            entry outside [0, beams) leaves its beam's own state and raises
  *            FLCE_ERR_BAD_INDEX in the error word (flce_get_error).

@@ -1083,7 +1083,8 @@ def beam_reorder(states, parents, *, length: int | None = None, length_dim: int 
     With ``length`` only the first ``length`` positions along ``length_dim`` follow (a
     cache filled so far); the others are left as they were.  Without ``out`` the
     states are reordered in place, with no scratch memory; with ``out`` (the same
-    structure, not overlapping the states) they are gathered into it.  ``parents``
+    structure) they are gathered into it.  Nothing that is written may share memory with
+    another state, with what is read or with ``parents``: refused.  ``parents``
     int64 [B, K]; entries outside [0, K) keep the beam's own state and raise
     FLCE_ERR_BAD_INDEX (``get_error``).  Returns what was written.
     """
