@@ -282,7 +282,8 @@ int flce_ce_backward(const void* logits, int dtype, const int64_t* labels, const
  * All arithmetic between the inputs and the one rounding of each output is
  * FP32 or FP64; what a mean rounded to FP32 leaves over is taken out of the
  * centred values, so a mean that is large against the row's spread costs no
- * digits.  Outputs may not overlap inputs.
+ * digits.  An output, or the workspace, that shares bytes with an input or
+ * another output is refused (FLCE_ERR_INVALID_ARG).
  */
 size_t flce_layer_norm_workspace_size(int64_t n_tokens, int64_t hidden_size);
 int flce_layer_norm_forward(const void* x, int dtype, int64_t n_tokens, int64_t hidden_size,

@@ -37,6 +37,7 @@
 #include <vector>
 
 #include "chunked_ce.cuh"
+#include "extents.cuh"
 #include "layer_norm.cuh"
 
 namespace flce {
@@ -716,78 +717,15 @@ __global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(const __g
   }
 }
 
-// Bytes base + b batch_stride + k beam_stride + o outer_stride + [0, inner) of a state.
-struct ReorderExtent {
-  uint64_t base, end;  // end: behind the last byte
-  int64_t stride[3], count[3], inner;
-  bool written;
-};
-static ReorderExtent reorder_extent(const void* base, const int64_t (&stride)[3], const int64_t (&count)[3],
-                                    int64_t inner, bool written) {
-  ReorderExtent e{reinterpret_cast<uint64_t>(base), 0, {}, {}, inner, written};
-  unsigned __int128 end = static_cast<unsigned __int128>(e.base) + uint64_t(inner);
-  for (int d = 0; d < 3; ++d) {
-    e.count[d] = stride[d] == 0 ? 1 : count[d];
-    e.stride[d] = e.count[d] == 1 ? 0 : stride[d];
-    end += static_cast<unsigned __int128>(e.count[d] - 1) * uint64_t(e.stride[d]);
-  }
-  e.end = end > UINT64_MAX ? UINT64_MAX : uint64_t(end);
-  return e;
-}
-// Whether two of them have a byte in common.  Piece p of one and piece q of the other
-// do when their distance, base - base' plus a multiple of every stride (those of the second
-// one taken away), lies within their lengths.  Strides are tried from the largest
-// down, and of each only the multiples that the smaller ones can still make good: one
-// or two where both have the same strides.
-struct ReorderStep {
-  __int128 stride, low, high;  // multiples allowed
-};
-static bool reorder_reach(const ReorderStep* step, int n, __int128 at, __int128 from, __int128 to) {
-  if (n == 0) return at >= from && at <= to;
-  __int128 least = 0, most = 0;  // what the smaller strides add
-  for (int i = 1; i < n; ++i) {
-    least += step[i].low * step[i].stride;
-    most += step[i].high * step[i].stride;
-  }
-  auto floor_div = [](__int128 a, __int128 b) { return a / b - (a % b < 0 ? 1 : 0); };
-  const __int128 s = step[0].stride;
-  const __int128 first = std::max(step[0].low, -floor_div(at + most - from, s));
-  const __int128 last = std::min(step[0].high, floor_div(to - at - least, s));
-  for (__int128 c = first; c <= last; ++c)
-    if (reorder_reach(step + 1, n - 1, at + c * s, from, to)) return true;
-  return false;
-}
-static bool reorder_overlap(const ReorderExtent& a, const ReorderExtent& b) {
-  if (a.base >= b.end || b.base >= a.end) return false;
-  ReorderStep step[6];
-  int n = 0;
-  for (int d = 0; d < 6; ++d) {
-    const ReorderExtent& e = d < 3 ? a : b;
-    if (e.count[d % 3] == 1) continue;
-    const __int128 most = e.count[d % 3] - 1;
-    ReorderStep one{e.stride[d % 3], d < 3 ? 0 : -most, d < 3 ? most : 0};
-    int at = 0;
-    while (at < n && step[at].stride > one.stride) ++at;
-    if (at < n && step[at].stride == one.stride) {
-      step[at].low += one.low;
-      step[at].high += one.high;
-      continue;
-    }
-    for (int i = n++; i > at; --i) step[i] = step[i - 1];
-    step[at] = one;
-  }
-  return reorder_reach(step, n, __int128(a.base) - __int128(b.base), -(__int128(a.inner) - 1),
-                       __int128(b.inner) - 1);
-}
 // Extents [first, last), in ascending order of their bases, that are slices of one buffer's
 // entries (a cache's layers, keys and values behind [batch, beams]): the same strides,
 // each slice behind the one before, all of them within the stride of the entries. Such
 // slices share nothing, and need not be looked at in pairs (160 of them: 460 us).
-static bool reorder_slices(const ReorderExtent* first, const ReorderExtent* last) {
+static bool reorder_slices(const Extent* first, const Extent* last) {
   const int big = first->stride[0] >= first->stride[1] ? 0 : 1;
   const uint64_t large = uint64_t(first->stride[big]), small = uint64_t(first->stride[1 - big]);
   uint64_t end = first->base;
-  for (const ReorderExtent* e = first; e != last; ++e) {
+  for (const Extent* e = first; e != last; ++e) {
     if (e->base < end || e->stride[0] != first->stride[0] || e->stride[1] != first->stride[1]) return false;
     end = e->base + uint64_t(e->count[2] - 1) * uint64_t(e->stride[2]) + uint64_t(e->inner);
   }
@@ -799,21 +737,21 @@ static bool reorder_slices(const ReorderExtent* first, const ReorderExtent* last
 // state written over another one, over one that is read or over the parents.
 static int reorder_check(const flce_beam_state* states, int64_t count, const int64_t* parents,
                          int64_t batch, int64_t beams) try {
-  std::vector<ReorderExtent> all;
+  std::vector<Extent> all;
   all.reserve(size_t(2 * count + 1));
-  all.push_back(reorder_extent(parents, {0, 0, 0}, {1, 1, 1}, batch * beams * 8, false));
+  all.push_back(make_extent(parents, {0, 0, 0}, {1, 1, 1}, batch * beams * 8, false));
   for (int64_t i = 0; i < count; ++i) {
     const flce_beam_state& s = states[i];
     if (s.outer * s.inner == 0) continue;
     const int64_t counts[3] = {batch, beams, s.outer};
-    all.push_back(reorder_extent(s.dst, {s.dst_batch_stride, s.dst_beam_stride, s.outer_stride}, counts,
-                                 s.inner, true));
+    all.push_back(make_extent(s.dst, {s.dst_batch_stride, s.dst_beam_stride, s.outer_stride}, counts,
+                              s.inner, true));
     if (s.src != s.dst)
-      all.push_back(reorder_extent(s.src, {s.src_batch_stride, s.src_beam_stride, s.outer_stride}, counts,
-                                   s.inner, false));
+      all.push_back(make_extent(s.src, {s.src_batch_stride, s.src_beam_stride, s.outer_stride}, counts,
+                                s.inner, false));
   }
   std::sort(all.begin(), all.end(),
-            [](const ReorderExtent& a, const ReorderExtent& b) { return a.base < b.base; });
+            [](const Extent& a, const Extent& b) { return a.base < b.base; });
   for (size_t first = 0, last; first < all.size(); first = last) {
     uint64_t end = all[first].end;  // of those up to `last`, which lie among one another
     for (last = first + 1; last < all.size() && all[last].base < end; ++last)
@@ -821,7 +759,7 @@ static int reorder_check(const flce_beam_state* states, int64_t count, const int
     if (reorder_slices(all.data() + first, all.data() + last)) continue;
     for (size_t i = first; i < last; ++i)
       for (size_t j = i + 1; j < last && all[j].base < all[i].end; ++j)
-        if ((all[i].written || all[j].written) && reorder_overlap(all[i], all[j]))
+        if ((all[i].written || all[j].written) && extents_overlap(all[i], all[j]))
           return FLCE_ERR_INVALID_ARG;
   }
   return FLCE_OK;

@@ -30,7 +30,10 @@
 
 #include <cuda_bf16.h>
 
+#include <initializer_list>
+
 #include "epilogues.cuh"
+#include "extents.cuh"
 
 namespace flce {
 
@@ -982,6 +985,17 @@ static bool ln_sizes_ok(int64_t n, int64_t h) {
 static bool ln_ld_ok(int64_t n, int64_t h, int64_t ld) {
   return ld >= h && ld <= (int64_t(1) << 40) / std::max<int64_t>(n, 1);
 }
+// n rows of `row` bytes, ld bytes apart (nothing where p is nullptr), read or written.
+static Extent ln_extent(const void* p, int64_t n, int64_t row, int64_t ld, bool written) {
+  return make_extent(p, {ld, 0, 0}, {p == nullptr ? 1 : n, 1, 1}, p == nullptr ? 0 : row, written);
+}
+// True where one of them is written over another one.
+static bool ln_overlap(std::initializer_list<Extent> all) {
+  for (const Extent* a = all.begin(); a != all.end(); ++a)
+    for (const Extent* b = a + 1; b != all.end(); ++b)
+      if ((a->written || b->written) && extents_overlap(*a, *b)) return true;
+  return false;
+}
 static bool ln_dtype_ok(int d) { return d == FLCE_BF16 || d == FLCE_F32; }
 
 template <typename T, typename W>
@@ -1058,6 +1072,10 @@ extern "C" int flce_layer_norm_forward(const void* x, int dtype, int64_t n, int6
   if (x == nullptr || y == nullptr || !aligned(x, esz) || !aligned(y, esz) ||
       !aligned(mean, 4) || !aligned(rstd, 4))
     return FLCE_ERR_INVALID_ARG;
+  if (ln_overlap({ln_extent(x, n, h * esz, ldx * esz, false), ln_extent(weight, 1, h * wsz, 0, false),
+                  ln_extent(bias, 1, h * wsz, 0, false), ln_extent(y, n, h * esz, ldy * esz, true),
+                  ln_extent(mean, 1, n * 4, 0, true), ln_extent(rstd, 1, n * 4, 0, true)}))
+    return FLCE_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;
   const int st = device_info(&dev);
   if (st != FLCE_OK) return st;
@@ -1111,6 +1129,12 @@ extern "C" int flce_layer_norm_backward(const void* dy, int64_t lddy, const void
   if (params && (workspace == nullptr || !aligned(workspace, 16) || ws_bytes < 2 * half))
     return FLCE_ERR_WORKSPACE;
   if (!params && (dx == nullptr || n == 0)) return FLCE_OK;
+  if (ln_overlap({ln_extent(dy, n, h * esz, lddy * esz, false), ln_extent(x, n, h * esz, ldx * esz, false),
+                  ln_extent(weight, 1, h * wsz, 0, false), ln_extent(mean, 1, n * 4, 0, false),
+                  ln_extent(rstd, 1, n * 4, 0, false), ln_extent(dx, n, h * esz, lddx * esz, true),
+                  ln_extent(dweight, 1, h * wsz, 0, true), ln_extent(dbias, 1, h * wsz, 0, true),
+                  ln_extent(params ? workspace : nullptr, 1, int64_t(2 * half), 0, true)}))
+    return FLCE_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;
   const int st = device_info(&dev);
   if (st != FLCE_OK) return st;

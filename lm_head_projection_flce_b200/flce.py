@@ -701,6 +701,7 @@ def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-5,
     ``bias`` [H] bf16 or fp32, either may be None.  Returns ``(y, mean, rstd)``:
     y in x's dtype and shape, the row statistics FP32 [N] for the backward
     (``stats=False``: None for statistics that were not given, and not written).
+    Outputs given may not share memory with inputs or one another: refused.
     """
     lib = _LIB or load_library()
     _norm_input(x)
