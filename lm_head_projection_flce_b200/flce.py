@@ -1159,7 +1159,12 @@ class CapturedBeamStep:
         stream = torch.cuda.Stream(dev)
         stream.wait_stream(torch.cuda.current_stream(dev))
         with torch.cuda.stream(stream):
-            self._step(reorder=False)  # eager: per-device set-up and argument checks, outside capture
+            # Eager: per-device set-up and argument checks, outside capture.  The states are
+            # reordered with every beam keeping its own, which moves nothing.
+            self._step(reorder=False)
+            if states is not None:
+                own = torch.arange(hidden.shape[1], device=dev)
+                beam_reorder(states, own.repeat(hidden.shape[0], 1))
         torch.cuda.current_stream(dev).wait_stream(stream)
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph, stream=stream):
