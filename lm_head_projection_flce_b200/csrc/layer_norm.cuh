@@ -456,6 +456,13 @@ __device__ __forceinline__ void ln_ring_read(const uint8_t* slot, const void* ba
                                  v);
   }
 }
+// After a wait that ran out, by the thread that issues the copies: those still in flight
+// get time to land before the block can exit.
+__device__ __forceinline__ void ln_ring_settle() {
+  const uint64_t t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < 200000ull) {
+  }
+}
 // Two rows at a time: both sums of a reduction travel together.
 template <typename T, typename W, int VN, bool kExact>
 __global__ void __launch_bounds__(kLnMaxThreads, 1)
@@ -469,7 +476,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
   int loaded = 0;  // thread 0: rows issued so far, and the slot of the next
   LnRingPos put, get;
   auto issue = [&]() {
-    if (loaded >= count) return;
+    if (loaded >= count || put.slot < 0) return;
     const LnRingRow row =
         ln_ring_row<T>(a.x, a.ldx, a.n, a.h, int64_t(blockIdx.x) + int64_t(loaded++) * gridDim.x);
     const uint32_t bar = smem_u32(&full[put.slot]);
@@ -499,8 +506,12 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
   const float inv_h = 1.0f / float(h);
   int buf = 0;
   auto fetch = [&](int64_t r, float2 (&v)[8]) {
-    // A wait that ran out is recorded and the row's result lost; the loop ends as usual.
-    wait_phase(smem_u32(&full[get.slot]), get.parity, &ctl, g.err, g.timeout_ns);
+    // A wait that ran out is recorded and the row's result lost; nothing more is loaded,
+    // and the loop ends as usual.
+    const uint32_t bar = smem_u32(&full[get.slot]);
+    if (!mbar_try_wait(bar, get.parity) &&
+        !wait_phase(bar, get.parity, &ctl, g.err, g.timeout_ns) && t == 0)
+      put.slot = -1;  // tested where the slot is needed anyway: a flag of its own took 2% longer
     ln_ring_read<T, VN, kExact>(ring + uint32_t(get.slot) * g.slot_bytes, a.x, a.ldx, a.n, h, r, v);
     get.advance(g.slots);
   };
@@ -532,6 +543,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     finish(r, v0, ln_stats(m0, c.x, c.y, inv_h, a.eps));
     if (two) finish(r + gridDim.x, v1, ln_stats(m1, c.z, c.w, inv_h, a.eps));
   }
+  if (t == 0 && ctl.abort) ln_ring_settle();
 }
 
 // Rows too long for the registers of one block: three looks at the row, the
@@ -807,7 +819,8 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     const int64_t next = i + 1 < count ? r + gridDim.x : r;
     const float next_mean = a.mean[next], next_rstd = a.rstd[next];
     const uint8_t* at = ring + uint32_t(get.slot) * 2u * g.slot_bytes;
-    wait_phase(smem_u32(&full[get.slot]), get.parity, &ctl, g.err, g.timeout_ns);
+    if (!wait_phase(smem_u32(&full[get.slot]), get.parity, &ctl, g.err, g.timeout_ns))
+      loaded = count;  // as in the forward
     get.advance(g.slots);
     float2 xh[8], d[8];
     ln_ring_read<T, VN, kExact>(at, a.x, a.ldx, a.n, h, r, xh);
@@ -825,6 +838,7 @@ __global__ void __launch_bounds__(kLnMaxThreads, 1)
     mean = next_mean;
     rstd = next_rstd;
   }
+  if (t == 0 && ctl.abort) ln_ring_settle();
   if (a.part_w) ln_share_store<float, VN, kExact>(a.part_w + int64_t(blockIdx.x) * h, t, tpr, h, aw);
   if (a.part_b) ln_share_store<float, VN, kExact>(a.part_b + int64_t(blockIdx.x) * h, t, tpr, h, ab);
   ln_backward_far<T, W, VN, 1>(a, ln_sees_far(a, blockIdx.x, gridDim.x),
