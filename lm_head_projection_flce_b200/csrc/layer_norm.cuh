@@ -48,7 +48,7 @@ constexpr int kLnReduceWarps = 16;
 // N consecutive elements at a time, as floats.  The address is aligned to the
 // vector's size (16 bytes at most per access).
 template <typename T, int N>
-struct LnIo;
+struct LnIo;  // N: 1, 4 or 8
 template <int N>
 struct LnIo<__nv_bfloat16, N> {
   static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&x)[N]) {
@@ -66,10 +66,6 @@ struct LnIo<__nv_bfloat16, N> {
       x[1] = __uint_as_float(w.x & 0xffff0000u);
       x[2] = __uint_as_float(w.y << 16);
       x[3] = __uint_as_float(w.y & 0xffff0000u);
-    } else if constexpr (N == 2) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-      x[0] = __uint_as_float(w << 16);
-      x[1] = __uint_as_float(w & 0xffff0000u);
     } else {
       x[0] = __bfloat162float(*p);
     }
@@ -80,8 +76,6 @@ struct LnIo<__nv_bfloat16, N> {
                                                 pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     } else if constexpr (N == 4) {
       *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-    } else if constexpr (N == 2) {
-      *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x[0], x[1]);
     } else {
       *p = __float2bfloat16_rn(x[0]);
     }
@@ -99,10 +93,6 @@ struct LnIo<float, N> {
         x[i + 2] = w.z;
         x[i + 3] = w.w;
       }
-    } else if constexpr (N == 2) {
-      const float2 w = *reinterpret_cast<const float2*>(p);
-      x[0] = w.x;
-      x[1] = w.y;
     } else {
       x[0] = *p;
     }
@@ -112,8 +102,6 @@ struct LnIo<float, N> {
 #pragma unroll
       for (int i = 0; i < N; i += 4)
         *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-    } else if constexpr (N == 2) {
-      *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
     } else {
       *p = x[0];
     }

@@ -52,9 +52,8 @@ struct MxGemmArgs {
   const uint8_t* m_scales;
   const uint8_t* n_codes;
   const uint8_t* n_scales;
-  int tile_n;         // N rows per tile, a multiple of 16 (of 64 where there are several)
-  int64_t m_tiles, n_tiles;
-  int m_stream;       // the M side's codes are read once: they need not stay in L2
+  int tile_n;         // N rows per tile: all there are, rounded up, or kMxpN
+  int64_t m_tiles;    // of the pair kernel: tiles along its M side, the tokens
   int64_t tiles;
   int stages;
   float softcap, inv_softcap;
@@ -181,7 +180,8 @@ __host__ __device__ __forceinline__ uint32_t mxg_stage_bytes(int tile_n) {
   return uint32_t((kMxgM + tile_n) * kMxgKBytes + (1 + mxg_scale_tiles(tile_n)) * 2 * kMxTileBytes);
 }
 
-// kSft: scale tiles of 128 rows that a tile's N side touches (2 above 128 rows).
+// Tiles are 128 head rows x all tokens.
+// kSft: scale tiles of 128 rows on the N side (2 above 128 tokens).
 template <typename TO, int kSft>
 __global__ void __launch_bounds__(kMxgThreads, 1)
     mx_gemm_kernel(const MxGemmArgs g) {
@@ -205,12 +205,6 @@ __global__ void __launch_bounds__(kMxgThreads, 1)
   const uint32_t off_sfb = off_sfa + 2 * kMxTileBytes;
   const int64_t blocks = mx_blocks(g.h);
   const int num_kb = int(mx_ctiles(g.h));
-  const int64_t n_row_tiles = (g.rows_n + kMxTileRows - 1) / kMxTileRows;
-  // The token tiles of a head tile follow one another, and share it in L2.
-  auto coords = [&](int64_t t, int64_t& mt, int64_t& n0) {
-    mt = t / g.n_tiles;
-    n0 = (t - mt * g.n_tiles) * g.tile_n;
-  };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -242,30 +236,24 @@ __global__ void __launch_bounds__(kMxgThreads, 1)
   if (warp == 0) {
     // -------------------------------------------------- loads
     const bool leader = elect_one();
-    // A head read once is marked first to go, which spares the rest of L2 (64 ->
-    // 55 us at 8 tokens x 4096 x 128256).
-    const uint64_t pol_m = g.m_stream ? l2_policy_evict_first() : l2_policy_evict_normal();
-    const uint64_t pol_n = g.m_stream ? l2_policy_evict_last() : l2_policy_evict_normal();
+    // The head, read once, is marked first to go, which spares the rest of L2 (64 -> 55 us
+    // at 8 tokens x 4096 x 128256).
+    const uint64_t pol_m = l2_policy_evict_first(), pol_n = l2_policy_evict_last();
+    // The tokens' codes: up to 128 rows of one row tile, the rest from the next.
+    constexpr bool two = kSft == 2;
+    const uint32_t bytes0 = uint32_t(min(g.tile_n, kMxTileRows)) * kMxgKBytes;
+    const uint32_t bytes1 = uint32_t(g.tile_n) * kMxgKBytes - bytes0;
+    const uint32_t expect =
+        kMxCodeBytes + 4 * kMxTileBytes + bytes0 + (two ? bytes1 + 2 * kMxTileBytes : 0u);
     int st = 0;
     uint32_t ph = 0, base = smem_base, full = full_bar(0);
     bool ok = true;
     for (int64_t t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
-      int64_t mt, n0;
-      coords(t, mt, n0);
-      // The N side's rows: from row n0 % 128 of row tile bt, up to two row tiles.
-      const int64_t bt = n0 / kMxTileRows;
-      const bool two = kSft == 2 && bt + 1 < n_row_tiles;
-      const int r0 = int(n0 % kMxTileRows), first = min(g.tile_n, kMxTileRows - r0);
-      const uint32_t bytes0 = uint32_t(first) * kMxgKBytes;
-      const uint32_t bytes1 = uint32_t(g.tile_n - first) * kMxgKBytes;
-      const uint32_t expect = kMxCodeBytes + 4 * kMxTileBytes + bytes0 +
-                              (two ? bytes1 + 2 * kMxTileBytes : 0u);
-      const uint8_t* mc = g.m_codes + mt * num_kb * kMxCodeBytes;
-      const uint8_t* ms = g.m_scales + mt * num_kb * (2 * kMxTileBytes);
-      const uint8_t* nc = g.n_codes + bt * num_kb * kMxCodeBytes + r0 * kMxgKBytes;
-      const uint8_t* ns = g.n_scales + bt * num_kb * (2 * kMxTileBytes);
-      // ... and of the second row tile, from its first row
-      const uint8_t* nc1 = g.n_codes + (bt + 1) * num_kb * kMxCodeBytes;
+      const uint8_t* mc = g.m_codes + t * num_kb * kMxCodeBytes;
+      const uint8_t* ms = g.m_scales + t * num_kb * (2 * kMxTileBytes);
+      const uint8_t* nc = g.n_codes;
+      const uint8_t* ns = g.n_scales;
+      const uint8_t* nc1 = nc + num_kb * kMxCodeBytes;
       const uint8_t* ns1 = ns + num_kb * (2 * kMxTileBytes);
       int ahead = 0;
       if (t == blockIdx.x) {
@@ -343,9 +331,6 @@ __global__ void __launch_bounds__(kMxgThreads, 1)
     uint64_t da = da0, dsa = dsa0;
     bool ok = true;
     for (int64_t t = blockIdx.x; ok && t < g.tiles; t += gridDim.x) {
-      int64_t mt, n0;
-      coords(t, mt, n0);
-      const uint32_t shift = uint32_t(n0 % kMxTileRows) / 32u;  // first N row's scale column
       if (!wait_warp(tempty_bar(acc), acc_ph ^ 1u, ctl, g.err, g.timeout_ns)) {
         ok = false;
         break;
@@ -371,12 +356,11 @@ __global__ void __launch_bounds__(kMxgThreads, 1)
           tc_copy_scales_one(sfb + 4u * kSft, dsb + kTile);
           if (kSft == 2) tc_copy_scales_one(sfb + 4u * kSft + 4u, dsb + 3 * kTile);
           const uint64_t db = da + db_off;
-          const uint32_t sb = sfb + shift;
-          tc_mma_mxf4_one(d, da, db, idesc, sfa, sb, more);
-          if (left > 2) tc_mma_mxf4_one(d, da + 2, db + 2, idesc | kIdOdd, sfa, sb, 1u);
-          if (left > 4) tc_mma_mxf4_one(d, da + 4, db + 4, idesc, sfa + 4u, sb + 4u * kSft, 1u);
+          tc_mma_mxf4_one(d, da, db, idesc, sfa, sfb, more);
+          if (left > 2) tc_mma_mxf4_one(d, da + 2, db + 2, idesc | kIdOdd, sfa, sfb, 1u);
+          if (left > 4) tc_mma_mxf4_one(d, da + 4, db + 4, idesc, sfa + 4u, sfb + 4u * kSft, 1u);
           if (left > 6)
-            tc_mma_mxf4_one(d, da + 6, db + 6, idesc | kIdOdd, sfa + 4u, sb + 4u * kSft, 1u);
+            tc_mma_mxf4_one(d, da + 6, db + 6, idesc | kIdOdd, sfa + 4u, sfb + 4u * kSft, 1u);
           tc_commit_one(full + 8u * kMxgMaxStages);
         }
         __syncwarp();
@@ -411,15 +395,13 @@ __global__ void __launch_bounds__(kMxgThreads, 1)
     int acc = 0;
     uint32_t acc_ph = 0;
     const bool capped = g.softcap > 0.0f;
+    const int cols = int(g.rows_n);
     for (int64_t t = blockIdx.x; t < g.tiles; t += gridDim.x) {
-      int64_t mt, n0;
-      coords(t, mt, n0);
       if (!wait_warp(tfull_bar(acc), acc_ph, ctl, g.err, g.timeout_ns)) break;
       __syncwarp();
       tc_fence_after_sync();
-      const int64_t row = mt * kMxgM + quarter * 32 + lane;
+      const int64_t row = t * kMxgM + quarter * 32 + lane;
       const bool live = row < g.rows_m;
-      const int cols = int(min(int64_t(g.tile_n), g.rows_n - n0));
       const uint32_t taddr =
           tmem + (static_cast<uint32_t>(quarter * 32) << 16) + uint32_t(acc) * uint32_t(g.tile_n);
       for (int c0 = 32 * half; c0 < cols; c0 += 64) {
@@ -427,7 +409,7 @@ __global__ void __launch_bounds__(kMxgThreads, 1)
         tmem_load_32cols(taddr + c0, x);
         if (capped) mx_softcap(x, g.softcap, g.inv_softcap);
         if (!live) continue;  // what is above is for the whole warp
-        TO* out = static_cast<TO*>(g.out) + (n0 + c0) * g.ldo + row;
+        TO* out = static_cast<TO*>(g.out) + int64_t(c0) * g.ldo + row;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           const float one[1] = {x[j]};
@@ -934,12 +916,10 @@ extern "C" int flce_mxfp4_logits(const void* hidden, int dtype, int64_t n, int64
   g.n_codes = tokens_m ? wc : a_codes;
   g.n_scales = tokens_m ? wsc : a_scales;
   g.tile_n = int(std::min<int64_t>(cdiv(g.rows_n, 16) * 16, kMxgMaxN));
-  if (g.tile_n > 128) g.tile_n = kMxgMaxN;  // tiles start on a multiple of 64 rows
+  if (g.tile_n > 128) g.tile_n = kMxgMaxN;
   if (tokens_m) g.tile_n = kMxpN;
   g.m_tiles = cdiv(g.rows_m, tokens_m ? 2 * kMxgM : kMxgM);
-  g.n_tiles = cdiv(g.rows_n, g.tile_n);
-  g.m_stream = !tokens_m && g.n_tiles == 1;
-  g.tiles = g.m_tiles * g.n_tiles;
+  g.tiles = g.m_tiles * cdiv(g.rows_n, g.tile_n);  // one along the N side with few tokens
   const int sf_stages = (kTmemCols - 2 * g.tile_n) / (8 + 8 * mxg_scale_tiles(g.tile_n));
   g.stages = std::min({kMxgMaxStages, sf_stages, int(kMxgSmem / mxg_stage_bytes(g.tile_n))});
   g.softcap = softcap;
