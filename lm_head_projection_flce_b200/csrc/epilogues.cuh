@@ -90,6 +90,7 @@ struct EpiForward {
 #pragma unroll 1
     for (int c0 = 0; c0 < kBN; c0 += 32) {
       float v[32];
+      __syncwarp();
       tmem_load_32cols(taddr + c0, v);
       if (capped) {
         const float2 c2 = make_float2(p.softcap, p.softcap);
@@ -192,6 +193,7 @@ struct EpiGrad {
 #pragma unroll 1
     for (int c0 = 0; c0 < kBN; c0 += 32) {
       float v[32];
+      __syncwarp();
       tmem_load_32cols(taddr + c0, v);
       if (!capped) {
         // sc * 2^(z log2 e - lse log2 e), two columns per packed FMA / multiply
@@ -269,6 +271,7 @@ struct EpiStoreRows {
 #pragma unroll 1
     for (int c0 = 0; c0 < kBN; c0 += 32) {
       float v[32];
+      __syncwarp();
       tmem_load_32cols(taddr + c0, v);
       if (!live) continue;
       if (p.v8 && h0 + c0 + 32 <= p.cols) {  // all 32 columns in range
@@ -334,6 +337,7 @@ struct EpiAccumRows {
 #pragma unroll 1
     for (int c0 = 0; c0 < kBN; c0 += 32) {
       float v[32];
+      __syncwarp();
       tmem_load_32cols(taddr + c0, v);
       if (!live) continue;
 #pragma unroll

@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(kMxgThreads, 1)
           tmem + (static_cast<uint32_t>(quarter * 32) << 16) + uint32_t(acc) * uint32_t(g.tile_n);
       for (int c0 = 32 * half; c0 < cols; c0 += 64) {
         float x[32];
+        __syncwarp();  // lanes behind the last row store nothing and come here first
         tmem_load_32cols(taddr + c0, x);
         if (capped) mx_softcap(x, g.softcap, g.inv_softcap);
         if (!live) continue;  // what is above is for the whole warp

@@ -130,11 +130,9 @@ __device__ __forceinline__ void tc_fence_after_sync() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 // 32 consecutive FP32 columns of this thread's TMEM lane (warp w reads lanes
-// 32*(w%4) .. +31), waiting for the load before returning.  All lanes call it; those
-// that had less to store since the last one wait here for the others, as both
-// instructions want the warp together (.aligned).
+// 32*(w%4) .. +31), waiting for the load before returning.  Both instructions want the
+// warp together (.aligned): where lanes may part between two loads, __syncwarp() first.
 __device__ __forceinline__ void tmem_load_32cols(uint32_t taddr, float (&v)[32]) {
-  __syncwarp();
   uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
