@@ -130,8 +130,12 @@ __device__ __forceinline__ uint64_t mx_scale_desc(uint32_t addr) {
 
 // c tanh(z / c) of a thread's 32 values, to a few units in the last place of FP32.  With
 // x = z / c and |x| <= 5/8 it is z + z t(x^2), t the odd series' tail as a polynomial
-// of five terms fitted for the least largest relative error (4e-9), and no special
-// function; beyond, c - 2c / (exp(2 |x|) + 1) with z's sign.  A warp whose values are
+// of five terms (fitted here for a small largest relative error: 8.7e-9 with the
+// coefficients rounded to FP32, at x = 0.604), and no special function; beyond, c -
+// 2c / (exp(2 |x|) + 1) with z's sign.  The method, an odd polynomial near 0 and the
+// exponential form beyond it, is that of Cody and Waite's "Software Manual for the
+// Elementary Functions" (1980) and of Moshier's "Methods and Programs for
+// Mathematical Functions" (1989).  A warp whose values are
 // all small, as most logits of a cap are, skips the second: 1024 x 4096 x 65536 takes
 // 109 us then, as without a cap, and 129 us with large values (tanhf for every
 // value: 130 us either way).  One reciprocal for two values gained nothing.
